@@ -178,6 +178,9 @@ int device_sm_count() {
     return sms > 0 ? sms : 1;
 }
 
+trit_status abi_check_device() { return check_device(); }
+trit_status abi_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
 // ---- MLP blocks in two launches ----------------------------------------------------
 
 namespace {

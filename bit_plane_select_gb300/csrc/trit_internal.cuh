@@ -470,6 +470,15 @@ cudaError_t launch_bitcos_many(const BitcosDev *list, int count, cudaStream_t s)
 int bitcos_pack_host(const int8_t *w, int64_t N, int64_t K, uint64_t *bitmap, uint32_t *sign_off,
                      uint32_t *signs, int64_t *sign_words);
 
+// The decode step between the products.
+cudaError_t launch_kv_append(const trit_kv_append_job &J, uint32_t *err, cudaStream_t s);
+cudaError_t launch_draft_verify(const trit_verify_job &J, uint32_t *err, cudaStream_t s);
+
 int device_sm_count();
+
+// Shared by the extern "C" files: the device check (TRIT_OK on sm_103) and the
+// record of a failed CUDA call (returns TRIT_E_CUDA).
+trit_status abi_check_device();
+trit_status abi_cuda_fail(cudaError_t e);
 
 }  // namespace trit

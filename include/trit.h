@@ -84,6 +84,8 @@ typedef enum trit_status {
 #define TRIT_ERR_NOT_TERNARY 4u   /* trit_pack saw a value outside {-1, 0, +1} */
 #define TRIT_ERR_NONFINITE 8u     /* trit_quant_act saw a NaN or infinity */
 #define TRIT_ERR_TIMEOUT 16u      /* a bounded wait inside a kernel gave up */
+#define TRIT_ERR_INDEX 32u        /* a page id, position, length or token outside its range */
+#define TRIT_ERR_EMPTY 64u        /* trit_draft_verify: no token has a positive probability */
 
 /* Most list entries one launch of the *_many calls accepts; longer lists are
  * split into consecutive launches on the same stream. */
@@ -556,6 +558,135 @@ typedef struct trit_bitcos_proj {
  * trit_gemm_many (K <= TRIT_BITCOS_MAX_K). */
 TRIT_API trit_status trit_bitcos_gemv_many(const trit_bitcos_proj *list, int32_t count,
                                            trit_stream_t stream);
+
+/*
+ * ---- the decode step between the products ---------------------------------------
+ * A token's q, k and v products are rotated and appended to a paged cache
+ * (trit_kv_append), its queries attend to the cache (trit_attn_paged), whose
+ * fp32 or 16-bit output is the o projection's input, and drafted tokens are
+ * verified against the target's probabilities (trit_draft_verify).  The three
+ * share the cache and batch descriptors below.
+ */
+#define TRIT_F32 0
+#define TRIT_BF16 1
+#define TRIT_F16 2
+
+/* One layer's paged cache.  Element (page, head, slot, d) of both k and v is at
+ * page * page_stride + head * head_stride + slot * slot_stride + d, strides in
+ * elements, so [pages][heads][page_size][D] and [pages][page_size][heads][D]
+ * are both described.  Pointers 16-byte aligned, strides multiples of 8. */
+typedef struct trit_kv_cache {
+    void *k, *v;
+    int64_t page_stride, head_stride, slot_stride;
+    int32_t pages, heads;        /* pages in the cache; key heads */
+    int32_t page_size;           /* keys in a page: any number >= 1 */
+    int32_t head_dim;            /* D: 64 or 128 */
+    int32_t dtype;               /* TRIT_BF16 or TRIT_F16 */
+    int32_t reserved;            /* must be 0 */
+} trit_kv_cache;
+
+/*
+ * B sequences of at most T new tokens each.  Key p of the shared prefix
+ * (p < prefix_len) is slot p % page_size of page prefix_table[p / page_size];
+ * own key i of sequence b (i < lens[b]) is slot i % page_size of page
+ * table[b * table_stride + i / page_size].  lens counts the new tokens too: of
+ * n = new_lens[b] (T where new_lens is NULL), token t < n is own key
+ * i = lens[b] - n + t at position prefix_len + i, and sees the whole prefix
+ * and own keys 0..i.  Tokens t >= n are padding.  Tables, lens and new_lens are
+ * read by the kernels when they run; prefix_len is fixed by the call.
+ */
+typedef struct trit_kv_batch {
+    const int32_t *prefix_table;  /* [prefix_pages]; may be NULL when prefix_len = 0 */
+    const int32_t *table;         /* [B][table_stride] */
+    const int32_t *lens;          /* [B] */
+    const int32_t *new_lens;      /* [B], or NULL */
+    int64_t prefix_len;
+    int64_t table_stride;         /* >= table_pages */
+    int32_t prefix_pages, table_pages;
+    int32_t B, T;                 /* B <= TRIT_MAX_SEQUENCES */
+} trit_kv_batch;
+#define TRIT_MAX_SEQUENCES 4096
+
+/*
+ * trit_kv_append -- the new tokens' keys and values into their cache slots, and
+ * their queries into q_out, in one launch: per head vector x of q and k, with a
+ * gain g the norm x <- x / sqrt(mean(x^2) + eps) * g (skipped where the gain is
+ * NULL), then the rotation of the first `rot` columns by the token's position,
+ *     (a, b) <- (a cos - b sin, b cos + a sin),
+ * where (a, b) are columns (j, j + rot/2) and the angle is column j of the
+ * tables, or columns (2j, 2j + 1) with TRIT_ROPE_PAIRS; v is copied.  All in
+ * fp32, rounded once to the cache's type.  Padding tokens' q_out rows are 0 and
+ * nothing of them is appended.  A token whose own index is negative, whose
+ * table column or page id is outside its range or whose position has no row in
+ * the tables sets TRIT_ERR_INDEX and is treated as padding.
+ *   q, k, v   token (b, t) at (b*T + t) * stride: Hq, heads, heads vectors of D;
+ *             src_dtype TRIT_F32 or the cache's.  q may be NULL (then q_out too)
+ *   q_out     [B][T][Hq][D], the cache's type
+ *   cos, sin  [max_pos][rot/2] fp32; may be NULL when rot = 0
+ * Pointers 16-byte aligned, token strides multiples of 16 bytes, rot a multiple
+ * of 8 with rot <= D.  Asynchronous on `stream`.
+ */
+#define TRIT_ROPE_PAIRS 1u
+typedef struct trit_kv_append_job {
+    trit_kv_cache cache;
+    trit_kv_batch batch;
+    const void *q, *k, *v;
+    void *q_out;
+    const float *cos, *sin;
+    const float *q_gain, *k_gain;       /* [D] fp32, or NULL: no norm */
+    int64_t q_stride, k_stride, v_stride;   /* elements between tokens */
+    int64_t max_pos;
+    float eps;
+    int32_t q_heads, rot, src_dtype;
+    uint32_t flags;                     /* 0 or TRIT_ROPE_PAIRS */
+    int32_t reserved;                   /* must be 0 */
+} trit_kv_append_job;
+TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err_flag,
+                                    trit_stream_t stream);
+
+/*
+ * trit_draft_verify -- which drafted tokens the target keeps, and the token that
+ * follows them.  Draft t of sequence b, x = draft[b][t], is kept while
+ *     u[b][t] * q[b][t][x] < p[b][t][x]      (one fp32 product),
+ * which happens with probability min(1, p/q) for u uniform in [0, 1).  At the
+ * first draft k not kept the next token is drawn from r = max(p[k] - q[k], 0)
+ * (from p[k] where r is nowhere positive); when all n = n_draft[b] are kept,
+ * from r = p[n].  The draw is a race of given exponential numbers:
+ *     next = argmax_i r[i] / race[b][i]      (fp32 difference and quotient),
+ * over the i with r[i] > 0 and a quotient that is not negative or NaN, the
+ * lowest i winning a tie: token i has probability r[i] / sum r when the race
+ * numbers are independent and Exp(1), and no sum over the vocabulary enters, so
+ * the answer does not depend on any order of summation.
+ *   p  [B][T+1][V], q [B][T][V] by strides; dtype TRIT_F32, TRIT_BF16 or TRIT_F16
+ *   draft [B][T] int32, n_draft [B] int32 or NULL (T), u [B][T] fp32, race [B][V] fp32
+ *   tokens   [B][T+1] int32 out: the kept drafts, the next token, then -1
+ *   accepted [B] int32 out: how many were kept
+ *   workspace  trit_verify_workspace_bytes(B) bytes, 8-byte aligned, zeroed once
+ *        before its first use; every call leaves it zeroed.
+ * A draft outside [0, V) is not kept and an n_draft outside [0, T] is clamped,
+ * both with TRIT_ERR_INDEX; a sequence without any candidate gets the token -1
+ * and TRIT_ERR_EMPTY.
+ */
+typedef struct trit_verify_job {
+    const void *p, *q;
+    const int32_t *draft;
+    const int32_t *n_draft;
+    const float *u;
+    const float *race;
+    int32_t *tokens;
+    int32_t *accepted;
+    void *workspace;
+    int64_t p_seq_stride, p_tok_stride;   /* elements */
+    int64_t q_seq_stride, q_tok_stride;
+    int64_t race_stride;                  /* elements between sequences */
+    int64_t V;
+    int32_t B, T;
+    int32_t dtype;
+    uint32_t flags;                       /* must be 0 */
+} trit_verify_job;
+TRIT_API int64_t trit_verify_workspace_bytes(int64_t B);
+TRIT_API trit_status trit_draft_verify(const trit_verify_job *job, uint32_t *err_flag,
+                                       trit_stream_t stream);
 
 #ifdef __cplusplus
 }
