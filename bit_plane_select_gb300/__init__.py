@@ -11,7 +11,7 @@ Functions carry the C names:
   trit_pack, trit_unpack, trit_verify, trit_quant_act, trit_quant_act_many,
   trit_gemv, trit_gemm, trit_gemm_many, trit_quant_gemv_many, trit_gemm_noalloc,
   trit_quant_act_folded, trit_intmlp_quant, trit_intmlp_gemv_many, trit_check_div127,
-  trit_read_probe, trit_kv_append, trit_draft_verify
+  trit_read_probe, trit_kv_append, trit_attn_paged, trit_draft_verify
 """
 from __future__ import annotations
 
@@ -146,6 +146,9 @@ def lib():
         L.trit_bitcos_pack.argtypes = [p, i64, i64, p, p, p, p]
         L.trit_bitcos_gemv_many.argtypes = [p, i32, p]
         L.trit_kv_append.argtypes = [p, p, p]
+        L.trit_attn_workspace_bytes.restype = i64
+        L.trit_attn_workspace_bytes.argtypes = [p]
+        L.trit_attn_paged.argtypes = [p, p, p]
         L.trit_verify_workspace_bytes.restype = i64
         L.trit_verify_workspace_bytes.argtypes = [i64]
         L.trit_draft_verify.argtypes = [p, p, p]
@@ -155,7 +158,7 @@ def lib():
                      "trit_intmlp_quant", "trit_check_div127", "trit_read_probe",
                      "trit_intmlp_gemv_many", "trit_bitcos_pack", "trit_bitcos_gemv_many",
                      "trit_issue_probe", "trit_mlp_gate_up", "trit_mlp_down", "trit_kv_append",
-                     "trit_draft_verify"):
+                     "trit_attn_paged", "trit_draft_verify"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib

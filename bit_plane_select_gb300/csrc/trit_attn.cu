@@ -1,0 +1,600 @@
+// trit_attn_paged: out = softmax(scale q K^T) V over a paged cache, the shared
+// prefix read once for the batch.
+//
+// The keys of every item (trit_attn.cuh) are cut into steps of 64, all steps of
+// the call are laid end to end, and each of a fixed grid of CTAs takes an equal
+// run of them, whatever the lengths (which only the device knows): a CTA's run
+// may end one item, cover several and begin another.  Items a CTA does not
+// finish alone leave partial results that a second launch joins.
+//
+// Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
+// reading K and V: 4 D bytes a key against 4 D R flops.  A step's 64 keys go 16
+// to a warp; every warp has its own ring of three stages of 16 keys (K and V),
+// filled by 16-byte asynchronous copies two stages ahead, so warps never wait
+// for one another inside an item.  S = Q K^T and O += P V are 16-bit
+// mma.sync with fp32 sums (the rows fill one or two m16 tiles); the rows' m and
+// l live in registers and O is only rescaled when a maximum moved.
+// P is rounded to the cache's 16-bit type for the second product: relative
+// 2^-9 (bf16) or 2^-12 (fp16) of each term on average, the size of the output's own rounding.
+#include "trit_attn.cuh"
+#include "trit_tc.cuh"
+
+namespace trit {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kKeys = kStep / kWarps;   // keys of a warp's stage: 16
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int clamped_len(const Args &A, int b, bool report) {
+    const int cap = A.J.batch.table_pages * A.J.cache.page_size;
+    const int n = A.J.batch.lens[b];
+    if (n >= 0 && n <= cap) return n;
+    if (report) raise_flag(A.err, TRIT_ERR_INDEX);
+    return n < 0 ? 0 : cap;
+}
+
+// Where a step of the work lies.
+struct Place {
+    int b;         // -1: the prefix
+    int h, tile;   // key head, row tile
+    int step;      // step of the item's keys
+    int steps;     // steps of the item
+};
+
+__device__ __forceinline__ Place place_of(const Args &A, const int32_t *cum, int64_t u) {
+    Place p;
+    const int64_t pre = int64_t(A.J.cache.heads) * A.pre_tiles * A.pre_steps;
+    if (u < pre) {
+        const int64_t item = u / A.pre_steps;
+        p.b = -1;
+        p.step = int(u - item * A.pre_steps);
+        p.steps = A.pre_steps;
+        p.h = int(item / A.pre_tiles);
+        p.tile = int(item - int64_t(p.h) * A.pre_tiles);
+        return p;
+    }
+    const int64_t v = u - pre;
+    const int items = A.J.cache.heads * A.own_tiles;
+    const int at = int(v / items);            // in steps of one item: cum[b] <= at < cum[b + 1]
+    int lo = 0, hi = A.J.batch.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    p.b = lo;
+    p.steps = cum[lo + 1] - cum[lo];
+    const int64_t rest = v - int64_t(cum[lo]) * items;
+    const int item = int(rest / p.steps);
+    p.step = int(rest - int64_t(item) * p.steps);
+    p.h = item / A.own_tiles;
+    p.tile = item - p.h * A.own_tiles;
+    return p;
+}
+
+// The keys of a place: their page table and how many there are.
+struct Keys {
+    const int32_t *table;
+    int n;
+};
+__device__ __forceinline__ Keys keys_of(const Args &A, const Place &p) {
+    Keys k;
+    if (p.b < 0) {
+        k.table = A.J.batch.prefix_table;
+        k.n = int(A.J.batch.prefix_len);
+    } else {
+        k.table = A.J.batch.table + p.b * A.J.batch.table_stride;
+        k.n = clamped_len(A, p.b, false);
+    }
+    return k;
+}
+
+// A warp's stage of 16 keys: K then V, rows of D 16-bit values whose 16-byte
+// chunk c lies at c ^ (row & 7), so that the eight rows of an ldmatrix fall on
+// different banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+    return uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
+}
+
+template <int D>
+struct Loader {
+    // Issues the copies of keys [key0, key0 + 16) of head h; rows past the end,
+    // and rows of pages outside the cache, are filled with zeros.
+    static __device__ __forceinline__ void issue(const Args &A, const Keys &K, int h, int key0, uint8_t *stage,
+                                                 int lane) {
+        constexpr int CH = D / 8;            // chunks of a row
+        constexpr int RI = 32 / CH;          // rows of one copy instruction
+        const trit_kv_cache &C = A.J.cache;
+        const int c = lane % CH, r0 = lane / CH;
+        const uint16_t *kb = static_cast<const uint16_t *>(C.k) + h * C.head_stride + c * 8;
+        const uint16_t *vb = static_cast<const uint16_t *>(C.v) + h * C.head_stride + c * 8;
+        int64_t at = 0;
+        bool one_page = (C.page_size & 15) == 0, good = false;
+        if (one_page && key0 < K.n) {
+            const int col = A.page_shift >= 0 ? key0 >> A.page_shift : key0 / C.page_size;
+            const int page = __ldg(K.table + col);
+            good = page >= 0 && page < C.pages;
+            if (!good) raise_flag(A.err, TRIT_ERR_INDEX);
+            at = page * C.page_stride + int64_t(key0 - col * C.page_size) * C.slot_stride;
+        }
+#pragma unroll
+        for (int j = 0; j < kKeys / RI; ++j) {
+            const int r = r0 + j * RI, key = key0 + r;
+            int64_t off = at + r * C.slot_stride;
+            bool ok = good && key < K.n;
+            if (!one_page && key < K.n) {
+                const int col = key / C.page_size;
+                const int page = __ldg(K.table + col);
+                ok = page >= 0 && page < C.pages;
+                if (!ok) raise_flag(A.err, TRIT_ERR_INDEX);
+                off = page * C.page_stride + int64_t(key - col * C.page_size) * C.slot_stride;
+            }
+            if (!ok) off = 0;
+            tc::cp_async16(stage + chunk_at<D>(r, c), kb + off, ok ? 16u : 0u);
+            tc::cp_async16(stage + kKeys * D * 2 + chunk_at<D>(r, c), vb + off, ok ? 16u : 0u);
+        }
+    }
+};
+
+// Exclusive prefix sums of the sequences' steps into cum[0..B] (shared memory).
+__device__ __forceinline__ void count_steps(const Args &A, int32_t *cum, int32_t *scratch, bool report) {
+    const int B = A.J.batch.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (B + kThreads - 1) / kThreads, from = tid * per;
+    int sum = 0;
+    for (int i = 0; i < per; ++i)
+        if (from + i < B) sum += (clamped_len(A, from + i, report) + kStep - 1) / kStep;
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += scratch[w];
+    for (int i = 0; i < per; ++i)
+        if (from + i < B) {
+            cum[from + i] = before;
+            before += (clamped_len(A, from + i, false) + kStep - 1) / kStep;
+            if (from + i == B - 1) cum[B] = before;
+        }
+    __syncthreads();
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_kernel(const __grid_constant__ Args A) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int RT = 16 * MT;
+    constexpr int kStageBytes = 2 * kKeys * D * 2;
+    static_assert(kStageBytes == 16 * D * 4, "a stage holds one m16 tile of fp32 sums");
+    const trit_attn_job &J = A.J;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = smem + warp * kStages * kStageBytes;
+    float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);   // [kWarps][RT] (m, l)
+    int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
+    int32_t *cum = scratch + kWarps;
+
+    pdl_launch();
+    count_steps(A, cum, scratch, blockIdx.x == 0);
+    const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
+    const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
+    const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
+    const int64_t lo = W * blockIdx.x / gridDim.x, hi = W * (blockIdx.x + 1) / gridDim.x;
+    if (lo >= hi) return;
+
+    // the ring runs ahead of the products, across items
+    int64_t lu = lo;
+    Place lp = place_of(A, cum, lo);
+    Keys lk = keys_of(A, lp);
+    auto load_next = [&](int stage) {
+        if (lu < hi) {
+            Loader<D>::issue(A, lk, lp.h, lp.step * kStep + warp * kKeys, ring + stage * kStageBytes, lane);
+            if (++lu < hi) {
+                if (++lp.step == lp.steps) {
+                    lp = place_of(A, cum, lu);
+                    lk = keys_of(A, lp);
+                }
+            }
+        }
+        tc::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < kStages; ++s) load_next(s);
+
+    uint32_t qf[MT][D / 16][4];
+    float o[MT][D / 8][4];
+    float m[MT][2], l[MT][2];
+    int lim[MT][2];
+    Place p = lp;
+    int nkeys = 0, mts = 1, first_step = 0;
+    int64_t u = lo;
+    bool fresh = true;
+    int stage = 0;
+    while (u < hi) {
+        if (fresh) {
+            fresh = false;
+            p = place_of(A, cum, u);
+            first_step = p.step;
+            nkeys = keys_of(A, p).n;
+            const int rows = p.b < 0 ? B * A.R : A.R;
+            mts = MT == 1 || rows - p.tile * RT <= 16 ? 1 : 2;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = p.tile * RT + mt * 16 + i * 8 + (lane >> 2);
+                    int b = p.b, r = row;
+                    if (p.b < 0) {
+                        b = row / A.R;
+                        r = row - b * A.R;
+                    }
+                    const int t = r / G, g = r - t * G;
+                    bool ok = row < rows;
+                    int n = 0;
+                    if (ok) {
+                        n = batch_new(J.batch, b);
+                        ok = t < n;
+                    }
+                    lim[mt][i] = 0;
+                    if (ok) {
+                        lim[mt][i] = nkeys;
+                        if (p.b >= 0) {
+                            const int see = nkeys - n + t + 1;
+                            lim[mt][i] = see < 0 ? 0 : see;
+                        }
+                    }
+                    m[mt][i] = -INFINITY;
+                    l[mt][i] = 0.0f;
+                    const T *q = static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride +
+                                 (int64_t(p.h) * G + g) * D + 2 * (lane & 3);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        qf[mt][ks][i] = ok ? __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16)) : 0u;
+                        qf[mt][ks][2 + i] = ok ? __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 8)) : 0u;
+                    }
+                }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) o[mt][d][0] = o[mt][d][1] = o[mt][d][2] = o[mt][d][3] = 0.0f;
+        }
+
+        tc::cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const int key0 = p.step * kStep + warp * kKeys;
+        uint8_t *st = ring + stage * kStageBytes;
+        if (key0 < nkeys) {
+            const uint32_t kaddr = tc::smem_u32(st), vaddr = kaddr + kKeys * D * 2;
+            float s[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
+            const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t kf[4];
+                ldsm4(kf, kaddr + chunk_at<D>(krow, 2 * ks + kch));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (mt < mts) {
+                        mma16816<T>(s[mt][0], qf[mt][ks], kf[0], kf[1]);
+                        mma16816<T>(s[mt][1], qf[mt][ks], kf[2], kf[3]);
+                    }
+            }
+            uint32_t pf[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                if (mt < mts) {
+                    float alpha[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = key0 + n * 8 + 2 * (lane & 3) + e;
+                                float &v = s[mt][n][2 * i + e];
+                                v = key < lim[mt][i] ? v * A.scale2 : -INFINITY;
+                                mx = fmaxf(mx, v);
+                            }
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                        const float top = fmaxf(m[mt][i], mx), base = base_of(top);
+                        alpha[i] = ex2(m[mt][i] - base);
+                        m[mt][i] = top;
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float e0 = ex2(s[mt][n][2 * i] - base), e1 = ex2(s[mt][n][2 * i + 1] - base);
+                            sum += e0 + e1;
+                            pf[mt][2 * n + i] = pack16<T>(e0, e1);
+                        }
+                        l[mt][i] = l[mt][i] * alpha[i] + sum;
+                    }
+                    if (__any_sync(~0u, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+                        for (int d = 0; d < D / 8; ++d) {
+                            o[mt][d][0] *= alpha[0];
+                            o[mt][d][1] *= alpha[0];
+                            o[mt][d][2] *= alpha[1];
+                            o[mt][d][3] *= alpha[1];
+                        }
+                    }
+                }
+            const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
+#pragma unroll
+            for (int dn = 0; dn < D / 16; ++dn) {
+                uint32_t vf[4];
+                ldsm4t(vf, vaddr + chunk_at<D>(vrow, 2 * dn + vch));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    if (mt < mts) {
+                        mma16816<T>(o[mt][2 * dn], pf[mt], vf[0], vf[1]);
+                        mma16816<T>(o[mt][2 * dn + 1], pf[mt], vf[2], vf[3]);
+                    }
+            }
+        }
+        __syncwarp();   // every lane has read the stage
+
+        if (p.step + 1 == p.steps || u + 1 == hi) {
+            // the item's run in this CTA ends: join the four warps through their free stages
+            const bool starts = first_step == 0, ends = p.step + 1 == p.steps;
+            const bool whole = starts && ends;
+            const bool direct = whole && p.b >= 0 && J.batch.prefix_len == 0;
+            const int64_t slot = whole ? (p.b < 0 ? slot_prefix(A, p.h, p.tile) : slot_own(A, p.b, p.h, p.tile))
+                                       : 2 * int64_t(blockIdx.x) + (starts ? 1 : 0);
+            float *part = A.parts + slot * part_floats(RT, D);
+            const int rows = p.b < 0 ? B * A.R : A.R;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (mt >= mts) break;
+                float *mine = reinterpret_cast<float *>(st);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = i * 8 + (lane >> 2);
+                    float sum = l[mt][i];
+                    sum += __shfl_xor_sync(~0u, sum, 1);
+                    sum += __shfl_xor_sync(~0u, sum, 2);
+                    if ((lane & 3) == 0) {
+                        stats[(warp * RT + mt * 16 + r) * 2] = m[mt][i];
+                        stats[(warp * RT + mt * 16 + r) * 2 + 1] = sum;
+                    }
+#pragma unroll
+                    for (int d = 0; d < D / 8; ++d)
+                        *reinterpret_cast<float2 *>(mine + r * D + ((d * 8 + 2 * (lane & 3)) ^ ((r & 7) << 3))) =
+                            make_float2(o[mt][d][2 * i], o[mt][d][2 * i + 1]);
+                }
+                __syncthreads();
+                constexpr int LR = D / 4, RW = 32 / LR;   // lanes of a row, rows of a warp pass
+                const float *all = reinterpret_cast<const float *>(smem + stage * kStageBytes);
+                for (int r = warp * RW + lane / LR; r < 16; r += kWarps * RW) {
+                    const int row = p.tile * RT + mt * 16 + r;
+                    if (row >= rows) break;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * RT + mt * 16 + r) * 2]);
+                    const float base = base_of(top);
+                    const int c = (lane % LR) * 4, cs = c ^ ((r & 7) << 3);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = ex2(stats[(w * RT + mt * 16 + r) * 2] - base);
+                        const float4 x = *reinterpret_cast<const float4 *>(
+                            all + w * kStages * (kStageBytes / 4) + r * D + cs);
+                        v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+                        sum += f * stats[(w * RT + mt * 16 + r) * 2 + 1];
+                    }
+                    if (direct) {
+                        const int t = row / G, g = row - t * G;
+                        const int64_t at = (int64_t(p.b) * J.batch.T + t) * J.q_heads + int64_t(p.h) * G + g;
+                        const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+                        store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                        if (J.lse && lane % LR == 0) J.lse[at] = lse_of(top, sum);
+                    } else {
+                        *reinterpret_cast<float4 *>(part + (mt * 16 + r) * D + c) = v;
+                        if (lane % LR == 0)
+                            *reinterpret_cast<float2 *>(part + RT * D + (mt * 16 + r) * 2) = make_float2(top, sum);
+                    }
+                }
+                __syncthreads();
+            }
+            fresh = true;
+        }
+        load_next(stage);
+        if (++stage == kStages) stage = 0;
+        ++p.step;
+        ++u;
+    }
+    tc::cp_async_wait<0>();
+}
+
+// One warp per output row that no CTA finished: joins its partial results.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A) {
+    pdl_wait();
+    const trit_attn_job &J = A.J;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int Hkv = J.cache.heads, G = A.G, B = J.batch.B, T_ = J.batch.T;
+    if (row >= int64_t(B) * T_ * J.q_heads) return;
+    const int hq = int(row % J.q_heads), h = hq / G;
+    const int64_t tok = row / J.q_heads;
+    const int b = int(tok / T_), t = int(tok - int64_t(b) * T_);
+    const int r = t * G + hq - h * G;
+    const int RT = A.RT;
+
+    // the own item's parts, then the prefix item's: slots and the row in them
+    const int c0 = A.cum[b], n = A.cum[b + 1] - c0;
+    const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
+    const int64_t W = pre + int64_t(A.cum[B]) * Hkv * A.own_tiles;
+    const int tile = r / RT, rl = r - tile * RT;
+    int64_t of = 0, ol = -1;
+    if (n > 0) {
+        const int64_t s0 = pre + (int64_t(c0) * Hkv * A.own_tiles) + (int64_t(h) * A.own_tiles + tile) * n;
+        of = cta_of(s0, W, A.grid);
+        ol = cta_of(s0 + n - 1, W, A.grid);
+        if (of == ol && J.batch.prefix_len == 0) return;   // written directly
+    }
+    const int own = int(ol - of + 1);
+    int64_t pf = 0, pl = -1;
+    const int64_t fr = int64_t(b) * A.R + r;
+    const int ptile = int(fr / RT), prl = int(fr - int64_t(ptile) * RT);
+    if (A.pre_tiles) {
+        const int64_t s0 = (int64_t(h) * A.pre_tiles + ptile) * A.pre_steps;
+        pf = cta_of(s0, W, A.grid);
+        pl = cta_of(s0 + A.pre_steps - 1, W, A.grid);
+    }
+    const int prefix = int(pl - pf + 1), total = own + prefix;
+    auto part = [&](int i, int &at) -> const float * {
+        int64_t slot;
+        if (i < own) {
+            at = rl;
+            slot = own == 1 ? slot_own(A, b, h, tile) : 2 * (of + i) + (i == 0 ? 1 : 0);
+        } else {
+            at = prl;
+            i -= own;
+            slot = prefix == 1 ? slot_prefix(A, h, ptile) : 2 * (pf + i) + (i == 0 ? 1 : 0);
+        }
+        return A.parts + slot * part_floats(RT, D);
+    };
+    float m = -INFINITY;
+    for (int i = lane; i < total; i += 32) {
+        int at;
+        const float *p = part(i, at);
+        m = fmaxf(m, p[RT * D + 2 * at]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float base = base_of(m);
+    constexpr int V = D / 32;    // columns of a lane
+    float v[V], l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < total; ++i) {
+        int at;
+        const float *p = part(i, at);
+        const float2 ml = *reinterpret_cast<const float2 *>(p + RT * D + 2 * at);
+        const float f = ex2(ml.x - base);
+        l += f * ml.y;
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] += f * p[at * D + k * 32 + lane];
+    }
+    const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int64_t at = row * D + k * 32 + lane;
+        if (J.out_dtype == TRIT_F32) static_cast<float *>(J.out)[at] = v[k] * inv;
+        else static_cast<T *>(J.out)[at] = static_cast<T>(v[k] * inv);
+    }
+    if (J.lse && lane == 0) J.lse[row] = lse_of(m, l);
+}
+
+// The work's layout from the job's sizes; the grid that a call would use.
+Args layout(const trit_attn_job &J, int sms) {
+    Args A = {};
+    A.J = J;
+    A.G = J.q_heads / J.cache.heads;
+    A.R = J.batch.T * A.G;
+    const int64_t pre_rows = J.batch.prefix_len > 0 ? int64_t(J.batch.B) * A.R : 0;
+    A.RT = A.R > 16 || pre_rows > 16 ? 32 : 16;
+    A.own_tiles = (A.R + A.RT - 1) / A.RT;
+    A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
+    A.pre_steps = int((J.batch.prefix_len + kStep - 1) / kStep);
+    A.page_shift = -1;
+    for (int s = 0; s < 31; ++s)
+        if (J.cache.page_size == (1 << s)) A.page_shift = s;
+    const int64_t cap = (int64_t(J.batch.table_pages) * J.cache.page_size + kStep - 1) / kStep;
+    const int64_t most = int64_t(J.cache.heads) * (int64_t(A.pre_tiles) * A.pre_steps +
+                                                   int64_t(J.batch.B) * A.own_tiles * cap);
+    const int64_t grid = int64_t(sms) * (J.cache.head_dim == 64 && A.RT == 16 ? 4 : 2);
+    A.grid = int(most < grid ? most : grid);
+    return A;
+}
+
+int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
+
+int64_t bytes_of(const Args &A) {
+    const int64_t slots = slot_prefix(A, 0, 0) + int64_t(A.J.cache.heads) * A.pre_tiles;
+    return cum_bytes(A.J) + slots * part_floats(A.RT, A.J.cache.head_dim) * 4;
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch(const Args &A, cudaStream_t s) {
+    const size_t smem = size_t(kWarps) * kStages * (2 * kKeys * D * 2) + kWarps * 16 * MT * 8 + kWarps * 4 +
+                        (size_t(A.J.batch.B) + 1) * 4;
+    static bool set = false;
+    if (!set) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   128 * 1024);
+        if (e != cudaSuccess) return e;
+        set = true;
+    }
+    attn_kernel<T, D, MT><<<A.grid, kThreads, smem, s>>>(A);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t rows = int64_t(A.J.batch.B) * A.J.batch.T * A.J.q_heads;
+    return launch_pdl(join_kernel<T, D>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, s, A);
+}
+
+template <typename T>
+cudaError_t launch_t(const Args &A, cudaStream_t s) {
+    if (A.J.cache.head_dim == 128) return A.RT == 16 ? launch<T, 128, 1>(A, s) : launch<T, 128, 2>(A, s);
+    return A.RT == 16 ? launch<T, 64, 1>(A, s) : launch<T, 64, 2>(A, s);
+}
+
+}  // namespace
+}  // namespace attn
+
+int64_t attn_workspace_bytes(const trit_attn_job &J) { return attn::bytes_of(attn::layout(J, 152)); }
+
+cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_t s) {
+    attn::Args A = attn::layout(J, 152);
+    A.err = err;
+    A.scale2 = J.scale * 1.4426950408889634f;
+    A.cum = static_cast<int32_t *>(J.workspace);
+    A.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(J.workspace) + attn::cum_bytes(J));
+    return J.cache.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A, s) : attn::launch_t<__half>(A, s);
+}
+
+}  // namespace trit

@@ -1,0 +1,79 @@
+// Attention over a paged cache: what its kernels share -- the work's layout,
+// the partial results and how they are joined.
+//
+// A query row's softmax over keys split in parts needs of each part only
+//     m = max_j s_j,  l = sum_j 2^(s_j - m),  o = sum_j 2^(s_j - m) v_j
+// (s = scale log2(e) q.k): parts a and b join as m = max(m_a, m_b),
+// l = l_a 2^(m_a - m) + l_b 2^(m_b - m), o likewise; out = o / l and
+// lse = m ln 2 + ln l at the end.  All of it is fp32.
+#pragma once
+
+#include "trit_serve.cuh"
+
+namespace trit {
+namespace attn {
+
+constexpr int kStep = 64;          // keys of one step of a CTA
+
+// Rows: row r = t*G + g of a (sequence, key head) pair is token t and query
+// head h*G + g; a prefix row is the sequence's index times R plus r.  An item
+// is a tile of RT rows of one key head against either one sequence's own keys
+// ("own", (b, h, tile)) or the shared prefix ("prefix", (h, tile)).
+struct Args {
+    trit_attn_job J;
+    uint32_t *err;
+    float scale2;            // scale * log2(e)
+    int32_t G, R;            // query heads per key head; rows per (sequence, key head)
+    int32_t RT;              // rows of an item
+    int32_t own_tiles;       // row tiles per (sequence, key head)
+    int32_t pre_tiles;       // row tiles of the prefix, per key head (0: no prefix item)
+    int32_t pre_steps;       // steps of the prefix
+    int32_t grid;            // CTAs the work is cut over
+    int32_t page_shift;      // log2(page_size), or -1
+    int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
+    float *parts;            // workspace: the partial results
+};
+
+// A partial result: RT x D sums, then RT pairs (m, l).
+__host__ __device__ inline int64_t part_floats(int RT, int D) { return int64_t(RT) * (D + 2); }
+
+// Slots of partial results: CTA c's first and last unfinished items at 2c and
+// 2c + 1, then one per own item and per prefix item finished by a single CTA.
+__host__ __device__ inline int64_t slot_own(const Args &A, int b, int h, int tile) {
+    return 2 * int64_t(A.grid) + (int64_t(b) * A.J.cache.heads + h) * A.own_tiles + tile;
+}
+__host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
+    return 2 * int64_t(A.grid) + int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles +
+           int64_t(h) * A.pre_tiles + tile;
+}
+
+// The CTA whose share [W c / grid, W (c + 1) / grid) holds step u of W.
+__device__ __forceinline__ int64_t cta_of(int64_t u, int64_t W, int64_t grid) {
+    return ((u + 1) * grid - 1) / W;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x is taken against this base: -inf (a row that has seen no key) must not
+// meet itself.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Four consecutive columns of a finished row.
+template <typename T>
+__device__ __forceinline__ void store_out(const trit_attn_job &J, int64_t at, float4 v) {
+    if (J.out_dtype == TRIT_F32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(J.out) + at) = v;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<T *>(J.out) + at) =
+            make_uint2(pack16<T>(v.x, v.y), pack16<T>(v.z, v.w));
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : m * 0.693147180559945309f + logf(l);
+}
+
+}  // namespace attn
+}  // namespace trit

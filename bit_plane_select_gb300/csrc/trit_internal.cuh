@@ -472,6 +472,8 @@ int bitcos_pack_host(const int8_t *w, int64_t N, int64_t K, uint64_t *bitmap, ui
 
 // The decode step between the products.
 cudaError_t launch_kv_append(const trit_kv_append_job &J, uint32_t *err, cudaStream_t s);
+int64_t attn_workspace_bytes(const trit_attn_job &J);
+cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_t s);
 cudaError_t launch_draft_verify(const trit_verify_job &J, uint32_t *err, cudaStream_t s);
 
 int device_sm_count();

@@ -40,6 +40,19 @@ bool heads_ok(int32_t hq, const trit_kv_cache &c) {
     return hq >= 1 && hq <= kMaxHeads && hq % c.heads == 0;
 }
 
+// Everything of an attention job but its data pointers.
+trit_status check_attn_sizes(const trit_attn_job &J) {
+    trit_status st = check_cache(J.cache);
+    if (st == TRIT_OK) st = check_batch(J.batch, J.cache);
+    if (st != TRIT_OK) return st;
+    if (J.flags != 0 || (J.out_dtype != TRIT_F32 && J.out_dtype != J.cache.dtype)) return TRIT_E_ARG;
+    if (!heads_ok(J.q_heads, J.cache) ||
+        int64_t(J.batch.B) * J.batch.T * J.q_heads > (int64_t(1) << 28) ||
+        J.batch.B * ((int64_t(J.batch.table_pages) * J.cache.page_size + 63) / 64) > (int64_t(1) << 30))
+        return TRIT_E_SHAPE;   // the last: steps of 64 keys are counted in 32 bits
+    return TRIT_OK;
+}
+
 bool err_ok(const uint32_t *err) { return err && aligned(err, 4); }
 
 }  // namespace
@@ -72,6 +85,27 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
     st = abi_check_device();
     if (st != TRIT_OK) return st;
     const cudaError_t e = launch_kv_append(J, err_flag, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TRIT_OK : abi_cuda_fail(e);
+}
+
+TRIT_API int64_t trit_attn_workspace_bytes(const trit_attn_job *job) {
+    return job && check_attn_sizes(*job) == TRIT_OK ? attn_workspace_bytes(*job) : -1;
+}
+
+TRIT_API trit_status trit_attn_paged(const trit_attn_job *job, uint32_t *err_flag,
+                                     trit_stream_t stream) {
+    if (!job || !err_ok(err_flag)) return TRIT_E_ARG;
+    const trit_attn_job &J = *job;
+    trit_status st = check_attn_sizes(J);
+    if (st != TRIT_OK) return st;
+    if (!J.q || !J.out || !J.workspace || !aligned(J.q, 16) || !aligned(J.out, 16) || !aligned(J.lse, 4) ||
+        !aligned(J.workspace, 16) || J.q_stride < 0 || J.q_stride % 8)
+        return TRIT_E_ARG;
+    if (!isfinite(J.scale)) return TRIT_E_SCALE;
+    if (J.workspace_bytes < attn_workspace_bytes(J)) return TRIT_E_SCRATCH;
+    st = abi_check_device();
+    if (st != TRIT_OK) return st;
+    const cudaError_t e = launch_attn_paged(J, err_flag, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TRIT_OK : abi_cuda_fail(e);
 }
 

@@ -15,9 +15,9 @@ import torch
 
 from . import _check, _dev, _stream, lib
 
-__all__ = ["KvCache", "KvBatch", "Rope", "AppendJob", "VerifyJob", "TritKvCache",
-           "TritKvBatch", "TritKvAppendJob", "TritVerifyJob", "trit_kv_append",
-           "trit_draft_verify", "trit_verify_workspace_bytes", "ERR_INDEX", "ERR_EMPTY",
+__all__ = ["KvCache", "KvBatch", "Rope", "AppendJob", "AttnJob", "VerifyJob", "TritKvCache",
+           "TritKvBatch", "TritKvAppendJob", "TritAttnJob", "TritVerifyJob", "trit_kv_append",
+           "trit_attn_paged", "trit_attn_workspace_bytes", "trit_draft_verify", "trit_verify_workspace_bytes", "ERR_INDEX", "ERR_EMPTY",
            "ROPE_PAIRS", "MAX_SEQUENCES"]
 
 ERR_INDEX = 32
@@ -48,6 +48,12 @@ class TritKvAppendJob(ctypes.Structure):
                 ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("max_pos", _i64),
                 ("eps", _f32), ("q_heads", _i32), ("rot", _i32), ("src_dtype", _i32),
                 ("flags", _u32), ("reserved", _i32)]
+
+
+class TritAttnJob(ctypes.Structure):
+    _fields_ = [("cache", TritKvCache), ("batch", TritKvBatch), ("q", _p), ("out", _p),
+                ("lse", _p), ("workspace", _p), ("workspace_bytes", _i64), ("q_stride", _i64),
+                ("scale", _f32), ("q_heads", _i32), ("out_dtype", _i32), ("flags", _u32)]
 
 
 class TritVerifyJob(ctypes.Structure):
@@ -207,6 +213,44 @@ def trit_kv_append(job: AppendJob, err_flag: torch.Tensor, stream=None):
     _check(lib().trit_kv_append(job.ref, _dev(err_flag, torch.int32, "err_flag"), _stream(stream)),
            "trit_kv_append")
     return job.q_out
+
+
+def trit_attn_workspace_bytes(job: TritAttnJob) -> int:
+    """Bytes of the workspace of a job (its pointers are not read); -1 for
+    sizes that are not supported."""
+    return int(lib().trit_attn_workspace_bytes(ctypes.byref(job)))
+
+
+class AttnJob(_Job):
+    """The arguments of trit_attn_paged: cache, batch, q (the cache's type;
+    token rows may be strided views) and out [B, T, Hq, D] (the cache's type or
+    fp32), optionally lse [B, T, Hq] fp32; scale defaults to 1/sqrt(D).  The
+    workspace is made here (or given: zeroed once, at least
+    trit_attn_workspace_bytes)."""
+
+    def __init__(self, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=None, workspace=None):
+        B, T, D, dt = batch.B, batch.T, cache.k.shape[3], cache.k.dtype
+        hq = q.numel() // max(1, B * T * D)
+        q_p, q_s = _token_rows(q, "q", (dt,), B, T, hq, D)
+        c = TritAttnJob(cache.c, batch.c, q_p, _whole(out, "out", (dt, torch.float32), (B, T, hq, D)),
+                        _whole(lse, "lse", (torch.float32,), (B, T, hq), True), None, 0, q_s,
+                        float(D ** -0.5 if scale is None else scale), hq, _DTYPE[out.dtype], 0)
+        need = trit_attn_workspace_bytes(c)
+        if need < 0:
+            raise ValueError("sizes outside the supported range")
+        if workspace is None:
+            workspace = _workspace(need, q.device)
+        c.workspace = _whole(workspace, "workspace", (torch.uint8,), workspace.shape)
+        c.workspace_bytes = workspace.numel()
+        self.out, self.lse, self.workspace = out, lse, workspace
+        self._bind(c, cache, batch, q, out, lse, workspace)
+
+
+def trit_attn_paged(job: AttnJob, err_flag: torch.Tensor, stream=None):
+    """Attention of the new tokens to the keys they see.  Returns out."""
+    _check(lib().trit_attn_paged(job.ref, _dev(err_flag, torch.int32, "err_flag"), _stream(stream)),
+           "trit_attn_paged")
+    return job.out
 
 
 def trit_verify_workspace_bytes(B: int) -> int:

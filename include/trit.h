@@ -645,6 +645,44 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
                                     trit_stream_t stream);
 
 /*
+ * trit_attn_paged -- attention of every new token to the keys it sees, the
+ * shared prefix computed once for the whole batch:
+ *     out = sum_j softmax_j(scale * q.k_j) v_j,
+ *     lse = ln sum_j exp(scale * q.k_j),
+ * query head h reading key head h / (Hq / heads).  Products are formed by 16-bit
+ * tensor-core instructions with fp32 sums; maxima, sums and partial outputs are
+ * fp32.  A row that sees no key (padding, or nothing cached) gives out = 0 and
+ * lse = -inf.  Keys past a sequence's length are never read: their slots may
+ * hold anything.  lens[b] outside [0, table_pages * page_size] or a page id
+ * outside the cache sets TRIT_ERR_INDEX (the length is clamped, the page's keys
+ * read as zeros).
+ *   q    token (b, t) at (b*T + t) * q_stride elements: Hq vectors of D of the
+ *        cache's type; 16-byte aligned, stride a multiple of 8
+ *   out  [B][T][Hq][D], out_dtype TRIT_F32 or the cache's; 16-byte aligned
+ *   lse  [B][T][Hq] fp32, or NULL
+ *   workspace  trit_attn_workspace_bytes(job) bytes (its pointers are not read),
+ *        16-byte aligned, zeroed once before its first use; every call leaves it
+ *        ready for the next.  Calls that may run at the same time need one each.
+ */
+typedef struct trit_attn_job {
+    trit_kv_cache cache;
+    trit_kv_batch batch;
+    const void *q;
+    void *out;
+    float *lse;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_stride;
+    float scale;                        /* finite */
+    int32_t q_heads, out_dtype;
+    uint32_t flags;                     /* must be 0 */
+} trit_attn_job;
+/* Bytes of the workspace, or -1 where the sizes are not supported. */
+TRIT_API int64_t trit_attn_workspace_bytes(const trit_attn_job *job);
+TRIT_API trit_status trit_attn_paged(const trit_attn_job *job, uint32_t *err_flag,
+                                     trit_stream_t stream);
+
+/*
  * trit_draft_verify -- which drafted tokens the target keeps, and the token that
  * follows them.  Draft t of sequence b, x = draft[b][t], is kept while
  *     u[b][t] * q[b][t][x] < p[b][t][x]      (one fp32 product),

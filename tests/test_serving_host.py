@@ -22,7 +22,8 @@ def trit():
 
 def structs(trit):
     return {"trit_kv_cache": trit.TritKvCache, "trit_kv_batch": trit.TritKvBatch,
-            "trit_kv_append_job": trit.TritKvAppendJob, "trit_verify_job": trit.TritVerifyJob}
+            "trit_kv_append_job": trit.TritKvAppendJob, "trit_attn_job": trit.TritAttnJob,
+            "trit_verify_job": trit.TritVerifyJob}
 
 
 def test_struct_layouts_match_the_c_compiler(trit, tmp_path):
@@ -90,6 +91,34 @@ def test_append_refusals(trit):
     assert fn(ctypes.byref(append_job(trit, b=batch(trit, B=4096, T=1 << 20))), P, NULL) == SHAPE
     assert fn(ctypes.byref(append_job(trit)), NULL, NULL) == ARG
     assert fn(None, P, NULL) == ARG
+
+
+def test_attn_refusals(trit):
+    L = trit.lib()
+
+    def job(c=None, b=None, **kw):
+        a = dict(cache=c or cache(trit), batch=b or batch(trit), q=P, out=P, lse=NULL, workspace=P,
+                 workspace_bytes=1 << 40, q_stride=2560, scale=0.1, q_heads=20, out_dtype=0, flags=0)
+        a.update(kw)
+        return trit.TritAttnJob(**a)
+    fn = L.trit_attn_paged
+    assert L.trit_attn_workspace_bytes(ctypes.byref(job())) > 0
+    for kw, code in BAD_CACHE:
+        assert fn(ctypes.byref(job(c=cache(trit, **kw))), P, NULL) == code, kw
+        assert L.trit_attn_workspace_bytes(ctypes.byref(job(c=cache(trit, **kw)))) == -1
+    for kw, code in BAD_BATCH:
+        assert fn(ctypes.byref(job(b=batch(trit, **kw))), P, NULL) == code, kw
+    need = L.trit_attn_workspace_bytes(ctypes.byref(job()))
+    for kw, code in [(dict(q=NULL), ARG), (dict(out=NULL), ARG), (dict(workspace=NULL), ARG), (dict(q=ODD), ARG),
+                     (dict(out=ODD), ARG), (dict(lse=ctypes.c_void_p(65538)), ARG), (dict(q_stride=2564), ARG),
+                     (dict(q_stride=-8), ARG), (dict(flags=1), ARG), (dict(out_dtype=2), ARG),
+                     (dict(q_heads=21), SHAPE), (dict(q_heads=0), SHAPE), (dict(scale=float("inf")), SCALE),
+                     (dict(workspace_bytes=need - 1), 8)]:
+        assert fn(ctypes.byref(job(**kw)), P, NULL) == code, kw
+    assert fn(ctypes.byref(job(b=batch(trit, B=4096, T=1 << 20))), P, NULL) == SHAPE
+    assert fn(ctypes.byref(job()), NULL, NULL) == ARG
+    assert fn(None, P, NULL) == ARG
+    assert L.trit_attn_workspace_bytes(None) == -1
 
 
 def test_verify_refusals(trit):
