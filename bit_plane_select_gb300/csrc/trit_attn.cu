@@ -217,7 +217,10 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
     const int64_t lo = W * blockIdx.x / gridDim.x, hi = W * (blockIdx.x + 1) / gridDim.x;
-    if (lo >= hi) return;
+    if (lo >= hi) {
+        pdl_wait();
+        return;
+    }
 
     // the ring runs ahead of the products, across items
     int64_t lu = lo;
@@ -446,135 +449,165 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
         ++u;
     }
     tc::cp_async_wait<0>();
+    // the join reads this grid's partial results and the prefix kernel's: end after both
+    pdl_wait();
 }
 
-// One warp per output row that no CTA finished: joins its partial results.
+// Joins the partial results of the rows no CTA finished: four rows of one
+// (sequence, key head) per CTA, four columns per thread, rows by lane first so
+// that both forms of partial results (by row, and the tensor-core kernel's by
+// column group) are read in whole sectors.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args A) {
     pdl_wait();
     const trit_attn_job &J = A.J;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int Hkv = J.cache.heads, G = A.G, B = J.batch.B, T_ = J.batch.T;
-    if (row >= int64_t(B) * T_ * J.q_heads) return;
-    const int hq = int(row % J.q_heads), h = hq / G;
-    const int64_t tok = row / J.q_heads;
-    const int b = int(tok / T_), t = int(tok - int64_t(b) * T_);
-    const int r = t * G + hq - h * G;
-    const int RT = A.RT;
+    const int Hkv = J.cache.heads, G = A.G, T_ = J.batch.T, RT = A.RT;
+    const int per = (A.R + 3) / 4, bh = int(blockIdx.x) / per;
+    const int row4 = int(blockIdx.x) - bh * per, b = bh / Hkv, h = bh - b * Hkv;
+    const int r = row4 * 4 + (threadIdx.x & 3), c = threadIdx.x >> 2;     // columns 4c ..
+    if (r >= A.R) return;
+    const int t = r / G, g = r - t * G;
 
-    // the own item's parts, then the prefix item's: slots and the row in them
+    // the own item's parts
     const int c0 = A.cum[b], n = A.cum[b + 1] - c0;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
-    const int64_t W = pre + int64_t(A.cum[B]) * Hkv * A.own_tiles;
+    const int64_t W = pre + int64_t(A.cum[J.batch.B]) * Hkv * A.own_tiles;
     const int tile = r / RT, rl = r - tile * RT;
-    int64_t of = 0, ol = -1;
+    int64_t first = 0;
+    int own = 0;
     if (n > 0) {
         const int64_t s0 = pre + (int64_t(c0) * Hkv * A.own_tiles) + (int64_t(h) * A.own_tiles + tile) * n;
-        of = cta_of(s0, W, A.grid);
-        ol = cta_of(s0 + n - 1, W, A.grid);
-        if (of == ol && J.batch.prefix_len == 0) return;   // written directly
+        first = cta_of(s0, W, A.grid);
+        own = int(cta_of(s0 + n - 1, W, A.grid) - first) + 1;
+        if (own == 1 && J.batch.prefix_len == 0) return;   // written directly
     }
-    const int own = int(ol - of + 1);
-    int64_t pf = 0, pl = -1;
+    // the prefix's
     const int64_t fr = int64_t(b) * A.R + r;
-    const int ptile = int(fr / RT), prl = int(fr - int64_t(ptile) * RT);
-    if (A.pre_tiles) {
-        const int64_t s0 = (int64_t(h) * A.pre_tiles + ptile) * A.pre_steps;
-        pf = cta_of(s0, W, A.grid);
-        pl = cta_of(s0 + A.pre_steps - 1, W, A.grid);
+    int64_t pfirst = 0;
+    int prefix = 0, pitem = 0, prl = 0, pstep = 1;
+    if (A.tc_items) {
+        const int ptile = int(fr / kTcRows), group = ptile >> 1;
+        const bool pair = 2 * group + 1 < A.tc_tiles;
+        prl = int(fr - int64_t(ptile) * kTcRows);
+        pfirst = int64_t(h * A.tc_groups + group) * A.tc_splits * 2 + (pair ? ptile & 1 : 0);
+        pstep = pair ? 2 : 1;
+        prefix = pair ? A.tc_splits : 2 * A.tc_splits;
+        if (t >= batch_new(J.batch, b)) prefix = 0;        // padding: that kernel does not look
+    } else if (A.pre_tiles) {
+        pitem = int(fr / RT);
+        prl = int(fr - int64_t(pitem) * RT);
+        const int64_t s0 = (int64_t(h) * A.pre_tiles + pitem) * A.pre_steps;
+        pfirst = cta_of(s0, W, A.grid);
+        prefix = int(cta_of(s0 + A.pre_steps - 1, W, A.grid) - pfirst) + 1;
     }
-    const int prefix = int(pl - pf + 1), total = own + prefix;
-    auto part = [&](int i, int &at) -> const float * {
-        int64_t slot;
-        if (i < own) {
-            at = rl;
-            slot = own == 1 ? slot_own(A, b, h, tile) : 2 * (of + i) + (i == 0 ? 1 : 0);
-        } else {
-            at = prl;
-            i -= own;
-            slot = prefix == 1 ? slot_prefix(A, h, ptile) : 2 * (pf + i) + (i == 0 ? 1 : 0);
+    const int total = own + prefix;
+    float m = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 4;     // parts in flight
+    for (int i0 = 0; i0 < total; i0 += U) {
+        float2 ml[U];
+        float4 x[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            int i = i0 + k;
+            ml[k] = make_float2(-INFINITY, 0.0f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < total) {
+                if (i >= own && A.tc_items) {
+                    const float *p = A.tc_parts + (pfirst + int64_t(i - own) * pstep) * part_floats(kTcRows, D);
+                    ml[k] = *reinterpret_cast<const float2 *>(p + kTcRows * D + 2 * prl);
+                    x[k] = *reinterpret_cast<const float4 *>(p + (c * kTcRows + prl) * 4);
+                } else {
+                    int64_t slot;
+                    int at = rl;
+                    if (i < own) {
+                        slot = own == 1 ? slot_own(A, b, h, tile) : 2 * (first + i) + (i == 0 ? 1 : 0);
+                    } else {
+                        at = prl;
+                        i -= own;
+                        slot = prefix == 1 ? slot_prefix(A, h, pitem) : 2 * (pfirst + i) + (i == 0 ? 1 : 0);
+                    }
+                    const float *p = A.parts + slot * part_floats(RT, D);
+                    ml[k] = *reinterpret_cast<const float2 *>(p + RT * D + 2 * at);
+                    x[k] = *reinterpret_cast<const float4 *>(p + at * D + c * 4);
+                }
+            }
         }
-        return A.parts + slot * part_floats(RT, D);
-    };
-    float m = -INFINITY;
-    for (int i = lane; i < total; i += 32) {
-        int at;
-        const float *p = part(i, at);
-        m = fmaxf(m, p[RT * D + 2 * at]);
-    }
+        float top = m;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    const float base = base_of(m);
-    constexpr int V = D / 32;    // columns of a lane
-    float v[V], l = 0.0f;
+        for (int k = 0; k < U; ++k) top = fmaxf(top, ml[k].x);
+        const float base = base_of(top), f0 = ex2(m - base);
+        m = top;
+        l *= f0;
+        v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < total; ++i) {
-        int at;
-        const float *p = part(i, at);
-        const float2 ml = *reinterpret_cast<const float2 *>(p + RT * D + 2 * at);
-        const float f = ex2(ml.x - base);
-        l += f * ml.y;
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] += f * p[at * D + k * 32 + lane];
+        for (int k = 0; k < U; ++k) {
+            // a part without keys holds no sums (its o was never written)
+            const bool some = ml[k].x != -INFINITY || ml[k].y != 0.0f;
+            const float f = ex2(ml[k].x - base);
+            if (some) {
+                l += f * ml[k].y;
+                v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
+            }
+        }
     }
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const int64_t at = row * D + k * 32 + lane;
-        if (J.out_dtype == TRIT_F32) static_cast<float *>(J.out)[at] = v[k] * inv;
-        else static_cast<T *>(J.out)[at] = static_cast<T>(v[k] * inv);
-    }
-    if (J.lse && lane == 0) J.lse[row] = lse_of(m, l);
+    const int64_t at = (int64_t(b) * T_ + t) * J.q_heads + int64_t(h) * G + g;
+    store_out<T>(J, at * D + c * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (J.lse && c == 0) J.lse[at] = lse_of(m, l);
 }
 
 // The work's layout from the job's sizes; the grid that a call would use.
-Args layout(const trit_attn_job &J, int sms) {
+Args layout(const trit_attn_job &J) {
     Args A = {};
     A.J = J;
     A.G = J.q_heads / J.cache.heads;
     A.R = J.batch.T * A.G;
-    const int64_t pre_rows = J.batch.prefix_len > 0 ? int64_t(J.batch.B) * A.R : 0;
+    const bool on_tc = prefix_on_tensor_cores(J);
+    if (on_tc) prefix_layout(A);
+    const int64_t pre_rows = J.batch.prefix_len > 0 && !on_tc ? int64_t(J.batch.B) * A.R : 0;
     A.RT = A.R > 16 || pre_rows > 16 ? 32 : 16;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
-    A.pre_steps = int((J.batch.prefix_len + kStep - 1) / kStep);
+    A.pre_steps = on_tc ? 0 : int((J.batch.prefix_len + kStep - 1) / kStep);
     A.page_shift = -1;
     for (int s = 0; s < 31; ++s)
         if (J.cache.page_size == (1 << s)) A.page_shift = s;
     const int64_t cap = (int64_t(J.batch.table_pages) * J.cache.page_size + kStep - 1) / kStep;
     const int64_t most = int64_t(J.cache.heads) * (int64_t(A.pre_tiles) * A.pre_steps +
                                                    int64_t(J.batch.B) * A.own_tiles * cap);
-    const int64_t grid = int64_t(sms) * (J.cache.head_dim == 64 && A.RT == 16 ? 4 : 2);
+    const int64_t grid = int64_t(kSms) * (J.cache.head_dim == 64 && A.RT == 16 ? 4 : 2);
     A.grid = int(most < grid ? most : grid);
     return A;
 }
 
 int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
 
-int64_t bytes_of(const Args &A) {
+int64_t part_bytes(const Args &A) {
     const int64_t slots = slot_prefix(A, 0, 0) + int64_t(A.J.cache.heads) * A.pre_tiles;
-    return cum_bytes(A.J) + slots * part_floats(A.RT, A.J.cache.head_dim) * 4;
+    return (slots * part_floats(A.RT, A.J.cache.head_dim) * 4 + 255) / 256 * 256;
 }
+
+int64_t bytes_of(const Args &A) { return cum_bytes(A.J) + part_bytes(A) + prefix_part_bytes(A); }
 
 template <typename T, int D, int MT>
 cudaError_t launch(const Args &A, cudaStream_t s) {
     const size_t smem = size_t(kWarps) * kStages * (2 * kKeys * D * 2) + kWarps * 16 * MT * 8 + kWarps * 4 +
                         (size_t(A.J.batch.B) + 1) * 4;
-    static bool set = false;
-    if (!set) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   128 * 1024);
-        if (e != cudaSuccess) return e;
-        set = true;
-    }
-    attn_kernel<T, D, MT><<<A.grid, kThreads, smem, s>>>(A);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
     if (e != cudaSuccess) return e;
-    const int64_t rows = int64_t(A.J.batch.B) * A.J.batch.T * A.J.q_heads;
-    return launch_pdl(join_kernel<T, D>, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, s, A);
+    if (A.tc_items) {
+        // the prefix kernel first; this one depends on nothing of it and may start beside it
+        e = launch_prefix(A, s);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(attn_kernel<T, D, MT>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
+    } else {
+        attn_kernel<T, D, MT><<<A.grid, kThreads, smem, s>>>(A);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
+    return launch_pdl(join_kernel<T, D>, dim3(unsigned(joins)), dim3(D), 0, s, A);
 }
 
 template <typename T>
@@ -586,14 +619,15 @@ cudaError_t launch_t(const Args &A, cudaStream_t s) {
 }  // namespace
 }  // namespace attn
 
-int64_t attn_workspace_bytes(const trit_attn_job &J) { return attn::bytes_of(attn::layout(J, 152)); }
+int64_t attn_workspace_bytes(const trit_attn_job &J) { return attn::bytes_of(attn::layout(J)); }
 
 cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_t s) {
-    attn::Args A = attn::layout(J, 152);
+    attn::Args A = attn::layout(J);
     A.err = err;
     A.scale2 = J.scale * 1.4426950408889634f;
     A.cum = static_cast<int32_t *>(J.workspace);
     A.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(J.workspace) + attn::cum_bytes(J));
+    A.tc_parts = A.parts + attn::part_bytes(A) / 4;
     return J.cache.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A, s) : attn::launch_t<__half>(A, s);
 }
 

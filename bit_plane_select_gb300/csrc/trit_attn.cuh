@@ -13,7 +13,9 @@
 namespace trit {
 namespace attn {
 
+constexpr int kSms = 152;           // the grids are cut for this many
 constexpr int kStep = 64;          // keys of one step of a CTA
+constexpr int kTcRows = 128;       // rows of a tile of the tensor-core prefix kernel
 
 // Rows: row r = t*G + g of a (sequence, key head) pair is token t and query
 // head h*G + g; a prefix row is the sequence's index times R plus r.  An item
@@ -32,6 +34,10 @@ struct Args {
     int32_t page_shift;      // log2(page_size), or -1
     int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
     float *parts;            // workspace: the partial results
+    // the prefix on the tensor cores (tc_items = 0: its items are above, with the own ones)
+    int32_t tc_tiles, tc_groups;   // 128-row tiles per key head, and pairs of them
+    int32_t tc_items, tc_splits;   // (head, pair) items, and parts of the keys each is cut into
+    float *tc_parts;         // workspace: their partial results, [item][split][stream]
 };
 
 // A partial result: RT x D sums, then RT pairs (m, l).
@@ -74,6 +80,12 @@ __device__ __forceinline__ void store_out(const trit_attn_job &J, int64_t at, fl
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -INFINITY : m * 0.693147180559945309f + logf(l);
 }
+
+// trit_attn_prefix.cu: whether the prefix runs there, its layout, its launch.
+bool prefix_on_tensor_cores(const trit_attn_job &J);
+void prefix_layout(Args &A);
+int64_t prefix_part_bytes(const Args &A);
+cudaError_t launch_prefix(const Args &A, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace trit

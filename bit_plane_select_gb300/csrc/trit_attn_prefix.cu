@@ -1,0 +1,472 @@
+// The shared prefix of trit_attn_paged on the 5th-generation tensor cores: all
+// rows of the batch that read key head h -- B T Hq/Hkv of them -- against the
+// prefix's keys, read once per 256 rows.
+//
+// With R rows to a key the work is 4 D R flops on 4 D bytes, so above a few
+// hundred rows the tensor cores bound it, and before them the exponentials: 128 keys
+// x 128 rows take 2 x 512 SM-clocks of tensor pipe (S = Q K^T, then O += P V)
+// and 16384 exponentials.  One CTA therefore runs two streams, each a
+// 128-row softmax (one row per thread, no shuffles) on its own warpgroup and its
+// own accumulators in tensor memory, so that one stream's products run under
+// the other's softmax: S (128 x 128 fp32), overwritten in place by P (16-bit,
+// the A operand of the second product, which reads it from tensor memory), and
+// O (128 x D fp32).  Two row tiles of a head share the loads of K and V as the
+// two streams; a single tile's streams take alternate blocks of 128 keys.
+//
+// K and V blocks come page by page through TMA (128-byte swizzle) into a ring.
+// V is read as stored, keys by columns: an MN-major B operand.  O is rescaled
+// only when a row's maximum grew by more than 2^8 since its base was fixed; until
+// then P may exceed 1 (at most 2^8) and both l and O carry the same base.
+//
+// Each item (256 or 128 rows of a head) is cut along the keys into `splits`
+// parts, one CTA each; the partial results (unnormalised O, base, l) are joined with the
+// sequences' own by the join kernel.  They are stored four columns by row,
+// [D/4][128] float4, so that a warp's 32 rows store 512 contiguous bytes.
+#include <cuda.h>
+
+#include "trit_attn.cuh"
+#include "trit_tc.cuh"
+
+namespace trit {
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kBlockKeys = 128;
+constexpr int kRows = 128;
+constexpr int kRing = 4;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 320;
+constexpr int kTmemCols = 512;     // S of the two streams at 0 and 128, O at 256 and 384
+constexpr float kGrow = 8.0f;      // log2 of the growth of a maximum that O tolerates
+
+template <int D>
+__host__ __device__ constexpr int tile_bytes() { return kBlockKeys * D * 2; }
+template <int D>
+constexpr size_t smem_bytes() { return 1024 + size_t(2 + kRing) * tile_bytes<D>() + 256; }
+
+template <typename T>
+__host__ __device__ constexpr uint32_t type_bits() { return 0; }
+template <>
+__host__ __device__ constexpr uint32_t type_bits<__nv_bfloat16>() { return (1u << 7) | (1u << 10); }
+
+// Instruction descriptors, kind::f16, fp32 accumulator, M = 128: S (N = 128, both
+// operands K-major) and O (N = D, B MN-major).
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_s() { return (1u << 4) | type_bits<T>() | ((128u >> 3) << 17) | ((128u >> 4) << 24); }
+template <typename T, int D>
+__host__ __device__ constexpr uint32_t idesc_o() {
+    return (1u << 4) | type_bits<T>() | (1u << 16) | ((uint32_t(D) >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// MN-major 128-byte-swizzled operand: 64 columns (128 bytes) of a key are
+// contiguous, 8 keys make an atom of 1024 bytes (the stride between key groups),
+// and the next 64 columns start a half tile later.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((kBlockKeys * 128) >> 4) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+#define TRIT_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define TRIT_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+
+// 32 consecutive columns of the warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : TRIT_R8(v, 0), TRIT_R8(v, 8), TRIT_R8(v, 16), TRIT_R8(v, 24)
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::TRIT_W8(v, 0),
+        TRIT_W8(v, 8), TRIT_W8(v, 16), TRIT_W8(v, 24), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_page(void *dst, const CUtensorMap *map, int x, int slot, int head, int page,
+                                         uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5}], [%6];" ::
+            "r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int kTile = tile_bytes<D>();
+    uint8_t *qs = smem, *ring = smem + 2 * kTile;
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kTile);
+    uint64_t *empty = full + kRing;
+    uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
+    uint64_t *p_full = s_full + 2;       // stream's P is
+    uint64_t *o_full = p_full + 2;       // stream's O is finished
+    uint64_t *pv_done = o_full + 2;      // the product just issued has read its P
+    uint64_t *q_full = pv_done + 1;
+    uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+    uint32_t *timed_out = tmem_slot + 1;
+
+    const trit_attn_job &J = A.J;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = int(blockIdx.x) % A.tc_items, split = int(blockIdx.x) / A.tc_items;
+    const int group = item % A.tc_groups, h = item / A.tc_groups;
+    const int P = int(J.batch.prefix_len);
+    const int nb = (P + kBlockKeys - 1) / kBlockKeys;
+    const int j0 = int(int64_t(nb) * split / A.tc_splits), j1 = int(int64_t(nb) * (split + 1) / A.tc_splits);
+    const int n = j1 - j0;
+    const bool pair = 2 * group + 1 < A.tc_tiles;     // two row tiles, or one over two streams
+    const int ops = pair ? 2 * n : n;                  // op k: stream k & 1, block pair ? k / 2 : k
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRing; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_full[s], 4);
+            mbar_init(&o_full[s], 1);
+        }
+        mbar_init(pv_done, 1);
+        mbar_init(q_full, 8);
+        mbar_init(tail, 1);
+        *timed_out = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch();
+
+    // a block's place in the ring's order of use: K0 V0 K1 V1 ... for a pair,
+    // K0 K1 V0 K2 V1 ... for one tile on two streams
+    auto k_at = [&](int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
+    auto v_at = [&](int j) { return pair ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2); };
+
+    if (warp == kLoadWarp) {
+        const int ps = J.cache.page_size;
+        const int rows = ps < kBlockKeys ? ps : kBlockKeys;      // keys of one copy
+        const int npages = (P + ps - 1) / ps;
+        auto load = [&](int j, bool is_v, int at) -> bool {
+            const int s = at % kRing;
+            if (!mbar_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) return false;
+            const int key0 = (j0 + j) * kBlockKeys;
+            const int first = key0 / ps;
+            int copies = kBlockKeys / rows;
+            if (copies > npages - first) copies = npages - first;
+            const int keys = P - key0 < kBlockKeys ? P - key0 : kBlockKeys;
+            const bool clear = is_v && keys < kBlockKeys;
+            uint64_t *bar = clear ? tail : &full[s];
+            uint8_t *st = ring + s * kTile;
+            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * D * 2);
+            __syncwarp();
+            for (int i = lane; i < copies * (D / 64); i += 32) {
+                const int c = i / (D / 64), half = i % (D / 64);
+                const int page = __ldg(J.batch.prefix_table + first + c);
+                if (page < 0 || page >= J.cache.pages) raise_flag(A.err, TRIT_ERR_INDEX);   // reads as zeros
+                tma_page(st + half * (kBlockKeys * 128) + c * rows * 128, is_v ? &vmap : &kmap, half * 64,
+                         key0 - first * ps, h, page, bar);
+            }
+            if (clear) {   // keys past the prefix get P = 0, which must not meet a NaN
+                if (!__all_sync(~0u, mbar_wait(tail, 0, timed_out))) return false;
+                for (int i = lane; i < (kBlockKeys - keys) * (D / 8); i += 32) {
+                    const int r = keys + i / (D / 8), c = i % (D / 8);
+                    *reinterpret_cast<uint4 *>(st + (c / 8) * (kBlockKeys * 128) + r * 128 + (c % 8) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+            return true;
+        };
+        bool ok = pair ? true : load(0, false, 0);
+        for (int j = 0; ok && j < n; ++j) {
+            if (pair) ok = load(j, false, k_at(j));
+            else if (j + 1 < n) ok = load(j + 1, false, k_at(j + 1));
+            ok = ok && load(j, true, v_at(j));
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            const uint32_t qaddr = smem_u32(qs), raddr = smem_u32(ring);
+            auto issue_s = [&](int k) -> bool {
+                const int s = k & 1, j = pair ? k / 2 : k, at = k_at(j), st = at % kRing;
+                if (!mbar_wait(&full[st], (at / kRing) & 1, timed_out)) return false;
+                tc_fence_after();
+                const uint32_t a = qaddr + (pair ? s * kTile : 0), b = raddr + st * kTile;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk / 4) * (kBlockKeys * 128) + (kk % 4) * 32;
+                    mma_ss(tmem + s * 128, sw128_desc(a + off), sw128_desc(b + off), idesc_s<T>(), kk > 0);
+                }
+                if (!pair || s == 1) mma_commit(&empty[st]);
+                mma_commit(&s_full[s]);
+                return true;
+            };
+            bool ok = mbar_wait(q_full, 0, timed_out);
+            tc_fence_after();
+            for (int k = 0; ok && k < 2 && k < ops; ++k) ok = issue_s(k);
+            for (int k = 0; ok && k < ops; ++k) {
+                const int s = k & 1, j = pair ? k / 2 : k, at = v_at(j), st = at % kRing;
+                ok = mbar_wait(&p_full[s], (k >> 1) & 1, timed_out) &&
+                     mbar_wait(&full[st], (at / kRing) & 1, timed_out);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b = raddr + st * kTile;
+#pragma unroll
+                for (int kk = 0; kk < kBlockKeys / 16; ++kk)
+                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, mn_desc(b + kk * 2048), idesc_o<T, D>(),
+                           k > 1 || kk > 0);
+                if (!pair || s == 1) mma_commit(&empty[st]);
+                if (k + 2 >= ops) {
+                    mma_commit(&o_full[s]);
+                } else {
+                    // S of the stream's next block takes the place of this P
+                    mma_commit(pv_done);
+                    ok = mbar_wait(pv_done, k & 1, timed_out) && issue_s(k + 2);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // softmax: stream s, row r of its tile (tensor-memory lane r)
+        const int s = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
+        const int64_t rows = int64_t(J.batch.B) * A.R;
+        {   // the query tile: chunk c of row i, swizzled; the two streams' threads share a single tile
+            constexpr int CH = D / 8;
+            const int tile = 2 * group + (pair ? s : 0);
+            const uint32_t flip = A.scale2 < 0.0f ? 0x80008000u : 0u;   // -q, and |scale| below
+            uint8_t *dst = qs + (pair ? s * kTile : 0);
+            const int step = pair ? 128 : 256, from = pair ? r : int(threadIdx.x);
+            for (int i = from; i < kRows * CH; i += step) {
+                const int row = i / CH, c = i % CH;
+                const int64_t fr = int64_t(tile) * kRows + row;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (fr < rows) {
+                    const int b = int(fr / A.R), rr = int(fr - int64_t(b) * A.R), t = rr / A.G, g = rr - t * A.G;
+                    v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) +
+                                                              (int64_t(b) * J.batch.T + t) * J.q_stride +
+                                                              (int64_t(h) * A.G + g) * D + c * 8));
+                    v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+                }
+                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(row, c % 8)) = v;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        const float scale2 = fabsf(A.scale2);
+        const int mine = pair ? n : (n + 1 - s) / 2;       // this stream's blocks
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int i = 0; i < mine; ++i) {
+            ok = __all_sync(~0u, mbar_wait(&s_full[s], i & 1, timed_out));
+            if (!ok) break;
+            tc_fence_after();
+            const int j = pair ? i : 2 * i + s;
+            const int left = P - (j0 + j) * kBlockKeys;
+            uint32_t v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + s * 128 + quarter + c * 32, v + c * 32);
+            tmem_wait_ld();
+            if (left < kBlockKeys) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c >= left) v[c] = 0xff800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+            if (i == 0) {
+                m = top;
+            } else {
+                const bool grow = top > m + kGrow;
+                if (__any_sync(~0u, grow)) {
+                    // every product into O has completed: S was issued after them
+                    const float f = grow ? ex2(m - top) : 1.0f;
+                    if (grow) m = top;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t w[32];
+                        tmem_ld32(tmem + 256 + s * 128 + quarter + c * 32, w);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                        tmem_st32(tmem + 256 + s * 128 + quarter + c * 32, w);
+                    }
+                }
+            }
+            const float base = base_of(m);
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float e0 = ex2(fmaf(__uint_as_float(v[half * 64 + 2 * c]), scale2, -base));
+                    const float e1 = ex2(fmaf(__uint_as_float(v[half * 64 + 2 * c + 1]), scale2, -base));
+                    sum[c & 3] += e0 + e1;
+                    w[c] = pack16<T>(e0, e1);
+                }
+                tmem_st32(tmem + s * 128 + quarter + half * 32, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[s]);
+        }
+        float *part = A.tc_parts + ((int64_t(item) * A.tc_splits + split) * 2 + s) * part_floats(kRows, D);
+        if (mine > 0 && ok) {
+            ok = __all_sync(~0u, mbar_wait(&o_full[s], 0, timed_out));
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t w[32];
+                    tmem_ld32(tmem + 256 + s * 128 + quarter + c * 32, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<uint4 *>(part + ((c * 8 + e) * kRows + r) * 4) =
+                            make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                }
+            }
+        }
+        *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m, l);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *timed_out) raise_flag(A.err, TRIT_ERR_TIMEOUT);
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// The cache as (column, slot, head, page); a copy is 64 columns of min(page_size,
+// 128) keys of one head's page.
+bool make_map(CUtensorMap *map, const trit_kv_cache &C, void *base) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {cuuint64_t(C.head_dim), cuuint64_t(C.page_size), cuuint64_t(C.heads),
+                                cuuint64_t(C.pages)};
+    const cuuint64_t one = cuuint64_t(C.head_dim) * 2;   // a dimension of one entry needs no stride
+    const cuuint64_t strides[3] = {C.page_size > 1 ? cuuint64_t(C.slot_stride) * 2 : one,
+                                   C.heads > 1 ? cuuint64_t(C.head_stride) * 2 : one,
+                                   C.pages > 1 ? cuuint64_t(C.page_stride) * 2 : one};
+    const cuuint32_t box[4] = {64, cuuint32_t(C.page_size < kBlockKeys ? C.page_size : kBlockKeys), 1, 1};
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    return fn(map, C.dtype == TRIT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
+              dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch(const Args &A, cudaStream_t s) {
+    CUtensorMap kmap, vmap;
+    if (!make_map(&kmap, A.J.cache, A.J.cache.k) || !make_map(&vmap, A.J.cache, A.J.cache.v))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(smem_bytes<D>()));
+    if (e != cudaSuccess) return e;
+    prefix_kernel<T, D><<<A.tc_items * A.tc_splits, kThreads, smem_bytes<D>(), s>>>(A, kmap, vmap);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prefix_on_tensor_cores(const trit_attn_job &J) {
+    const trit_kv_cache &C = J.cache;
+    const int64_t rows = int64_t(J.batch.B) * J.batch.T * (J.q_heads / C.heads);
+    const bool pow2 = (C.page_size & (C.page_size - 1)) == 0;
+    // strides a copy's descriptor cannot hold (or that overlap) stay on the other path
+    const int64_t most = int64_t(1) << 38;
+    const bool strides = C.slot_stride >= C.head_dim && (C.heads == 1 || C.head_stride >= C.head_dim) &&
+                         (C.pages == 1 || C.page_stride >= C.head_dim) && C.slot_stride < most &&
+                         C.head_stride < most && C.page_stride < most;
+    // a scale of 0 would meet the -inf of masked columns there
+    return J.batch.prefix_len > 0 && J.scale != 0.0f && rows > 32 && pow2 && C.page_size >= 16 && strides;
+}
+
+void prefix_layout(Args &A) {
+    const trit_attn_job &J = A.J;
+    const int64_t rows = int64_t(J.batch.B) * A.R;
+    const int nb = int((J.batch.prefix_len + kBlockKeys - 1) / kBlockKeys);
+    A.tc_tiles = int((rows + kRows - 1) / kRows);
+    A.tc_groups = (A.tc_tiles + 1) / 2;
+    A.tc_items = A.tc_groups * J.cache.heads;
+    int splits = kSms / A.tc_items;
+    if (splits < 1) splits = 1;
+    if (splits > nb) splits = nb;
+    A.tc_splits = splits;
+}
+
+cudaError_t launch_prefix(const Args &A, cudaStream_t s) {
+    if (A.J.cache.dtype == TRIT_BF16)
+        return A.J.cache.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, s) : launch<__nv_bfloat16, 64>(A, s);
+    return A.J.cache.head_dim == 128 ? launch<__half, 128>(A, s) : launch<__half, 64>(A, s);
+}
+
+int64_t prefix_part_bytes(const Args &A) {
+    return int64_t(A.tc_items) * A.tc_splits * 2 * part_floats(kRows, A.J.cache.head_dim) * 4;
+}
+
+}  // namespace attn
+}  // namespace trit

@@ -141,6 +141,52 @@ def test_matches_64_bits(t, case, wide):
     assert err == 0
 
 
+LONG = [
+    # several blocks of 128 keys to a part: one row tile on two streams, two tiles, odd tiles
+    ([3] * 40, 1, None, 32, 32, 64, 16, BF, 4000, False),
+    ([5] * 34, 4, [1 + i % 4 for i in range(34)], 20, 20, 64, 64, HF, 3969, True),
+    ([5] * 34, 2, None, 20, 20, 128, 256, BF, 2100, False),
+    ([9] * 66, 1, None, 40, 10, 128, 32, HF, 1793, False),
+    ([1] * 33, 1, None, 40, 40, 128, 16, BF, 2048, True),
+]
+
+
+@pytest.mark.parametrize("case", LONG)
+@pytest.mark.parametrize("sharp", [1, 6, -6])
+def test_long_prefix_many_rows(t, case, sharp):
+    """Sharp scores make the maxima grow from block to block; a negative scale too."""
+    lens, T, new, hq, hkv, D, page, dt, prefix, nhd = case
+    c = build_case(lens, T, new, hq, hkv, D, page, dt, prefix, nhd, seed=prefix)
+    if abs(sharp) > 1:
+        c["q"] *= abs(sharp)
+        ramp = torch.linspace(0.1, 1.0, prefix)[:, None, None]
+        at = ref.slots(c["pre"], prefix, page)
+        kk = c["k"].permute(0, 2, 1, 3)
+        kk[at] = (kk[at].float() * ramp).to(dt)
+    err, _ = run(t, c, dt, scale=math.copysign(D ** -0.5, sharp))
+    assert err == 0
+
+
+def test_zero_scale(t):
+    """Every visible key weighs the same."""
+    for lens in ([5, 9], [3] * 40):
+        c = build_case(lens, 1, None, 4, 1, 64, 16, BF, 133)
+        err, _ = run(t, c, BF, scale=0.0)
+        assert err == 0
+
+
+def test_a_bad_prefix_page_is_flagged(t):
+    for lens in ([5, 9], [3] * 40):
+        for bad in (-1, 9999):
+            c = build_case(lens, 1, None, 4, 1, 64, 16, BF, 133, poison=False)
+            c["pre"][3] = bad
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            job = make_job(t, c, BF)
+            t.trit_attn_paged(job, err)
+            torch.cuda.synchronize()
+            assert int(err.item()) == t.ERR_INDEX and bool(job.out.isfinite().all())
+
+
 def test_more_new_tokens_than_own_keys(t):
     """Tokens before own key 0 see the prefix alone (nothing, without one)."""
     for prefix in (0, 40):
