@@ -5,7 +5,9 @@
 // the call are laid end to end, and each of a fixed grid of CTAs takes an equal
 // run of them, whatever the lengths (which only the device knows): a CTA's run
 // may end one item, cover several and begin another.  Items a CTA does not
-// finish alone leave partial results that a second launch joins.
+// finish alone leave partial results, joined by the last of the item's CTAs where
+// there is no prefix and by a second launch where there is one (a prefix
+// part belongs to many sequences).
 //
 // Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
 // reading K and V: 4 D bytes a key against 4 D R flops.  A step's 64 keys go 16
@@ -196,6 +198,15 @@ __device__ __forceinline__ void count_steps(const Args &A, int32_t *cum, int32_t
     __syncthreads();
 }
 
+// One part joined to l and v, which are against `base`.  A part without keys
+// (m = -inf, l = 0) holds no sums: its o was never written.
+__device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float &l, float4 &v) {
+    if (ml.x == -INFINITY && ml.y == 0.0f) return;
+    const float f = ex2(ml.x - base);
+    l += f * ml.y;
+    v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+}
+
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -216,7 +227,19 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
         for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
-    const int64_t lo = W * blockIdx.x / gridDim.x, hi = W * (blockIdx.x + 1) / gridDim.x;
+    const int64_t ctas = W < gridDim.x ? W : gridDim.x;      // that have a share: at least a step each
+    const int64_t lo = blockIdx.x < ctas ? W * blockIdx.x / ctas : W;
+    const int64_t hi = blockIdx.x < ctas ? W * (blockIdx.x + 1) / ctas : W;
+    if (J.batch.prefix_len == 0) {   // sequences without a key are in no CTA's share
+        for (int b = blockIdx.x; b < B; b += gridDim.x) {
+            if (cum[b] != cum[b + 1]) continue;
+            const int64_t at = int64_t(b) * J.batch.T * J.q_heads;
+            const int rows = J.batch.T * J.q_heads;
+            for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads)
+                store_out<T>(J, at * D + int64_t(i) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+            for (int i = threadIdx.x; J.lse && i < rows; i += kThreads) J.lse[at + i] = -INFINITY;
+        }
+    }
     if (lo >= hi) {
         pdl_wait();
         return;
@@ -240,6 +263,63 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     };
 #pragma unroll 1
     for (int s = 0; s < kStages; ++s) load_next(s);
+
+    // Without a prefix, the last of an item's CTAs to get here joins its parts: one
+    // counter per item, left at zero.
+    auto join_last = [&](const Place &q, int rows, int filled) {
+        const int64_t s0 = int64_t(cum[q.b]) * Hkv * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
+        const int64_t c0 = cta_of(s0, W, ctas);
+        const int parts = int(cta_of(s0 + q.steps - 1, W, ctas) - c0) + 1;
+        uint32_t *count = A.count + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
+        if (threadIdx.x == 0) {
+            __threadfence();
+            const bool last = atomicAdd(count, 1u) + 1 == uint32_t(parts);
+            if (last) *count = 0;
+            __threadfence();
+            scratch[0] = last;
+        }
+        __syncthreads();
+        if (scratch[0]) {
+            constexpr int CH = D / 4;
+            for (int i = threadIdx.x; i < filled * CH; i += kThreads) {
+                const int r = i / CH, c = (i % CH) * 4, row = q.tile * RT + r;
+                if (row >= rows) break;
+                float m = -INFINITY, l = 0.0f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                constexpr int U = 8;     // parts in flight
+                for (int k0 = 0; k0 < parts; k0 += U) {
+                    float2 ml[U];
+                    float4 x[U];
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        ml[k] = make_float2(-INFINITY, 0.0f);
+                        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (k0 + k < parts) {
+                            const float *part =
+                                A.parts + (2 * (c0 + k0 + k) + (k0 + k == 0 ? 1 : 0)) * part_floats(RT, D);
+                            ml[k] = __ldcg(reinterpret_cast<const float2 *>(part + RT * D + 2 * r));
+                            x[k] = __ldcg(reinterpret_cast<const float4 *>(part + r * D + c));
+                        }
+                    }
+                    float top = m;
+#pragma unroll
+                    for (int k = 0; k < U; ++k) top = fmaxf(top, ml[k].x);
+                    const float base = base_of(top), f0 = ex2(m - base);
+                    m = top;
+                    l *= f0;
+                    v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
+#pragma unroll
+                    for (int k = 0; k < U; ++k) add_part(ml[k], x[k], base, l, v);
+                }
+                const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+                const int t = row / G, g = row - t * G;
+                const int64_t at = (int64_t(q.b) * J.batch.T + t) * J.q_heads + int64_t(q.h) * G + g;
+                store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                if (J.lse && c == 0) J.lse[at] = lse_of(m, l);
+            }
+        }
+        __syncthreads();   // scratch[0] is free again
+    };
 
     uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4];
@@ -441,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
                 }
                 __syncthreads();
             }
+            if (!direct && J.batch.prefix_len == 0) join_last(p, rows, mts * 16);
             fresh = true;
         }
         load_next(stage);
@@ -453,33 +534,37 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     pdl_wait();
 }
 
-// Joins the partial results of the rows no CTA finished: four rows of one
+// Joins the partial results of a call with a prefix: four rows of one
 // (sequence, key head) per CTA, four columns per thread, rows by lane first so
 // that both forms of partial results (by row, and the tensor-core kernel's by
-// column group) are read in whole sectors.
+// column group) are read in whole sectors; kJoin groups of threads take every
+// kJoin-th part, four at a time, since the loads' latency is the cost.
+constexpr int kJoin = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ Args A) {
+    __shared__ float sh[kJoin - 1][6][D];
     pdl_wait();
     const trit_attn_job &J = A.J;
     const int Hkv = J.cache.heads, G = A.G, T_ = J.batch.T, RT = A.RT;
     const int per = (A.R + 3) / 4, bh = int(blockIdx.x) / per;
     const int row4 = int(blockIdx.x) - bh * per, b = bh / Hkv, h = bh - b * Hkv;
-    const int r = row4 * 4 + (threadIdx.x & 3), c = threadIdx.x >> 2;     // columns 4c ..
-    if (r >= A.R) return;
+    const int tid = threadIdx.x % D, part0 = threadIdx.x / D;            // the group's first part
+    const int r4 = row4 * 4 + (tid & 3), c = tid >> 2;                    // columns 4c ..
+    const int r = r4 < A.R ? r4 : A.R - 1;
     const int t = r / G, g = r - t * G;
 
     // the own item's parts
     const int c0 = A.cum[b], n = A.cum[b + 1] - c0;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(A.cum[J.batch.B]) * Hkv * A.own_tiles;
+    const int64_t ctas = W < A.grid ? W : A.grid;
     const int tile = r / RT, rl = r - tile * RT;
     int64_t first = 0;
     int own = 0;
     if (n > 0) {
         const int64_t s0 = pre + (int64_t(c0) * Hkv * A.own_tiles) + (int64_t(h) * A.own_tiles + tile) * n;
-        first = cta_of(s0, W, A.grid);
-        own = int(cta_of(s0 + n - 1, W, A.grid) - first) + 1;
-        if (own == 1 && J.batch.prefix_len == 0) return;   // written directly
+        first = cta_of(s0, W, ctas);
+        own = int(cta_of(s0 + n - 1, W, ctas) - first) + 1;
     }
     // the prefix's
     const int64_t fr = int64_t(b) * A.R + r;
@@ -497,19 +582,19 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args A)
         pitem = int(fr / RT);
         prl = int(fr - int64_t(pitem) * RT);
         const int64_t s0 = (int64_t(h) * A.pre_tiles + pitem) * A.pre_steps;
-        pfirst = cta_of(s0, W, A.grid);
-        prefix = int(cta_of(s0 + A.pre_steps - 1, W, A.grid) - pfirst) + 1;
+        pfirst = cta_of(s0, W, ctas);
+        prefix = int(cta_of(s0 + A.pre_steps - 1, W, ctas) - pfirst) + 1;
     }
     const int total = own + prefix;
     float m = -INFINITY, l = 0.0f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 4;     // parts in flight
-    for (int i0 = 0; i0 < total; i0 += U) {
+    for (int i0 = part0; i0 < total; i0 += U * kJoin) {
         float2 ml[U];
         float4 x[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            int i = i0 + k;
+            int i = i0 + k * kJoin;
             ml[k] = make_float2(-INFINITY, 0.0f);
             x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < total) {
@@ -541,16 +626,26 @@ __global__ void __launch_bounds__(D) join_kernel(const __grid_constant__ Args A)
         l *= f0;
         v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            // a part without keys holds no sums (its o was never written)
-            const bool some = ml[k].x != -INFINITY || ml[k].y != 0.0f;
-            const float f = ex2(ml[k].x - base);
-            if (some) {
-                l += f * ml[k].y;
-                v.x += f * x[k].x; v.y += f * x[k].y; v.z += f * x[k].z; v.w += f * x[k].w;
-            }
-        }
+        for (int k = 0; k < U; ++k) add_part(ml[k], x[k], base, l, v);
     }
+    if (part0) {
+        float(*o)[D] = sh[part0 - 1];
+        o[0][tid] = m; o[1][tid] = l;
+        o[2][tid] = v.x; o[3][tid] = v.y; o[4][tid] = v.z; o[5][tid] = v.w;
+    }
+    __syncthreads();
+    if (part0 || r4 >= A.R) return;
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kJoin - 1; ++k) top = fmaxf(top, sh[k][0][tid]);
+    const float base = base_of(top), f0 = ex2(m - base);
+    m = top;
+    l *= f0;
+    v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
+#pragma unroll
+    for (int k = 0; k < kJoin - 1; ++k)
+        add_part(make_float2(sh[k][0][tid], sh[k][1][tid]),
+                 make_float4(sh[k][2][tid], sh[k][3][tid], sh[k][4][tid], sh[k][5][tid]), base, l, v);
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     const int64_t at = (int64_t(b) * T_ + t) * J.q_heads + int64_t(h) * G + g;
     store_out<T>(J, at * D + c * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -581,14 +676,19 @@ Args layout(const trit_attn_job &J) {
     return A;
 }
 
+// [B + 1] sums of steps, then one counter per own item.
 int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
+int64_t head_bytes(const Args &A) {
+    const int64_t items = int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles;
+    return cum_bytes(A.J) + (items * 4 + 255) / 256 * 256;
+}
 
 int64_t part_bytes(const Args &A) {
     const int64_t slots = slot_prefix(A, 0, 0) + int64_t(A.J.cache.heads) * A.pre_tiles;
     return (slots * part_floats(A.RT, A.J.cache.head_dim) * 4 + 255) / 256 * 256;
 }
 
-int64_t bytes_of(const Args &A) { return cum_bytes(A.J) + part_bytes(A) + prefix_part_bytes(A); }
+int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_part_bytes(A); }
 
 template <typename T, int D, int MT>
 cudaError_t launch(const Args &A, cudaStream_t s) {
@@ -606,8 +706,9 @@ cudaError_t launch(const Args &A, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
+    if (A.J.batch.prefix_len == 0) return cudaSuccess;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
-    return launch_pdl(join_kernel<T, D>, dim3(unsigned(joins)), dim3(D), 0, s, A);
+    return launch_pdl(join_kernel<T, D>, dim3(unsigned(joins)), dim3(kJoin * D), 0, s, A);
 }
 
 template <typename T>
@@ -626,7 +727,9 @@ cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_
     A.err = err;
     A.scale2 = J.scale * 1.4426950408889634f;
     A.cum = static_cast<int32_t *>(J.workspace);
-    A.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(J.workspace) + attn::cum_bytes(J));
+    uint8_t *ws = static_cast<uint8_t *>(J.workspace);
+    A.count = reinterpret_cast<uint32_t *>(ws + attn::cum_bytes(J));
+    A.parts = reinterpret_cast<float *>(ws + attn::head_bytes(A));
     A.tc_parts = A.parts + attn::part_bytes(A) / 4;
     return J.cache.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A, s) : attn::launch_t<__half>(A, s);
 }

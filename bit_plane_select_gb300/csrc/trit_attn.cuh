@@ -33,6 +33,7 @@ struct Args {
     int32_t grid;            // CTAs the work is cut over
     int32_t page_shift;      // log2(page_size), or -1
     int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
+    uint32_t *count;         // workspace: arrivals per own item, zero between calls
     float *parts;            // workspace: the partial results
     // the prefix on the tensor cores (tc_items = 0: its items are above, with the own ones)
     int32_t tc_tiles, tc_groups;   // 128-row tiles per key head, and pairs of them
@@ -53,9 +54,10 @@ __host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
            int64_t(h) * A.pre_tiles + tile;
 }
 
-// The CTA whose share [W c / grid, W (c + 1) / grid) holds step u of W.
-__device__ __forceinline__ int64_t cta_of(int64_t u, int64_t W, int64_t grid) {
-    return ((u + 1) * grid - 1) / W;
+// The CTA whose share [W c / ctas, W (c + 1) / ctas) holds step u of W; ctas <= W,
+// so that no share is empty and an item's CTAs are consecutive.
+__device__ __forceinline__ int64_t cta_of(int64_t u, int64_t W, int64_t ctas) {
+    return ((u + 1) * ctas - 1) / W;
 }
 
 __device__ __forceinline__ float ex2(float x) {

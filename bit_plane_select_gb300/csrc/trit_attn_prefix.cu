@@ -106,6 +106,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
         TRIT_W8(v, 8), TRIT_W8(v, 16), TRIT_W8(v, 24), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+            TRIT_W8(v, 0),
+        TRIT_W8(v, 8), "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -129,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kTile);
     uint64_t *empty = full + kRing;
     uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
-    uint64_t *p_full = s_full + 2;       // stream's P is
-    uint64_t *o_full = p_full + 2;       // stream's O is finished
+    uint64_t *p_full = s_full + 2;       // [stream][half]: P of the first, second 64 keys is
+    uint64_t *o_full = p_full + 4;       // stream's O is finished
     uint64_t *pv_done = o_full + 2;      // the product just issued has read its P
     uint64_t *q_full = pv_done + 1;
     uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
@@ -155,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[s], 4);
+            mbar_init(&p_full[2 * s], 4);
+            mbar_init(&p_full[2 * s + 1], 4);
             mbar_init(&o_full[s], 1);
         }
         mbar_init(pv_done, 1);
@@ -245,15 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; ok && k < 2 && k < ops; ++k) ok = issue_s(k);
             for (int k = 0; ok && k < ops; ++k) {
                 const int s = k & 1, j = pair ? k / 2 : k, at = v_at(j), st = at % kRing;
-                ok = mbar_wait(&p_full[s], (k >> 1) & 1, timed_out) &&
-                     mbar_wait(&full[st], (at / kRing) & 1, timed_out);
-                if (!ok) break;
-                tc_fence_after();
+                ok = mbar_wait(&full[st], (at / kRing) & 1, timed_out);
                 const uint32_t b = raddr + st * kTile;
 #pragma unroll
-                for (int kk = 0; kk < kBlockKeys / 16; ++kk)
-                    mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, mn_desc(b + kk * 2048), idesc_o<T, D>(),
-                           k > 1 || kk > 0);
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && mbar_wait(&p_full[2 * s + half], (k >> 1) & 1, timed_out);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, mn_desc(b + kk * 2048),
+                               idesc_o<T, D>(), k > 1 || kk > 0);
+                }
+                if (!ok) break;
                 if (!pair || s == 1) mma_commit(&empty[st]);
                 if (k + 2 >= ops) {
                     mma_commit(&o_full[s]);
@@ -303,18 +315,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int j = pair ? i : 2 * i + s;
             const int left = P - (j0 + j) * kBlockKeys;
-            uint32_t v[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + s * 128 + quarter + c * 32, v + c * 32);
-            tmem_wait_ld();
-            if (left < kBlockKeys) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (c >= left) v[c] = 0xff800000u;
-            }
+            // S is read twice, 32 columns at a time, rather than held in 128 registers
+            const uint32_t sa = tmem + s * 128 + quarter;
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t v[2][32];
+            tmem_ld32(sa, v[0]);
 #pragma unroll
-            for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_ld();
+                if (q < 3) tmem_ld32(sa + (q + 1) * 32, v[(q + 1) & 1]);
+                uint32_t(&x)[32] = v[q & 1];
+                if (left < kBlockKeys) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (q * 32 + c >= left) x[c] = 0xff800000u;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+            }
+            tmem_ld32(sa, v[0]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
             if (i == 0) {
                 m = top;
@@ -329,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t w[32];
                         tmem_ld32(tmem + 256 + s * 128 + quarter + c * 32, w);
-                        tmem_wait_ld();
+                        tmem_wait_ld();   // and the first columns of S, if still on their way
 #pragma unroll
                         for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
                         tmem_st32(tmem + 256 + s * 128 + quarter + c * 32, w);
@@ -339,22 +358,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float base = base_of(m);
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t w[32];
+            for (int q = 0; q < 4; ++q) {
+                tmem_wait_ld();
+                if (q < 3) tmem_ld32(sa + (q + 1) * 32, v[(q + 1) & 1]);
+                uint32_t(&x)[32] = v[q & 1];
+                if (left < kBlockKeys) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float e0 = ex2(fmaf(__uint_as_float(v[half * 64 + 2 * c]), scale2, -base));
-                    const float e1 = ex2(fmaf(__uint_as_float(v[half * 64 + 2 * c + 1]), scale2, -base));
+                    for (int c = 0; c < 32; ++c)
+                        if (q * 32 + c >= left) x[c] = 0xff800000u;
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float e0 = ex2(fmaf(__uint_as_float(x[2 * c]), scale2, -base));
+                    const float e1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), scale2, -base));
                     sum[c & 3] += e0 + e1;
                     w[c] = pack16<T>(e0, e1);
                 }
-                tmem_st32(tmem + s * 128 + quarter + half * 32, w);
+                // columns 16 q .. 16 q + 15 of S have been read in both passes by now
+                tmem_st16(sa + q * 16, w);
+                if (q & 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * s + (q >> 1)]);
+                }
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[s]);
         }
         float *part = A.tc_parts + ((int64_t(item) * A.tc_splits + split) * 2 + s) * part_floats(kRows, D);
         if (mine > 0 && ok) {
@@ -452,9 +482,21 @@ void prefix_layout(Args &A) {
     A.tc_tiles = int((rows + kRows - 1) / kRows);
     A.tc_groups = (A.tc_tiles + 1) / 2;
     A.tc_items = A.tc_groups * J.cache.heads;
-    int splits = kSms / A.tc_items;
-    if (splits < 1) splits = 1;
-    if (splits > nb) splits = nb;
+    // Splits by a cost model in us (measured): a CTA costs about 4 and 1.6 per block
+    // of a pair (0.8 of a single tile), the join reads and this kernel writes every part.
+    const bool single = A.tc_tiles == 1;
+    const double per_block = single ? 0.8 : 1.6;
+    const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 8 / 4e6 * (single ? 2 : 1);
+    double best = 0;
+    int splits = 0;
+    for (int s = 1; s <= nb && s * A.tc_items <= (A.tc_items > kSms ? 4 * A.tc_items : 2 * kSms); ++s) {
+        const int waves = (s * A.tc_items + kSms - 1) / kSms;
+        const double cost = waves * (4 + (nb + s - 1) / s * per_block) + s * per_split;
+        if (splits == 0 || cost < best) {
+            best = cost;
+            splits = s;
+        }
+    }
     A.tc_splits = splits;
 }
 
