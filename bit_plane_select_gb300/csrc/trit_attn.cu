@@ -80,17 +80,17 @@ __device__ __forceinline__ Place place_of(const Args &A, const int32_t *cum, int
     Place p;
     const int64_t pre = int64_t(A.J.cache.heads) * A.pre_tiles * A.pre_steps;
     if (u < pre) {
-        const int64_t item = u / A.pre_steps;
+        const int64_t item = quot(u, A.pre_steps);
         p.b = -1;
         p.step = int(u - item * A.pre_steps);
         p.steps = A.pre_steps;
-        p.h = int(item / A.pre_tiles);
+        p.h = int(item) / A.pre_tiles;
         p.tile = int(item - int64_t(p.h) * A.pre_tiles);
         return p;
     }
     const int64_t v = u - pre;
     const int items = A.J.cache.heads * A.own_tiles;
-    const int at = int(v / items);            // in steps of one item: cum[b] <= at < cum[b + 1]
+    const int at = int(quot(v, items));            // in steps of one item: cum[b] <= at < cum[b + 1]
     int lo = 0, hi = A.J.batch.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -100,7 +100,7 @@ __device__ __forceinline__ Place place_of(const Args &A, const int32_t *cum, int
     p.b = lo;
     p.steps = cum[lo + 1] - cum[lo];
     const int64_t rest = v - int64_t(cum[lo]) * items;
-    const int item = int(rest / p.steps);
+    const int item = int(quot(rest, p.steps));
     p.step = int(rest - int64_t(item) * p.steps);
     p.h = item / A.own_tiles;
     p.tile = item - p.h * A.own_tiles;
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
     const int64_t ctas = W < gridDim.x ? W : gridDim.x;      // that have a share: at least a step each
-    const int64_t lo = blockIdx.x < ctas ? W * blockIdx.x / ctas : W;
-    const int64_t hi = blockIdx.x < ctas ? W * (blockIdx.x + 1) / ctas : W;
+    const int64_t lo = blockIdx.x < ctas ? quot(W * blockIdx.x, ctas) : W;
+    const int64_t hi = blockIdx.x < ctas ? quot(W * (blockIdx.x + 1), ctas) : W;
     if (J.batch.prefix_len == 0) {   // sequences without a key are in no CTA's share
         for (int b = blockIdx.x; b < B; b += gridDim.x) {
             if (cum[b] != cum[b + 1]) continue;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     int64_t pfirst = 0;
     int prefix = 0, pitem = 0, prl = 0, pstep = 1;
     if (A.tc_items) {
-        const int ptile = int(fr / kTcRows), group = ptile >> 1;
+        const int ptile = int(fr) / kTcRows, group = ptile >> 1;
         const bool pair = 2 * group + 1 < A.tc_tiles;
         prl = int(fr - int64_t(ptile) * kTcRows);
         pfirst = int64_t(h * A.tc_groups + group) * A.tc_splits * 2 + (pair ? ptile & 1 : 0);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
         prefix = pair ? A.tc_splits : 2 * A.tc_splits;
         if (t >= batch_new(J.batch, b)) prefix = 0;        // padding: that kernel does not look
     } else if (A.pre_tiles) {
-        pitem = int(fr / RT);
+        pitem = int(fr) / RT;
         prl = int(fr - int64_t(pitem) * RT);
         const int64_t s0 = (int64_t(h) * A.pre_tiles + pitem) * A.pre_steps;
         pfirst = cta_of(s0, W, ctas);

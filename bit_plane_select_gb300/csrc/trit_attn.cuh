@@ -56,8 +56,14 @@ __host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
 
 // The CTA whose share [W c / ctas, W (c + 1) / ctas) holds step u of W; ctas <= W,
 // so that no share is empty and an item's CTAs are consecutive.
+// Quotients here are 32-bit wherever the operands are (a 64-bit division takes
+// hundreds of SM-clocks).
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
+    return a / b;
+}
 __device__ __forceinline__ int64_t cta_of(int64_t u, int64_t W, int64_t ctas) {
-    return ((u + 1) * ctas - 1) / W;
+    return quot((u + 1) * ctas - 1, W);
 }
 
 __device__ __forceinline__ float ex2(float x) {

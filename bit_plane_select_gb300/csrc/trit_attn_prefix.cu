@@ -36,8 +36,11 @@ using namespace tc;
 constexpr int kBlockKeys = 128;
 constexpr int kRows = 128;
 constexpr int kRing = 4;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;   // one issuing warp per stream: 8 and 9
+constexpr int kThreads = 384;      // 8 softmax warps, three of the roles above, an idle one
+// Registers: launched with 168 a thread; the softmax warpgroups, which hold a row of
+// S, take 216 and the third keeps 72 (256 * 216 + 128 * 72 = 384 * 168).
+constexpr int kLaunchRegs = 168;
 constexpr int kTmemCols = 512;     // S of the two streams at 0 and 128, O at 256 and 384
 constexpr float kGrow = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
@@ -60,32 +63,94 @@ __host__ __device__ constexpr uint32_t idesc_o() {
     return (1u << 4) | type_bits<T>() | (1u << 16) | ((uint32_t(D) >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// MN-major 128-byte-swizzled operand: 64 columns (128 bytes) of a key are
-// contiguous, 8 keys make an atom of 1024 bytes (the stride between key groups),
-// and the next 64 columns start a half tile later.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-    return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t((kBlockKeys * 128) >> 4) << 16) |
-           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
+// Shared-memory matrix descriptors as two words: the start address and leading
+// offset, and the stride (1024 bytes between groups of eight 128-byte rows),
+// version and 128-byte swizzle.  A step along the operand adds to the first word
+// only.  K-major (Q, K): the leading offset is unused.  MN-major (V as stored: 64
+// columns of a key contiguous, 8 keys an atom): it is the distance of the
+// next 64 columns, half a tile.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescK = 1u << 16, kDescMn = uint32_t((kBlockKeys * 128) >> 4) << 16;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return saddr >> 4; }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(acc)), "r"(kDescHi));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+        "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(acc)), "r"(kDescHi));
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                      smem_u32(bar))
                  : "memory");
+}
+
+// Waits for the phase of the given parity; false once *timed_out is set or kWaitNs
+// have passed.  The clock is read every 256 tries only: a read of it
+// takes longer than the waits here.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, uint32_t *timed_out) {
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255) == 255) {
+            if (*reinterpret_cast<volatile uint32_t *>(timed_out)) return false;
+            const unsigned long long t = global_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitNs) {
+                atomicExch(timed_out, 1u);
+                return false;
+            }
+        }
+    }
+}
+
+// Two fp32 lanes in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The same for a whole warp: one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *timed_out) {
+    return __all_sync(~0u, bar_wait(bar, parity, timed_out));
 }
 
 #define TRIT_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
@@ -105,6 +170,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::TRIT_W8(v, 0),
         TRIT_W8(v, 8), TRIT_W8(v, 16), TRIT_W8(v, 24), "r"(addr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : TRIT_R8(v, 0), TRIT_R8(v, 8)
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
     asm volatile(
@@ -138,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
     uint64_t *p_full = s_full + 2;       // [stream][half]: P of the first, second 64 keys is
     uint64_t *o_full = p_full + 4;       // stream's O is finished
-    uint64_t *pv_done = o_full + 2;      // the product just issued has read its P
-    uint64_t *q_full = pv_done + 1;
+    uint64_t *pv_done = o_full + 2;      // stream's product into O has completed
+    uint64_t *q_full = pv_done + 2;
     uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
     uint32_t *timed_out = tmem_slot + 1;
@@ -153,20 +224,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j0 = int(int64_t(nb) * split / A.tc_splits), j1 = int(int64_t(nb) * (split + 1) / A.tc_splits);
     const int n = j1 - j0;
     const bool pair = 2 * group + 1 < A.tc_tiles;     // two row tiles, or one over two streams
-    const int ops = pair ? 2 * n : n;                  // op k: stream k & 1, block pair ? k / 2 : k
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRing; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], pair ? 2 : 1);     // streams that read the tile
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[2 * s], 4);
             mbar_init(&p_full[2 * s + 1], 4);
             mbar_init(&o_full[s], 1);
+            mbar_init(&pv_done[s], 1);
         }
-        mbar_init(pv_done, 1);
         mbar_init(q_full, 8);
         mbar_init(tail, 1);
         *timed_out = 0;
@@ -188,13 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto k_at = [&](int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
     auto v_at = [&](int j) { return pair ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2); };
 
+    // every warp of a warpgroup gives up or takes the same number of registers
     if (warp == kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int ps = J.cache.page_size;
         const int rows = ps < kBlockKeys ? ps : kBlockKeys;      // keys of one copy
         const int npages = (P + ps - 1) / ps;
         auto load = [&](int j, bool is_v, int at) -> bool {
             const int s = at % kRing;
-            if (!mbar_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) return false;
+            if (!warp_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) return false;
             const int key0 = (j0 + j) * kBlockKeys;
             const int first = key0 / ps;
             int copies = kBlockKeys / rows;
@@ -213,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          key0 - first * ps, h, page, bar);
             }
             if (clear) {   // keys past the prefix get P = 0, which must not meet a NaN
-                if (!__all_sync(~0u, mbar_wait(tail, 0, timed_out))) return false;
+                if (!warp_wait(tail, 0, timed_out)) return false;
                 for (int i = lane; i < (kBlockKeys - keys) * (D / 8); i += 32) {
                     const int r = keys + i / (D / 8), c = i % (D / 8);
                     *reinterpret_cast<uint4 *>(st + (c / 8) * (kBlockKeys * 128) + r * 128 + (c % 8) * 16) =
@@ -231,75 +303,94 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (j + 1 < n) ok = load(j + 1, false, k_at(j + 1));
             ok = ok && load(j, true, v_at(j));
         }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            const uint32_t qaddr = smem_u32(qs), raddr = smem_u32(ring);
-            auto issue_s = [&](int k) -> bool {
-                const int s = k & 1, j = pair ? k / 2 : k, at = k_at(j), st = at % kRing;
-                if (!mbar_wait(&full[st], (at / kRing) & 1, timed_out)) return false;
-                tc_fence_after();
-                const uint32_t a = qaddr + (pair ? s * kTile : 0), b = raddr + st * kTile;
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // stream s: S of its first block, then per block O += P V and S of the next,
+        // which takes the place of P once that product has completed.  The whole warp
+        // walks the loop (uniform values, so the operands are in uniform registers
+        // when a product is issued); one elected lane issues.
+        const int s = warp - kMmaWarp, mine = pair ? n : (n + 1 - s) / 2;
+        const bool leader = elect_one();
+        const uint32_t qlo = (desc_lo(smem_u32(qs)) | kDescK) + (pair ? s * (kTile >> 4) : 0);
+        const uint32_t rk = desc_lo(smem_u32(ring)) | kDescK, rv = desc_lo(smem_u32(ring)) | kDescMn;
+        const uint32_t sp = tmem + s * 128, o = tmem + 256 + s * 128;
+        auto k_there = [&](int i) -> bool {
+            const int at = k_at(pair ? i : 2 * i + s);
+            return warp_wait(&full[at % kRing], (at / kRing) & 1, timed_out);
+        };
+        auto issue_s = [&](int i) {
+            const int st = k_at(pair ? i : 2 * i + s) % kRing;
+            tc_fence_after();
+            const uint32_t b = rk + st * (kTile >> 4);
+            if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * (kBlockKeys * 128) + (kk % 4) * 32;
-                    mma_ss(tmem + s * 128, sw128_desc(a + off), sw128_desc(b + off), idesc_s<T>(), kk > 0);
+                    const uint32_t off = (kk / 4) * (kBlockKeys * 128 >> 4) + (kk % 4) * 2;
+                    mma_ss(sp, qlo + off, b + off, idesc_s<T>(), kk > 0);
                 }
-                if (!pair || s == 1) mma_commit(&empty[st]);
                 mma_commit(&s_full[s]);
-                return true;
-            };
-            bool ok = mbar_wait(q_full, 0, timed_out);
-            tc_fence_after();
-            for (int k = 0; ok && k < 2 && k < ops; ++k) ok = issue_s(k);
-            for (int k = 0; ok && k < ops; ++k) {
-                const int s = k & 1, j = pair ? k / 2 : k, at = v_at(j), st = at % kRing;
-                ok = mbar_wait(&full[st], (at / kRing) & 1, timed_out);
-                const uint32_t b = raddr + st * kTile;
+                mma_commit(&empty[st]);
+            }
+            __syncwarp();
+        };
+        bool ok = warp_wait(q_full, 0, timed_out);
+        // the streams start half a block apart: in step, they would want the tensor
+        // pipe together and then the exponentials together (measured: 4100 SM-clocks a
+        // block pair in step)
+        if (s == 1) ok = ok && warp_wait(&p_full[1], 0, timed_out);
+        if (ok && mine > 0) {
+            ok = k_there(0);
+            if (ok) issue_s(0);
+        }
+        for (int i = 0; ok && i < mine; ++i) {
+            const int at = v_at(pair ? i : 2 * i + s), st = at % kRing;
+            ok = warp_wait(&full[st], (at / kRing) & 1, timed_out);
+            const uint32_t b = rv + st * (kTile >> 4);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = ok && mbar_wait(&p_full[2 * s + half], (k >> 1) & 1, timed_out);
-                    if (!ok) break;
-                    tc_fence_after();
+            for (int half = 0; half < 2; ++half) {
+                ok = ok && warp_wait(&p_full[2 * s + half], i & 1, timed_out);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, mn_desc(b + kk * 2048),
-                               idesc_o<T, D>(), k > 1 || kk > 0);
+                        mma_ts(o, sp + kk * 8, b + kk * (2048 >> 4), idesc_o<T, D>(), i > 0 || kk > 0);
                 }
-                if (!ok) break;
-                if (!pair || s == 1) mma_commit(&empty[st]);
-                if (k + 2 >= ops) {
-                    mma_commit(&o_full[s]);
-                } else {
-                    // S of the stream's next block takes the place of this P
-                    mma_commit(pv_done);
-                    ok = mbar_wait(pv_done, k & 1, timed_out) && issue_s(k + 2);
-                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            const bool last = i + 1 == mine;
+            if (leader) {
+                mma_commit(last ? &o_full[s] : &pv_done[s]);
+                mma_commit(&empty[st]);
+            }
+            __syncwarp();
+            if (!last) {
+                ok = k_there(i + 1) && warp_wait(&pv_done[s], i & 1, timed_out);
+                if (ok) issue_s(i + 1);
             }
         }
-        __syncwarp();
-    } else {
+    } else if (warp < kMmaWarp) {
         // softmax: stream s, row r of its tile (tensor-memory lane r)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
-        const int64_t rows = int64_t(J.batch.B) * A.R;
-        {   // the query tile: chunk c of row i, swizzled; the two streams' threads share a single tile
+        {   // the query tile, a row per thread (half a row where the streams share a tile)
             constexpr int CH = D / 8;
             const int tile = 2 * group + (pair ? s : 0);
             const uint32_t flip = A.scale2 < 0.0f ? 0x80008000u : 0u;   // -q, and |scale| below
             uint8_t *dst = qs + (pair ? s * kTile : 0);
-            const int step = pair ? 128 : 256, from = pair ? r : int(threadIdx.x);
-            for (int i = from; i < kRows * CH; i += step) {
-                const int row = i / CH, c = i % CH;
-                const int64_t fr = int64_t(tile) * kRows + row;
+            const int fr = tile * kRows + r, rows = J.batch.B * A.R;
+            const int b = fr / A.R, rr = fr - b * A.R, t = rr / A.G, g = rr - t * A.G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(h) * A.G + g) * D);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (!pair && (c >= CH / 2) != (s == 1)) continue;
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (fr < rows) {
-                    const int b = int(fr / A.R), rr = int(fr - int64_t(b) * A.R), t = rr / A.G, g = rr - t * A.G;
-                    v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) +
-                                                              (int64_t(b) * J.batch.T + t) * J.q_stride +
-                                                              (int64_t(h) * A.G + g) * D + c * 8));
-                    v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
-                }
-                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(row, c % 8)) = v;
+                if (fr < rows) v = __ldg(src + c);
+                v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(r, c % 8)) = v;
             }
             fence_proxy_async();
             __syncwarp();
@@ -310,30 +401,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int i = 0; i < mine; ++i) {
-            ok = __all_sync(~0u, mbar_wait(&s_full[s], i & 1, timed_out));
+            ok = warp_wait(&s_full[s], i & 1, timed_out);
             if (!ok) break;
             tc_fence_after();
             const int j = pair ? i : 2 * i + s;
             const int left = P - (j0 + j) * kBlockKeys;
-            // S is read twice, 32 columns at a time, rather than held in 128 registers
             const uint32_t sa = tmem + s * 128 + quarter;
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            uint32_t v[2][32];
-            tmem_ld32(sa, v[0]);
+            uint32_t v[128];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld();
-                if (q < 3) tmem_ld32(sa + (q + 1) * 32, v[(q + 1) & 1]);
-                uint32_t(&x)[32] = v[q & 1];
-                if (left < kBlockKeys) {
+            for (int c = 0; c < 4; ++c) tmem_ld32(sa + c * 32, v + c * 32);
+            tmem_wait_ld();
+            if (left < kBlockKeys) {
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (q * 32 + c >= left) x[c] = 0xff800000u;
-                }
-#pragma unroll
-                for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+                for (int c = 0; c < 128; ++c)
+                    if (c >= left) v[c] = 0xff800000u;
             }
-            tmem_ld32(sa, v[0]);
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+#pragma unroll
+            for (int c = 8; c < 128; c += 2)
+                mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
             if (i == 0) {
                 m = top;
@@ -345,37 +433,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (grow) m = top;
                     l *= f;
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t w[32];
-                        tmem_ld32(tmem + 256 + s * 128 + quarter + c * 32, w);
-                        tmem_wait_ld();   // and the first columns of S, if still on their way
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t w[16];
+                        tmem_ld16(tmem + 256 + s * 128 + quarter + c * 16, w);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-                        tmem_st32(tmem + 256 + s * 128 + quarter + c * 32, w);
+                        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                        tmem_st16(tmem + 256 + s * 128 + quarter + c * 16, w);
                     }
                 }
             }
             const float base = base_of(m);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t k2 = pack2(scale2, scale2), b2 = pack2(-base, -base);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld();
-                if (q < 3) tmem_ld32(sa + (q + 1) * 32, v[(q + 1) & 1]);
-                uint32_t(&x)[32] = v[q & 1];
-                if (left < kBlockKeys) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (q * 32 + c >= left) x[c] = 0xff800000u;
-                }
                 uint32_t w[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
-                    const float e0 = ex2(fmaf(__uint_as_float(x[2 * c]), scale2, -base));
-                    const float e1 = ex2(fmaf(__uint_as_float(x[2 * c + 1]), scale2, -base));
-                    sum[c & 3] += e0 + e1;
+                    const int at = q * 32 + 2 * c;
+                    const float2 t = unpack2(fma2(pack2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), k2, b2));
+                    const float e0 = ex2(t.x), e1 = ex2(t.y);
+                    sum[c & 1] = add2(sum[c & 1], pack2(e0, e1));
                     w[c] = pack16<T>(e0, e1);
                 }
-                // columns 16 q .. 16 q + 15 of S have been read in both passes by now
                 tmem_st16(sa + q * 16, w);
                 if (q & 1) {
                     tmem_wait_st();
@@ -384,11 +465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&p_full[2 * s + (q >> 1)]);
                 }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 t = unpack2(add2(sum[0], sum[1]));
+            l += t.x + t.y;
         }
         float *part = A.tc_parts + ((int64_t(item) * A.tc_splits + split) * 2 + s) * part_floats(kRows, D);
         if (mine > 0 && ok) {
-            ok = __all_sync(~0u, mbar_wait(&o_full[s], 0, timed_out));
+            ok = warp_wait(&o_full[s], 0, timed_out);
             tc_fence_after();
             if (ok) {
 #pragma unroll
@@ -404,6 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m, l);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
     tc_fence_before();
     __syncthreads();
@@ -456,6 +540,11 @@ cudaError_t launch(const Args &A, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(smem_bytes<D>()));
     if (e != cudaSuccess) return e;
+    // the register split draws on what the launch allocates: never start it with less
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, prefix_kernel<T, D>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
     prefix_kernel<T, D><<<A.tc_items * A.tc_splits, kThreads, smem_bytes<D>(), s>>>(A, kmap, vmap);
     return cudaGetLastError();
 }
