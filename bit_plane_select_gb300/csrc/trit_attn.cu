@@ -1,7 +1,7 @@
 // trit_attn_paged: out = softmax(scale q K^T) V over a paged cache, the shared
 // prefix read once for the batch.
 //
-// The keys of every item (trit_attn.cuh) are cut into steps of 64, all steps of
+// The keys of every item (trit_attn.cuh) are cut into steps of 64 (128 where D = 64), all steps of
 // the call are laid end to end, and each of a fixed grid of CTAs takes an equal
 // run of them, whatever the lengths (which only the device knows): a CTA's run
 // may end one item, cover several and begin another.  Items a CTA does not
@@ -10,8 +10,8 @@
 // part belongs to many sequences).
 //
 // Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
-// reading K and V: 4 D bytes a key against 4 D R flops.  A step's 64 keys go 16
-// to a warp; every warp has its own ring of three stages of 16 keys (K and V),
+// reading K and V: 4 D bytes a key against 4 D R flops.  A step's keys go 16
+// (32 where D = 64) to a warp; every warp has its own ring of three such stages of K and V,
 // filled by 16-byte asynchronous copies two stages ahead, so warps never wait
 // for one another inside an item.  S = Q K^T and O += P V are 16-bit
 // mma.sync with fp32 sums (the rows fill one or two m16 tiles); the rows' m and
@@ -27,9 +27,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kKeys = kStep / kWarps;   // keys of a warp's stage: 16
+// Keys of a warp's stage: 8 KB of K and V either way (measured against 16 keys
+// for D = 64 too, where a stage's fixed work then outweighs its products).
+__host__ __device__ constexpr int keys_of_stage(int D) { return D == 64 ? 32 : 16; }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -107,19 +111,39 @@ __device__ __forceinline__ Place place_of(const Args &A, const int32_t *cum, int
     return p;
 }
 
+// What a CTA keeps of the batch in shared memory.
+struct Batch {
+    int32_t *cum;     // [B + 1] steps of the sequences before b
+    int32_t *len;     // [B] own lengths, clamped
+    int32_t *fresh;   // [B] valid new tokens
+};
+
+// The place of the step after p's last one.
+__device__ __forceinline__ void next_item(const Args &A, const Batch &S, Place &p) {
+    p.step = 0;
+    const int tiles = p.b < 0 ? A.pre_tiles : A.own_tiles;
+    if (++p.tile < tiles) return;
+    p.tile = 0;
+    if (++p.h < A.J.cache.heads) return;
+    p.h = 0;
+    do ++p.b;
+    while (S.cum[p.b + 1] == S.cum[p.b]);
+    p.steps = S.cum[p.b + 1] - S.cum[p.b];
+}
+
 // The keys of a place: their page table and how many there are.
 struct Keys {
     const int32_t *table;
     int n;
 };
-__device__ __forceinline__ Keys keys_of(const Args &A, const Place &p) {
+__device__ __forceinline__ Keys keys_of(const Args &A, const Batch &S, const Place &p) {
     Keys k;
     if (p.b < 0) {
         k.table = A.J.batch.prefix_table;
         k.n = int(A.J.batch.prefix_len);
     } else {
         k.table = A.J.batch.table + p.b * A.J.batch.table_stride;
-        k.n = clamped_len(A, p.b, false);
+        k.n = S.len[p.b];
     }
     return k;
 }
@@ -132,53 +156,96 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
     return uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
 }
 
+// The pages of a stage's keys, 16 by 16, read one stage ahead of their use: the
+// table's latency would otherwise stand before every stage's copies.
 template <int D>
-struct Loader {
-    // Issues the copies of keys [key0, key0 + 16) of head h; rows past the end,
-    // and rows of pages outside the cache, are filled with zeros.
-    static __device__ __forceinline__ void issue(const Args &A, const Keys &K, int h, int key0, uint8_t *stage,
-                                                 int lane) {
-        constexpr int CH = D / 8;            // chunks of a row
-        constexpr int RI = 32 / CH;          // rows of one copy instruction
-        const trit_kv_cache &C = A.J.cache;
-        const int c = lane % CH, r0 = lane / CH;
-        const uint16_t *kb = static_cast<const uint16_t *>(C.k) + h * C.head_stride + c * 8;
-        const uint16_t *vb = static_cast<const uint16_t *>(C.v) + h * C.head_stride + c * 8;
-        int64_t at = 0;
-        bool one_page = (C.page_size & 15) == 0, good = false;
-        if (one_page && key0 < K.n) {
-            const int col = A.page_shift >= 0 ? key0 >> A.page_shift : key0 / C.page_size;
-            const int page = __ldg(K.table + col);
-            good = page >= 0 && page < C.pages;
-            if (!good) raise_flag(A.err, TRIT_ERR_INDEX);
-            at = page * C.page_stride + int64_t(key0 - col * C.page_size) * C.slot_stride;
-        }
-#pragma unroll
-        for (int j = 0; j < kKeys / RI; ++j) {
-            const int r = r0 + j * RI, key = key0 + r;
-            int64_t off = at + r * C.slot_stride;
-            bool ok = good && key < K.n;
-            if (!one_page && key < K.n) {
-                const int col = key / C.page_size;
-                const int page = __ldg(K.table + col);
-                ok = page >= 0 && page < C.pages;
-                if (!ok) raise_flag(A.err, TRIT_ERR_INDEX);
-                off = page * C.page_stride + int64_t(key - col * C.page_size) * C.slot_stride;
-            }
-            if (!ok) off = 0;
-            tc::cp_async16(stage + chunk_at<D>(r, c), kb + off, ok ? 16u : 0u);
-            tc::cp_async16(stage + kKeys * D * 2 + chunk_at<D>(r, c), vb + off, ok ? 16u : 0u);
-        }
-    }
+struct Pages {
+    int id[keys_of_stage(D) / 16];
 };
+template <int D>
+__device__ __forceinline__ Pages<D> pages_of(const Args &A, const Keys &K, int key0) {
+    Pages<D> P;
+    const trit_kv_cache &C = A.J.cache;
+#pragma unroll
+    for (int p = 0; p < keys_of_stage(D) / 16; ++p) {
+        const int k = key0 + p * 16;
+        const int col = A.page_shift >= 0 ? k >> A.page_shift : k / C.page_size;
+        P.id[p] = k < K.n ? __ldg(K.table + col) : -1;
+    }
+    return P;
+}
+
+// Issues the copies of keys [key0, key0 + KW) of head h.  Rows past the end, and
+// rows of pages outside the cache, are filled with zeros.
+template <int D>
+__device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const Pages<D> &P, int h, int key0,
+                                           uint32_t stage, int lane) {
+    constexpr int KW = keys_of_stage(D);
+    constexpr int CH = D / 8;            // chunks of a row
+    constexpr int RI = 32 / CH;          // rows of one copy instruction
+    constexpr uint32_t VAT = KW * D * 2;
+    const trit_kv_cache &C = A.J.cache;
+    const int c = lane % CH, r0 = lane / CH;
+    // row r0 + j RI: r0 < RI, so its swizzled chunk is (c ^ r0) ^ (j RI & 7)
+    const uint32_t dst = stage + r0 * D * 2, x = uint32_t(c ^ r0) << 4;
+    const char *kb = static_cast<const char *>(C.k) + 2 * (h * C.head_stride + c * 8);
+    const int64_t to_v = static_cast<const char *>(C.v) - static_cast<const char *>(C.k);
+    const int n = K.n;
+    if ((C.page_size & 15) == 0) {
+        constexpr int PJ = 16 / RI;      // copy instructions of 16 keys, which lie in one page
+        const int64_t hop = int64_t(RI) * 2 * C.slot_stride;
+#pragma unroll
+        for (int p = 0; p < KW / 16; ++p) {
+            const int k0 = key0 + p * 16;
+            const int slot = A.page_shift >= 0 ? k0 & (C.page_size - 1) : k0 % C.page_size;
+            const int page = P.id[p];
+            const bool good = page >= 0 && page < C.pages;
+            if (!good && k0 < n) raise_flag(A.err, TRIT_ERR_INDEX);
+            const int live = good ? n - k0 : 0;          // rows of the 16 that are there
+            const char *src = kb + (good ? 2 * (page * C.page_stride + int64_t(slot + r0) * C.slot_stride) : 0);
+#pragma unroll
+            for (int j = 0; j < PJ; ++j) {
+                const int jj = p * PJ + j;
+                const uint32_t to = dst + jj * RI * D * 2 + (x ^ uint32_t(((jj * RI) & 7) << 4));
+                const bool ok = r0 + j * RI < live;
+                const char *at = ok ? src + j * hop : kb;
+                cp_async16(to, at, ok);
+                cp_async16(to + VAT, at + to_v, ok);
+            }
+        }
+        return;
+    }
+#pragma unroll 4
+    for (int j = 0; j < KW / RI; ++j) {
+        const int key = key0 + r0 + j * RI;
+        const uint32_t to = dst + j * RI * D * 2 + (x ^ uint32_t(((j * RI) & 7) << 4));
+        bool ok = key < n;
+        const char *at = kb;
+        if (ok) {
+            const int col = key / C.page_size;
+            const int page = __ldg(K.table + col);
+            ok = page >= 0 && page < C.pages;
+            if (ok) at += 2 * (page * C.page_stride + int64_t(key - col * C.page_size) * C.slot_stride);
+            else raise_flag(A.err, TRIT_ERR_INDEX);
+        }
+        cp_async16(to, at, ok);
+        cp_async16(to + VAT, at + to_v, ok);
+    }
+}
 
 // Exclusive prefix sums of the sequences' steps into cum[0..B] (shared memory).
-__device__ __forceinline__ void count_steps(const Args &A, int32_t *cum, int32_t *scratch, bool report) {
+template <int kStep>
+__device__ __forceinline__ void count_steps(const Args &A, const Batch &S, int32_t *scratch, bool report) {
     const int B = A.J.batch.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < B; i += kThreads) {
+        S.len[i] = clamped_len(A, i, report);
+        S.fresh[i] = batch_new(A.J.batch, i);
+    }
+    __syncthreads();
     const int per = (B + kThreads - 1) / kThreads, from = tid * per;
     int sum = 0;
     for (int i = 0; i < per; ++i)
-        if (from + i < B) sum += (clamped_len(A, from + i, report) + kStep - 1) / kStep;
+        if (from + i < B) sum += (S.len[from + i] + kStep - 1) / kStep;
     int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -191,9 +258,9 @@ __device__ __forceinline__ void count_steps(const Args &A, int32_t *cum, int32_t
     for (int w = 0; w < warp; ++w) before += scratch[w];
     for (int i = 0; i < per; ++i)
         if (from + i < B) {
-            cum[from + i] = before;
-            before += (clamped_len(A, from + i, false) + kStep - 1) / kStep;
-            if (from + i == B - 1) cum[B] = before;
+            S.cum[from + i] = before;
+            before += (S.len[from + i] + kStep - 1) / kStep;
+            if (from + i == B - 1) S.cum[B] = before;
         }
     __syncthreads();
 }
@@ -207,21 +274,34 @@ __device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float 
     v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
 }
 
+// Stages and CTAs per SM: three CTAs of two-stage rings where the registers allow
+// (D = 64, one m16 tile: 51 against 55 us for 96 sequences of about 650 keys), else two
+// of three stages (D = 128 in 168 registers spills: 130 against 105 us for two long sequences).
+__host__ __device__ constexpr bool small_state(int D, int MT) { return D == 64 && MT == 1; }
+__host__ __device__ constexpr int stages_of(int D, int MT) { return small_state(D, MT) ? 2 : 3; }
+__host__ __device__ constexpr int ctas_of(int D, int MT) { return small_state(D, MT) ? 3 : 2; }
+
 template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int RT = 16 * MT;
-    constexpr int kStageBytes = 2 * kKeys * D * 2;
-    static_assert(kStageBytes == 16 * D * 4, "a stage holds one m16 tile of fp32 sums");
+    constexpr int RT = 16 * MT, kStages = stages_of(D, MT);
+    constexpr int KW = keys_of_stage(D), NT = KW / 8, kStep = KW * kWarps;
+    constexpr int kStageBytes = 2 * KW * D * 2;
+    static_assert(kStageBytes >= 16 * D * 4, "a stage holds one m16 tile of fp32 sums");
     const trit_attn_job &J = A.J;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * kStages * kStageBytes;
+    const uint32_t ring_at = tc::smem_u32(ring);
     float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);   // [kWarps][RT] (m, l)
     int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
-    int32_t *cum = scratch + kWarps;
+    Batch S;
+    S.cum = scratch + kWarps;
+    S.len = S.cum + A.J.batch.B + 1;
+    S.fresh = S.len + A.J.batch.B;
+    const int32_t *cum = S.cum;
 
     pdl_launch();
-    count_steps(A, cum, scratch, blockIdx.x == 0);
+    count_steps<kStep>(A, S, scratch, blockIdx.x == 0);
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
@@ -248,15 +328,26 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     // the ring runs ahead of the products, across items
     int64_t lu = lo;
     Place lp = place_of(A, cum, lo);
-    Keys lk = keys_of(A, lp);
+    Keys lk = keys_of(A, S, lp);
+    Pages<D> lpages = pages_of<D>(A, lk, lp.step * kStep + warp * KW);
     auto load_next = [&](int stage) {
         if (lu < hi) {
-            Loader<D>::issue(A, lk, lp.h, lp.step * kStep + warp * kKeys, ring + stage * kStageBytes, lane);
+            load_stage<D>(A, lk, lpages, lp.h, lp.step * kStep + warp * KW, ring_at + stage * kStageBytes, lane);
             if (++lu < hi) {
                 if (++lp.step == lp.steps) {
-                    lp = place_of(A, cum, lu);
-                    lk = keys_of(A, lp);
+                    next_item(A, S, lp);
+                    lk = keys_of(A, S, lp);
+                    // its queries: into L1 by the time the products get there
+                    const int row = lp.tile * RT + (lane >> 1), rows = lp.b < 0 ? B * A.R : A.R;
+                    if (warp == 0 && row < rows) {
+                        const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
+                        const int t = r / G;
+                        const T *q = static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride +
+                                     (int64_t(lp.h) * G + r - t * G) * D + (lane & 1) * (D / 2);
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+                    }
                 }
+                lpages = pages_of<D>(A, lk, lp.step * kStep + warp * KW);
             }
         }
         tc::cp_async_commit();
@@ -325,19 +416,22 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2];
     int lim[MT][2];
-    Place p = lp;
-    int nkeys = 0, mts = 1, first_step = 0;
+    Place p = place_of(A, cum, lo);
+    int nkeys = 0, mts = 1, first_step = 0, clear = 0;   // no row's limit lies below `clear`
+    bool upper = false;                                  // rows 8.. of a lone m16 tile exist
     int64_t u = lo;
     bool fresh = true;
     int stage = 0;
     while (u < hi) {
         if (fresh) {
             fresh = false;
-            p = place_of(A, cum, u);
+            if (u != lo) next_item(A, S, p);
             first_step = p.step;
-            nkeys = keys_of(A, p).n;
+            nkeys = keys_of(A, S, p).n;
             const int rows = p.b < 0 ? B * A.R : A.R;
             mts = MT == 1 || rows - p.tile * RT <= 16 ? 1 : 2;
+            upper = rows - p.tile * RT > 8;
+            clear = nkeys;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -352,27 +446,27 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
                     bool ok = row < rows;
                     int n = 0;
                     if (ok) {
-                        n = batch_new(J.batch, b);
+                        n = S.fresh[b];
                         ok = t < n;
                     }
-                    lim[mt][i] = 0;
-                    if (ok) {
-                        lim[mt][i] = nkeys;
-                        if (p.b >= 0) {
-                            const int see = nkeys - n + t + 1;
-                            lim[mt][i] = see < 0 ? 0 : see;
-                        }
+                    lim[mt][i] = ok || row >= rows ? nkeys : 0;    // rows that are not there: never looked at
+                    if (ok && p.b >= 0) {
+                        const int see = nkeys - n + t + 1;
+                        lim[mt][i] = see < 0 ? 0 : see;
                     }
+                    clear = min(clear, lim[mt][i]);
                     m[mt][i] = -INFINITY;
                     l[mt][i] = 0.0f;
                     const T *q = static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride +
                                  (int64_t(p.h) * G + g) * D + 2 * (lane & 3);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        qf[mt][ks][i] = ok ? __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16)) : 0u;
-                        qf[mt][ks][2 + i] = ok ? __ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 8)) : 0u;
+                        qf[mt][ks][i] = ok ? (__ldg(reinterpret_cast<const uint32_t *>(q + ks * 16)) & A.keep) ^ A.flip : 0u;
+                        qf[mt][ks][2 + i] = ok ? (__ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 8)) & A.keep) ^ A.flip : 0u;
                     }
                 }
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) clear = min(clear, __shfl_xor_sync(~0u, clear, q));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -381,55 +475,64 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
 
         tc::cp_async_wait<kStages - 1>();
         __syncwarp();
-        const int key0 = p.step * kStep + warp * kKeys;
+        const int key0 = p.step * kStep + warp * KW;
         uint8_t *st = ring + stage * kStageBytes;
         if (key0 < nkeys) {
-            const uint32_t kaddr = tc::smem_u32(st), vaddr = kaddr + kKeys * D * 2;
-            float s[MT][2][4];
+            const uint32_t kaddr = ring_at + stage * kStageBytes, vaddr = kaddr + KW * D * 2;
+            float s[MT][NT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
+                for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
             const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t kf[4];
-                ldsm4(kf, kaddr + chunk_at<D>(krow, 2 * ks + kch));
+            for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    if (mt < mts) {
-                        mma16816<T>(s[mt][0], qf[mt][ks], kf[0], kf[1]);
-                        mma16816<T>(s[mt][1], qf[mt][ks], kf[2], kf[3]);
-                    }
-            }
-            uint32_t pf[MT][4];
+                for (int n2 = 0; n2 < NT / 2; ++n2) {
+                    uint32_t kf[4];
+                    ldsm4(kf, kaddr + chunk_at<D>(n2 * 16 + krow, 2 * ks + kch));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        if (mt < mts) {
+                            mma16816<T>(s[mt][2 * n2], qf[mt][ks], kf[0], kf[1]);
+                            mma16816<T>(s[mt][2 * n2 + 1], qf[mt][ks], kf[2], kf[3]);
+                        }
+                }
+            uint32_t pf[MT][NT / 2][4];
+            const bool masked = key0 + KW > clear;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 if (mt < mts) {
-                    float alpha[2];
+                    float alpha[2] = {1.0f, 1.0f};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float mx = -INFINITY;
+                        if (MT == 1 && i == 1 && !upper) {
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                            for (int n = 0; n < NT; ++n) pf[mt][n >> 1][2 * (n & 1) + 1] = 0u;
+                            break;
+                        }
+                        if (masked) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = key0 + n * 8 + 2 * (lane & 3) + e;
-                                float &v = s[mt][n][2 * i + e];
-                                v = key < lim[mt][i] ? v * A.scale2 : -INFINITY;
-                                mx = fmaxf(mx, v);
-                            }
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (key0 + n * 8 + 2 * (lane & 3) + e >= lim[mt][i]) s[mt][n][2 * i + e] = -INFINITY;
+                        }
+                        float mx = fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]);
+#pragma unroll
+                        for (int n = 1; n < NT; ++n) mx = max3(mx, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
                         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                        const float top = fmaxf(m[mt][i], mx), base = base_of(top);
+                        const float top = fmaxf(m[mt][i], mx * A.scale2), base = base_of(top);
                         alpha[i] = ex2(m[mt][i] - base);
                         m[mt][i] = top;
                         float sum = 0.0f;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const float e0 = ex2(s[mt][n][2 * i] - base), e1 = ex2(s[mt][n][2 * i + 1] - base);
+                        for (int n = 0; n < NT; ++n) {
+                            const float e0 = ex2(fmaf(s[mt][n][2 * i], A.scale2, -base));
+                            const float e1 = ex2(fmaf(s[mt][n][2 * i + 1], A.scale2, -base));
                             sum += e0 + e1;
-                            pf[mt][2 * n + i] = pack16<T>(e0, e1);
+                            pf[mt][n >> 1][2 * (n & 1) + i] = pack16<T>(e0, e1);
                         }
                         l[mt][i] = l[mt][i] * alpha[i] + sum;
                     }
@@ -445,16 +548,18 @@ __global__ void __launch_bounds__(kThreads, D == 64 && MT == 1 ? 4 : 2) attn_ker
                 }
             const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
 #pragma unroll
-            for (int dn = 0; dn < D / 16; ++dn) {
-                uint32_t vf[4];
-                ldsm4t(vf, vaddr + chunk_at<D>(vrow, 2 * dn + vch));
+            for (int k2 = 0; k2 < NT / 2; ++k2)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    if (mt < mts) {
-                        mma16816<T>(o[mt][2 * dn], pf[mt], vf[0], vf[1]);
-                        mma16816<T>(o[mt][2 * dn + 1], pf[mt], vf[2], vf[3]);
-                    }
-            }
+                for (int dn = 0; dn < D / 16; ++dn) {
+                    uint32_t vf[4];
+                    ldsm4t(vf, vaddr + chunk_at<D>(k2 * 16 + vrow, 2 * dn + vch));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+                        if (mt < mts) {
+                            mma16816<T>(o[mt][2 * dn], pf[mt][k2], vf[0], vf[1]);
+                            mma16816<T>(o[mt][2 * dn + 1], pf[mt][k2], vf[2], vf[3]);
+                        }
+                }
         }
         __syncwarp();   // every lane has read the stage
 
@@ -664,6 +769,7 @@ Args layout(const trit_attn_job &J) {
     A.RT = A.R > 16 || pre_rows > 16 ? 32 : 16;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
+    const int kStep = kWarps * keys_of_stage(J.cache.head_dim);
     A.pre_steps = on_tc ? 0 : int((J.batch.prefix_len + kStep - 1) / kStep);
     A.page_shift = -1;
     for (int s = 0; s < 31; ++s)
@@ -671,7 +777,7 @@ Args layout(const trit_attn_job &J) {
     const int64_t cap = (int64_t(J.batch.table_pages) * J.cache.page_size + kStep - 1) / kStep;
     const int64_t most = int64_t(J.cache.heads) * (int64_t(A.pre_tiles) * A.pre_steps +
                                                    int64_t(J.batch.B) * A.own_tiles * cap);
-    const int64_t grid = int64_t(kSms) * (J.cache.head_dim == 64 && A.RT == 16 ? 4 : 2);
+    const int64_t grid = int64_t(kSms) * ctas_of(J.cache.head_dim, A.RT / 16);
     A.grid = int(most < grid ? most : grid);
     return A;
 }
@@ -692,9 +798,9 @@ int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_
 
 template <typename T, int D, int MT>
 cudaError_t launch(const Args &A, cudaStream_t s) {
-    const size_t smem = size_t(kWarps) * kStages * (2 * kKeys * D * 2) + kWarps * 16 * MT * 8 + kWarps * 4 +
-                        (size_t(A.J.batch.B) + 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+    const size_t smem = size_t(kWarps) * stages_of(D, MT) * (2 * keys_of_stage(D) * D * 2) + kWarps * 16 * MT * 8 + kWarps * 4 +
+                        (size_t(A.J.batch.B) * 3 + 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     if (A.tc_items) {
         // the prefix kernel first; this one depends on nothing of it and may start beside it
@@ -725,7 +831,11 @@ int64_t attn_workspace_bytes(const trit_attn_job &J) { return attn::bytes_of(att
 cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_t s) {
     attn::Args A = attn::layout(J);
     A.err = err;
-    A.scale2 = J.scale * 1.4426950408889634f;
+    // scores are q k |scale| log2(e), with the sign of a negative scale moved into q; a
+    // scale of 0 (masked scores of -inf must not meet it) is zeros for q and 1
+    A.scale2 = J.scale == 0.0f ? 1.0f : fabsf(J.scale) * 1.4426950408889634f;
+    A.flip = J.scale < 0.0f ? 0x80008000u : 0u;
+    A.keep = J.scale == 0.0f ? 0u : 0xffffffffu;
     A.cum = static_cast<int32_t *>(J.workspace);
     uint8_t *ws = static_cast<uint8_t *>(J.workspace);
     A.count = reinterpret_cast<uint32_t *>(ws + attn::cum_bytes(J));

@@ -14,7 +14,6 @@ namespace trit {
 namespace attn {
 
 constexpr int kSms = 152;           // the grids are cut for this many
-constexpr int kStep = 64;          // keys of one step of a CTA
 constexpr int kTcRows = 128;       // rows of a tile of the tensor-core prefix kernel
 
 // Rows: row r = t*G + g of a (sequence, key head) pair is token t and query
@@ -24,7 +23,8 @@ constexpr int kTcRows = 128;       // rows of a tile of the tensor-core prefix k
 struct Args {
     trit_attn_job J;
     uint32_t *err;
-    float scale2;            // scale * log2(e)
+    float scale2;            // |scale| log2(e) (1 where scale is 0)
+    uint32_t flip, keep;     // on pairs of q: the sign of scale, and 0 where it is 0
     int32_t G, R;            // query heads per key head; rows per (sequence, key head)
     int32_t RT;              // rows of an item
     int32_t own_tiles;       // row tiles per (sequence, key head)
@@ -70,6 +70,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // 2^x is taken against this base: -inf (a row that has seen no key) must not

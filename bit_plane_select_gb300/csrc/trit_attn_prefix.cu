@@ -142,12 +142,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // The same for a whole warp: one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *timed_out) {
     return __all_sync(~0u, bar_wait(bar, parity, timed_out));
@@ -337,7 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the streams start half a block apart: in step, they would want the tensor
         // pipe together and then the exponentials together (measured: 4100 SM-clocks a
         // block pair in step)
-        if (s == 1) ok = ok && warp_wait(&p_full[1], 0, timed_out);
+        if (s == 1) {
+            ok = ok && warp_wait(&p_full[1], 0, timed_out);
+            if (n >= 8) ok = ok && warp_wait(&p_full[0], 1, timed_out);
+        }
         if (ok && mine > 0) {
             ok = k_there(0);
             if (ok) issue_s(0);
@@ -378,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         {   // the query tile, a row per thread (half a row where the streams share a tile)
             constexpr int CH = D / 8;
             const int tile = 2 * group + (pair ? s : 0);
-            const uint32_t flip = A.scale2 < 0.0f ? 0x80008000u : 0u;   // -q, and |scale| below
             uint8_t *dst = qs + (pair ? s * kTile : 0);
             const int fr = tile * kRows + r, rows = J.batch.B * A.R;
             const int b = fr / A.R, rr = fr - b * A.R, t = rr / A.G, g = rr - t * A.G;
@@ -389,14 +385,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!pair && (c >= CH / 2) != (s == 1)) continue;
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (fr < rows) v = __ldg(src + c);
-                v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+                v.x = (v.x & A.keep) ^ A.flip; v.y = (v.y & A.keep) ^ A.flip;
+                v.z = (v.z & A.keep) ^ A.flip; v.w = (v.w & A.keep) ^ A.flip;
                 *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(r, c % 8)) = v;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
-        const float scale2 = fabsf(A.scale2);
+        const float scale2 = A.scale2;
         const int mine = pair ? n : (n + 1 - s) / 2;       // this stream's blocks
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
@@ -560,8 +557,7 @@ bool prefix_on_tensor_cores(const trit_attn_job &J) {
     const bool strides = C.slot_stride >= C.head_dim && (C.heads == 1 || C.head_stride >= C.head_dim) &&
                          (C.pages == 1 || C.page_stride >= C.head_dim) && C.slot_stride < most &&
                          C.head_stride < most && C.page_stride < most;
-    // a scale of 0 would meet the -inf of masked columns there
-    return J.batch.prefix_len > 0 && J.scale != 0.0f && rows > 32 && pow2 && C.page_size >= 16 && strides;
+    return J.batch.prefix_len > 0 && rows > 32 && pow2 && C.page_size >= 16 && strides;
 }
 
 void prefix_layout(Args &A) {
