@@ -18,6 +18,8 @@
 // l live in registers and O is only rescaled when a maximum moved.
 // P is rounded to the cache's 16-bit type for the second product: relative
 // 2^-9 (bf16) or 2^-12 (fp16) of each term on average, the size of the output's own rounding.
+#include <type_traits>
+
 #include "trit_attn.cuh"
 #include "trit_tc.cuh"
 
@@ -27,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr size_t kSmemPerSm = 228 * 1024;   // 1 KB of it is taken by every CTA
 // Keys of a warp's stage: 8 KB of K and V either way (measured against 16 keys
 // for D = 64 too, where a stage's fixed work then outweighs its products).
 __host__ __device__ constexpr int keys_of_stage(int D) { return D == 64 ? 32 : 16; }
@@ -156,29 +159,27 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
     return uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
 }
 
-// The pages of a stage's keys, 16 by 16, read one stage ahead of their use: the
-// table's latency would otherwise stand before every stage's copies.
-template <int D>
+// The pages of the coming stages' keys, 16 keys by lane, read ahead of their use:
+// the table's latency would otherwise stand before every stage's copies.
 struct Pages {
-    int id[keys_of_stage(D) / 16];
+    int id;      // lane i: the page of 16-key group i of the warp's stages from `from` on
+    int from;
 };
 template <int D>
-__device__ __forceinline__ Pages<D> pages_of(const Args &A, const Keys &K, int key0) {
-    Pages<D> P;
-    const trit_kv_cache &C = A.J.cache;
-#pragma unroll
-    for (int p = 0; p < keys_of_stage(D) / 16; ++p) {
-        const int k = key0 + p * 16;
-        const int col = A.page_shift >= 0 ? k >> A.page_shift : k / C.page_size;
-        P.id[p] = k < K.n ? __ldg(K.table + col) : -1;
-    }
+__device__ __forceinline__ Pages pages_of(const Args &A, const Keys &K, int step, int warp, int lane) {
+    constexpr int KW = keys_of_stage(D), PP = KW / 16;
+    Pages P;
+    P.from = step;
+    const int k = (step + lane / PP) * (KW * kWarps) + warp * KW + (lane % PP) * 16;
+    const int col = A.page_shift >= 0 ? k >> A.page_shift : k / A.J.cache.page_size;
+    P.id = k >= 0 && k < K.n ? __ldg(K.table + col) : -1;
     return P;
 }
 
 // Issues the copies of keys [key0, key0 + KW) of head h.  Rows past the end, and
 // rows of pages outside the cache, are filled with zeros.
 template <int D>
-__device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const Pages<D> &P, int h, int key0,
+__device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const Pages &P, int h, int step, int warp,
                                            uint32_t stage, int lane) {
     constexpr int KW = keys_of_stage(D);
     constexpr int CH = D / 8;            // chunks of a row
@@ -190,7 +191,7 @@ __device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const P
     const uint32_t dst = stage + r0 * D * 2, x = uint32_t(c ^ r0) << 4;
     const char *kb = static_cast<const char *>(C.k) + 2 * (h * C.head_stride + c * 8);
     const int64_t to_v = static_cast<const char *>(C.v) - static_cast<const char *>(C.k);
-    const int n = K.n;
+    const int n = K.n, key0 = step * KW * kWarps + warp * KW;
     if ((C.page_size & 15) == 0) {
         constexpr int PJ = 16 / RI;      // copy instructions of 16 keys, which lie in one page
         const int64_t hop = int64_t(RI) * 2 * C.slot_stride;
@@ -198,7 +199,7 @@ __device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const P
         for (int p = 0; p < KW / 16; ++p) {
             const int k0 = key0 + p * 16;
             const int slot = A.page_shift >= 0 ? k0 & (C.page_size - 1) : k0 % C.page_size;
-            const int page = P.id[p];
+            const int page = __shfl_sync(~0u, P.id, (step - P.from) * (KW / 16) + p);
             const bool good = page >= 0 && page < C.pages;
             if (!good && k0 < n) raise_flag(A.err, TRIT_ERR_INDEX);
             const int live = good ? n - k0 : 0;          // rows of the 16 that are there
@@ -274,12 +275,9 @@ __device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float 
     v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
 }
 
-// Stages and CTAs per SM: three CTAs of two-stage rings where the registers allow
-// (D = 64, one m16 tile: 51 against 55 us for 96 sequences of about 650 keys), else two
-// of three stages (D = 128 in 168 registers spills: 130 against 105 us for two long sequences).
-__host__ __device__ constexpr bool small_state(int D, int MT) { return D == 64 && MT == 1; }
-__host__ __device__ constexpr int stages_of(int D, int MT) { return small_state(D, MT) ? 2 : 3; }
-__host__ __device__ constexpr int ctas_of(int D, int MT) { return small_state(D, MT) ? 3 : 2; }
+// Stages and CTAs per SM.
+__host__ __device__ constexpr int stages_of(int D, int MT) { return 2; }
+__host__ __device__ constexpr int ctas_of(int D, int MT) { return MT == 1 ? 3 : 2; }
 
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __grid_constant__ Args A) {
@@ -287,12 +285,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
     constexpr int RT = 16 * MT, kStages = stages_of(D, MT);
     constexpr int KW = keys_of_stage(D), NT = KW / 8, kStep = KW * kWarps;
     constexpr int kStageBytes = 2 * KW * D * 2;
+    constexpr int kQueries = kStages + 1;     // query tiles: the loads run at most kStages items ahead
     static_assert(kStageBytes >= 16 * D * 4, "a stage holds one m16 tile of fp32 sums");
     const trit_attn_job &J = A.J;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * kStages * kStageBytes;
     const uint32_t ring_at = tc::smem_u32(ring);
-    float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes);   // [kWarps][RT] (m, l)
+    const uint32_t q_at = tc::smem_u32(smem + kWarps * kStages * kStageBytes), q_bytes = A.q_rows * D * 2;
+    float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes + kQueries * q_bytes);   // [kWarps][RT] (m, l)
     int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
     Batch S;
     S.cum = scratch + kWarps;
@@ -300,17 +300,74 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
     S.fresh = S.len + A.J.batch.B;
     const int32_t *cum = S.cum;
 
+    // after the prefix kernel nothing is left to wait for until the end
+    if (!A.tc_items) pdl_wait();
     pdl_launch();
     count_steps<kStep>(A, S, scratch, blockIdx.x == 0);
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
     const int64_t ctas = W < gridDim.x ? W : gridDim.x;      // that have a share: at least a step each
     const int64_t lo = blockIdx.x < ctas ? quot(W * blockIdx.x, ctas) : W;
     const int64_t hi = blockIdx.x < ctas ? quot(W * (blockIdx.x + 1), ctas) : W;
-    if (J.batch.prefix_len == 0) {   // sequences without a key are in no CTA's share
+
+    // the ring runs ahead of the products, across items: keys and values by stage, and
+    // an item's queries with its first stage (each warp a quarter of the rows)
+    int64_t lu = lo;
+    Place lp = {};
+    Keys lk = {};
+    Pages lpages = {};
+    int lq = 0;
+    bool lnew = true;
+    if (lo < hi) {
+        lp = place_of(A, cum, lo);
+        lk = keys_of(A, S, lp);
+        lpages = pages_of<D>(A, lk, lp.step, warp, lane);
+    }
+    Place p = lp;
+    auto load_queries = [&]() {
+        constexpr int CH = D / 8, RI = 32 / CH;
+        const int rows = lp.b < 0 ? B * A.R : A.R, c = lane % CH;
+#pragma unroll
+        for (int j = 0; j < RT / kWarps / RI; ++j) {
+            const int rl = warp * (RT / kWarps) + j * RI + lane / CH, row = lp.tile * RT + rl;
+            if (rl >= A.q_rows) continue;
+            const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
+            const int t = r / G;
+            const bool ok = row < rows && t < S.fresh[b];
+            const T *q = static_cast<const T *>(J.q);
+            if (ok) q += (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(lp.h) * G + r - t * G) * D + c * 8;
+            cp_async16(q_at + lq * q_bytes + chunk_at<D>(rl, c), q, ok);
+        }
+        lq = lq + 1 == kQueries ? 0 : lq + 1;
+    };
+    auto load_next = [&](int stage) {
+        if (lu < hi) {
+            if (lnew) {
+                load_queries();
+                lnew = false;
+            }
+            load_stage<D>(A, lk, lpages, lp.h, lp.step, warp, ring_at + stage * kStageBytes, lane);
+            if (++lu < hi) {
+                if (++lp.step == lp.steps) {
+                    next_item(A, S, lp);
+                    lk = keys_of(A, S, lp);
+                    lpages = pages_of<D>(A, lk, 0, warp, lane);
+                    lnew = true;
+                } else if ((lp.step - lpages.from) * (KW / 16) == 32) {
+                    lpages = pages_of<D>(A, lk, lp.step, warp, lane);
+                }
+            }
+        }
+        tc::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < kStages; ++s) load_next(s);
+
+    // the join's copy of the sums, and the rows of sequences without a key (in no CTA's share)
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
+    if (J.batch.prefix_len == 0) {
         for (int b = blockIdx.x; b < B; b += gridDim.x) {
             if (cum[b] != cum[b + 1]) continue;
             const int64_t at = int64_t(b) * J.batch.T * J.q_heads;
@@ -321,39 +378,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         }
     }
     if (lo >= hi) {
-        pdl_wait();
+        if (A.tc_items) pdl_wait();
         return;
     }
-
-    // the ring runs ahead of the products, across items
-    int64_t lu = lo;
-    Place lp = place_of(A, cum, lo);
-    Keys lk = keys_of(A, S, lp);
-    Pages<D> lpages = pages_of<D>(A, lk, lp.step * kStep + warp * KW);
-    auto load_next = [&](int stage) {
-        if (lu < hi) {
-            load_stage<D>(A, lk, lpages, lp.h, lp.step * kStep + warp * KW, ring_at + stage * kStageBytes, lane);
-            if (++lu < hi) {
-                if (++lp.step == lp.steps) {
-                    next_item(A, S, lp);
-                    lk = keys_of(A, S, lp);
-                    // its queries: into L1 by the time the products get there
-                    const int row = lp.tile * RT + (lane >> 1), rows = lp.b < 0 ? B * A.R : A.R;
-                    if (warp == 0 && row < rows) {
-                        const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
-                        const int t = r / G;
-                        const T *q = static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride +
-                                     (int64_t(lp.h) * G + r - t * G) * D + (lane & 1) * (D / 2);
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
-                    }
-                }
-                lpages = pages_of<D>(A, lk, lp.step * kStep + warp * KW);
-            }
-        }
-        tc::cp_async_commit();
-    };
-#pragma unroll 1
-    for (int s = 0; s < kStages; ++s) load_next(s);
 
     // Without a prefix, the last of an item's CTAs to get here joins its parts: one
     // counter per item, left at zero.
@@ -412,17 +439,117 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         __syncthreads();   // scratch[0] is free again
     };
 
-    uint32_t qf[MT][D / 16][4];
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2];
     int lim[MT][2];
-    Place p = place_of(A, cum, lo);
     int nkeys = 0, mts = 1, first_step = 0, clear = 0;   // no row's limit lies below `clear`
     bool upper = false;                                  // rows 8.. of a lone m16 tile exist
+    uint32_t q_now = 0;                                  // the item's queries
+    int cq = 0;
+
+    // The products of one stage with the item's first NM row tiles.
+    auto products = [&](auto nm, uint32_t kaddr, int key0) {
+        constexpr int NM = decltype(nm)::value;
+        const uint32_t vaddr = kaddr + KW * D * 2;
+        float s[NM][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
+        const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
+        const int qrow = ((lane & 7) + ((lane >> 3) & 1) * 8) & (A.q_rows - 1), qch = lane >> 4;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t qf[NM][4];
+#pragma unroll
+            for (int mt = 0; mt < NM; ++mt) ldsm4(qf[mt], q_now + chunk_at<D>(mt * 16 + qrow, 2 * ks + qch));
+#pragma unroll
+            for (int n2 = 0; n2 < NT / 2; ++n2) {
+                uint32_t kf[4];
+                ldsm4(kf, kaddr + chunk_at<D>(n2 * 16 + krow, 2 * ks + kch));
+#pragma unroll
+                for (int mt = 0; mt < NM; ++mt) {
+                    mma16816<T>(s[mt][2 * n2], qf[mt], kf[0], kf[1]);
+                    mma16816<T>(s[mt][2 * n2 + 1], qf[mt], kf[2], kf[3]);
+                }
+            }
+        }
+        if (A.flip | ~A.keep) {      // a scale that is not positive
+#pragma unroll
+            for (int mt = 0; mt < NM; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[mt][n][e] = __uint_as_float((__float_as_uint(s[mt][n][e]) & A.keep) ^ (A.flip & 0x80000000u));
+        }
+        uint32_t pf[NM][NT / 2][4];
+        const bool masked = key0 + KW > clear;
+#pragma unroll
+        for (int mt = 0; mt < NM; ++mt) {
+            float alpha[2] = {1.0f, 1.0f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (MT == 1 && i == 1 && !upper) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) pf[mt][n >> 1][2 * (n & 1) + 1] = 0u;
+                    break;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (key0 + n * 8 + 2 * (lane & 3) + e >= lim[mt][i]) s[mt][n][2 * i + e] = -INFINITY;
+                }
+                float mx = fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]);
+#pragma unroll
+                for (int n = 1; n < NT; ++n) mx = max3(mx, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                const float top = fmaxf(m[mt][i], mx * A.scale2), base = base_of(top);
+                alpha[i] = ex2(m[mt][i] - base);
+                m[mt][i] = top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float e0 = ex2(fmaf(s[mt][n][2 * i], A.scale2, -base));
+                    const float e1 = ex2(fmaf(s[mt][n][2 * i + 1], A.scale2, -base));
+                    sum += e0 + e1;
+                    pf[mt][n >> 1][2 * (n & 1) + i] = pack16<T>(e0, e1);
+                }
+                l[mt][i] = l[mt][i] * alpha[i] + sum;
+            }
+            if (__any_sync(~0u, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+                for (int d = 0; d < D / 8; ++d) {
+                    o[mt][d][0] *= alpha[0];
+                    o[mt][d][1] *= alpha[0];
+                    o[mt][d][2] *= alpha[1];
+                    o[mt][d][3] *= alpha[1];
+                }
+            }
+        }
+        const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
+#pragma unroll
+        for (int k2 = 0; k2 < NT / 2; ++k2)
+#pragma unroll
+            for (int dn = 0; dn < D / 16; ++dn) {
+                uint32_t vf[4];
+                ldsm4t(vf, vaddr + chunk_at<D>(k2 * 16 + vrow, 2 * dn + vch));
+#pragma unroll
+                for (int mt = 0; mt < NM; ++mt) {
+                    mma16816<T>(o[mt][2 * dn], pf[mt][k2], vf[0], vf[1]);
+                    mma16816<T>(o[mt][2 * dn + 1], pf[mt][k2], vf[2], vf[3]);
+                }
+            }
+    };
+
     int64_t u = lo;
     bool fresh = true;
     int stage = 0;
     while (u < hi) {
+        tc::cp_async_wait<kStages - 1>();
         if (fresh) {
             fresh = false;
             if (u != lo) next_item(A, S, p);
@@ -433,133 +560,36 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
             upper = rows - p.tile * RT > 8;
             clear = nkeys;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = p.tile * RT + mt * 16 + i * 8 + (lane >> 2);
-                    int b = p.b, r = row;
-                    if (p.b < 0) {
-                        b = row / A.R;
-                        r = row - b * A.R;
-                    }
-                    const int t = r / G, g = r - t * G;
-                    bool ok = row < rows;
-                    int n = 0;
-                    if (ok) {
-                        n = S.fresh[b];
-                        ok = t < n;
-                    }
-                    lim[mt][i] = ok || row >= rows ? nkeys : 0;    // rows that are not there: never looked at
-                    if (ok && p.b >= 0) {
-                        const int see = nkeys - n + t + 1;
-                        lim[mt][i] = see < 0 ? 0 : see;
-                    }
-                    clear = min(clear, lim[mt][i]);
                     m[mt][i] = -INFINITY;
                     l[mt][i] = 0.0f;
-                    const T *q = static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride +
-                                 (int64_t(p.h) * G + g) * D + 2 * (lane & 3);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        qf[mt][ks][i] = ok ? (__ldg(reinterpret_cast<const uint32_t *>(q + ks * 16)) & A.keep) ^ A.flip : 0u;
-                        qf[mt][ks][2 + i] = ok ? (__ldg(reinterpret_cast<const uint32_t *>(q + ks * 16 + 8)) & A.keep) ^ A.flip : 0u;
+                    lim[mt][i] = nkeys;
+                    if (row < rows) {      // the others are never looked at
+                        const int b = p.b < 0 ? row / A.R : p.b, t = (p.b < 0 ? row - b * A.R : row) / G;
+                        const int n = S.fresh[b], see = nkeys - n + t + 1;
+                        if (t >= n || see < 0) lim[mt][i] = 0;
+                        else if (p.b >= 0) lim[mt][i] = see;
                     }
+                    clear = min(clear, lim[mt][i]);
                 }
 #pragma unroll
-            for (int q = 4; q < 32; q <<= 1) clear = min(clear, __shfl_xor_sync(~0u, clear, q));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
                 for (int d = 0; d < D / 8; ++d) o[mt][d][0] = o[mt][d][1] = o[mt][d][2] = o[mt][d][3] = 0.0f;
+            }
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) clear = min(clear, __shfl_xor_sync(~0u, clear, q));
+            q_now = q_at + cq * q_bytes;
+            cq = cq + 1 == kQueries ? 0 : cq + 1;
+            __syncthreads();               // the other warps' rows of the queries
         }
-
-        tc::cp_async_wait<kStages - 1>();
         __syncwarp();
         const int key0 = p.step * kStep + warp * KW;
         uint8_t *st = ring + stage * kStageBytes;
         if (key0 < nkeys) {
-            const uint32_t kaddr = ring_at + stage * kStageBytes, vaddr = kaddr + KW * D * 2;
-            float s[MT][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
-            const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                for (int n2 = 0; n2 < NT / 2; ++n2) {
-                    uint32_t kf[4];
-                    ldsm4(kf, kaddr + chunk_at<D>(n2 * 16 + krow, 2 * ks + kch));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        if (mt < mts) {
-                            mma16816<T>(s[mt][2 * n2], qf[mt][ks], kf[0], kf[1]);
-                            mma16816<T>(s[mt][2 * n2 + 1], qf[mt][ks], kf[2], kf[3]);
-                        }
-                }
-            uint32_t pf[MT][NT / 2][4];
-            const bool masked = key0 + KW > clear;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                if (mt < mts) {
-                    float alpha[2] = {1.0f, 1.0f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (MT == 1 && i == 1 && !upper) {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) pf[mt][n >> 1][2 * (n & 1) + 1] = 0u;
-                            break;
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (key0 + n * 8 + 2 * (lane & 3) + e >= lim[mt][i]) s[mt][n][2 * i + e] = -INFINITY;
-                        }
-                        float mx = fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]);
-#pragma unroll
-                        for (int n = 1; n < NT; ++n) mx = max3(mx, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
-                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                        const float top = fmaxf(m[mt][i], mx * A.scale2), base = base_of(top);
-                        alpha[i] = ex2(m[mt][i] - base);
-                        m[mt][i] = top;
-                        float sum = 0.0f;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const float e0 = ex2(fmaf(s[mt][n][2 * i], A.scale2, -base));
-                            const float e1 = ex2(fmaf(s[mt][n][2 * i + 1], A.scale2, -base));
-                            sum += e0 + e1;
-                            pf[mt][n >> 1][2 * (n & 1) + i] = pack16<T>(e0, e1);
-                        }
-                        l[mt][i] = l[mt][i] * alpha[i] + sum;
-                    }
-                    if (__any_sync(~0u, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-                        for (int d = 0; d < D / 8; ++d) {
-                            o[mt][d][0] *= alpha[0];
-                            o[mt][d][1] *= alpha[0];
-                            o[mt][d][2] *= alpha[1];
-                            o[mt][d][3] *= alpha[1];
-                        }
-                    }
-                }
-            const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
-#pragma unroll
-            for (int k2 = 0; k2 < NT / 2; ++k2)
-#pragma unroll
-                for (int dn = 0; dn < D / 16; ++dn) {
-                    uint32_t vf[4];
-                    ldsm4t(vf, vaddr + chunk_at<D>(k2 * 16 + vrow, 2 * dn + vch));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        if (mt < mts) {
-                            mma16816<T>(o[mt][2 * dn], pf[mt][k2], vf[0], vf[1]);
-                            mma16816<T>(o[mt][2 * dn + 1], pf[mt][k2], vf[2], vf[3]);
-                        }
-                }
+            if (MT == 1 || mts == 1) products(std::integral_constant<int, 1>{}, ring_at + stage * kStageBytes, key0);
+            else products(std::integral_constant<int, MT>{}, ring_at + stage * kStageBytes, key0);
         }
         __syncwarp();   // every lane has read the stage
 
@@ -636,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
     }
     tc::cp_async_wait<0>();
     // the join reads this grid's partial results and the prefix kernel's: end after both
-    pdl_wait();
+    if (A.tc_items) pdl_wait();
 }
 
 // Joins the partial results of a call with a prefix: four rows of one
@@ -757,6 +787,13 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     if (J.lse && c == 0) J.lse[at] = lse_of(m, l);
 }
 
+// Dynamic shared memory of a CTA: rings, query tiles, warps' (m, l), the batch.
+size_t smem_of(const Args &A) {
+    const int D = A.J.cache.head_dim, MT = A.RT / 16, stages = stages_of(D, MT);
+    return size_t(kWarps) * stages * (4 * keys_of_stage(D) * D) + size_t(stages + 1) * A.q_rows * D * 2 +
+           kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
+}
+
 // The work's layout from the job's sizes; the grid that a call would use.
 Args layout(const trit_attn_job &J) {
     Args A = {};
@@ -767,6 +804,7 @@ Args layout(const trit_attn_job &J) {
     if (on_tc) prefix_layout(A);
     const int64_t pre_rows = J.batch.prefix_len > 0 && !on_tc ? int64_t(J.batch.B) * A.R : 0;
     A.RT = A.R > 16 || pre_rows > 16 ? 32 : 16;
+    A.q_rows = A.R <= 8 && pre_rows <= 8 ? 8 : A.RT;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
     const int kStep = kWarps * keys_of_stage(J.cache.head_dim);
@@ -777,7 +815,9 @@ Args layout(const trit_attn_job &J) {
     const int64_t cap = (int64_t(J.batch.table_pages) * J.cache.page_size + kStep - 1) / kStep;
     const int64_t most = int64_t(J.cache.heads) * (int64_t(A.pre_tiles) * A.pre_steps +
                                                    int64_t(J.batch.B) * A.own_tiles * cap);
-    const int64_t grid = int64_t(kSms) * ctas_of(J.cache.head_dim, A.RT / 16);
+    int per_sm = int(kSmemPerSm / (smem_of(A) + 1024));   // resident together: no CTA waits for another's end
+    if (per_sm > ctas_of(J.cache.head_dim, A.RT / 16)) per_sm = ctas_of(J.cache.head_dim, A.RT / 16);
+    const int64_t grid = int64_t(kSms) * (per_sm > 0 ? per_sm : 1);
     A.grid = int(most < grid ? most : grid);
     return A;
 }
@@ -798,19 +838,12 @@ int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_
 
 template <typename T, int D, int MT>
 cudaError_t launch(const Args &A, cudaStream_t s) {
-    const size_t smem = size_t(kWarps) * stages_of(D, MT) * (2 * keys_of_stage(D) * D * 2) + kWarps * 16 * MT * 8 + kWarps * 4 +
-                        (size_t(A.J.batch.B) * 3 + 1) * 4;
+    const size_t smem = smem_of(A);
     cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
-    if (A.tc_items) {
-        // the prefix kernel first; this one depends on nothing of it and may start beside it
-        e = launch_prefix(A, s);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(attn_kernel<T, D, MT>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
-    } else {
-        attn_kernel<T, D, MT><<<A.grid, kThreads, smem, s>>>(A);
-        e = cudaGetLastError();
-    }
+    // the prefix kernel first: the next one depends on nothing of it and may start beside it
+    if (A.tc_items) e = launch_prefix(A, s);
+    if (e == cudaSuccess) e = launch_pdl(attn_kernel<T, D, MT>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
     if (e != cudaSuccess) return e;
     if (A.J.batch.prefix_len == 0) return cudaSuccess;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);

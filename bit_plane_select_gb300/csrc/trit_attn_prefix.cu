@@ -245,6 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // the kernels behind this one start once every CTA has passed here, and rely on it
+    // for all that came before
+    pdl_wait();
     pdl_launch();
 
     // a block's place in the ring's order of use: K0 V0 K1 V1 ... for a pair,
@@ -542,8 +545,8 @@ cudaError_t launch(const Args &A, cudaStream_t s) {
     e = cudaFuncGetAttributes(&f, prefix_kernel<T, D>);
     if (e != cudaSuccess) return e;
     if (f.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-    prefix_kernel<T, D><<<A.tc_items * A.tc_splits, kThreads, smem_bytes<D>(), s>>>(A, kmap, vmap);
-    return cudaGetLastError();
+    return launch_pdl(prefix_kernel<T, D>, dim3(unsigned(A.tc_items * A.tc_splits)), dim3(kThreads), smem_bytes<D>(), s, A,
+                      kmap, vmap);
 }
 
 }  // namespace
