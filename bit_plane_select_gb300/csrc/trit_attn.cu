@@ -672,12 +672,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
 // Joins the partial results of a call with a prefix: four rows of one
 // (sequence, key head) per CTA, four columns per thread, rows by lane first so
 // that both forms of partial results (by row, and the tensor-core kernel's by
-// column group) are read in whole sectors; kJoin groups of threads take every
-// kJoin-th part, four at a time, since the loads' latency is the cost.
-constexpr int kJoin = 4;
-template <typename T, int D>
+// column group) are read in whole sectors.  The loads' latency is the cost: where
+// there are few rows, kJoin = 4 groups of threads take every fourth part, four at
+// a time, else one group takes eight at a time.
+template <typename T, int D, int kJoin>
 __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ Args A) {
-    __shared__ float sh[kJoin - 1][6][D];
+    __shared__ float sh[kJoin > 1 ? kJoin - 1 : 1][6][D];
     pdl_wait();
     const trit_attn_job &J = A.J;
     const int Hkv = J.cache.heads, G = A.G, T_ = J.batch.T, RT = A.RT;
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     const int total = own + prefix;
     float m = -INFINITY, l = 0.0f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 4;     // parts in flight
+    constexpr int U = kJoin == 1 ? 8 : 4;     // parts in flight
     for (int i0 = part0; i0 < total; i0 += U * kJoin) {
         float2 ml[U];
         float4 x[U];
@@ -763,24 +763,27 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < U; ++k) add_part(ml[k], x[k], base, l, v);
     }
-    if (part0) {
-        float(*o)[D] = sh[part0 - 1];
-        o[0][tid] = m; o[1][tid] = l;
-        o[2][tid] = v.x; o[3][tid] = v.y; o[4][tid] = v.z; o[5][tid] = v.w;
+    if constexpr (kJoin > 1) {
+        if (part0) {
+            float(*o)[D] = sh[part0 - 1];
+            o[0][tid] = m; o[1][tid] = l;
+            o[2][tid] = v.x; o[3][tid] = v.y; o[4][tid] = v.z; o[5][tid] = v.w;
+        }
+        __syncthreads();
+        if (part0) return;
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kJoin - 1; ++k) top = fmaxf(top, sh[k][0][tid]);
+        const float base = base_of(top), f0 = ex2(m - base);
+        m = top;
+        l *= f0;
+        v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
+#pragma unroll
+        for (int k = 0; k < kJoin - 1; ++k)
+            add_part(make_float2(sh[k][0][tid], sh[k][1][tid]),
+                     make_float4(sh[k][2][tid], sh[k][3][tid], sh[k][4][tid], sh[k][5][tid]), base, l, v);
     }
-    __syncthreads();
-    if (part0 || r4 >= A.R) return;
-    float top = m;
-#pragma unroll
-    for (int k = 0; k < kJoin - 1; ++k) top = fmaxf(top, sh[k][0][tid]);
-    const float base = base_of(top), f0 = ex2(m - base);
-    m = top;
-    l *= f0;
-    v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
-#pragma unroll
-    for (int k = 0; k < kJoin - 1; ++k)
-        add_part(make_float2(sh[k][0][tid], sh[k][1][tid]),
-                 make_float4(sh[k][2][tid], sh[k][3][tid], sh[k][4][tid], sh[k][5][tid]), base, l, v);
+    if (r4 >= A.R) return;
     const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     const int64_t at = (int64_t(b) * T_ + t) * J.q_heads + int64_t(h) * G + g;
     store_out<T>(J, at * D + c * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -847,7 +850,8 @@ cudaError_t launch(const Args &A, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (A.J.batch.prefix_len == 0) return cudaSuccess;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
-    return launch_pdl(join_kernel<T, D>, dim3(unsigned(joins)), dim3(kJoin * D), 0, s, A);
+    if (joins <= 2 * kSms) return launch_pdl(join_kernel<T, D, 4>, dim3(unsigned(joins)), dim3(4 * D), 0, s, A);
+    return launch_pdl(join_kernel<T, D, 1>, dim3(unsigned(joins)), dim3(D), 0, s, A);
 }
 
 template <typename T>
