@@ -11,11 +11,12 @@
 //
 // Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
 // reading K and V: 4 D bytes a key against 4 D R flops.  A step's keys go 16
-// (32 where D = 64) to a warp; every warp has its own ring of three such stages of K and V,
-// filled by 16-byte asynchronous copies two stages ahead, so warps never wait
-// for one another inside an item.  S = Q K^T and O += P V are 16-bit
-// mma.sync with fp32 sums (the rows fill one or two m16 tiles); the rows' m and
-// l live in registers and O is only rescaled when a maximum moved.
+// (32 where D = 64) to a warp; every warp has its own ring of two such stages of K and V,
+// filled by 16-byte asynchronous copies a stage ahead, so warps never wait
+// for one another inside an item.  S^T = K Q^T and O^T += V^T P^T are 16-bit
+// mma.sync with fp32 sums, the rows on the n8 side: four rows fill half a tile, not a
+// quarter of an m16 one, and O takes D/4 registers per 8 rows.  The rows' m and l
+// live in registers and O is only rescaled when a maximum moved.
 // P is rounded to the cache's 16-bit type for the second product: relative
 // 2^-9 (bf16) or 2^-12 (fp16) of each term on average, the size of the output's own rounding.
 #include <type_traits>
@@ -48,6 +49,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
+__device__ __forceinline__ uint32_t transposed8(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
 }
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -275,14 +282,14 @@ __device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float 
     v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
 }
 
-// Stages and CTAs per SM.
-__host__ __device__ constexpr int stages_of(int D, int MT) { return 2; }
-__host__ __device__ constexpr int ctas_of(int D, int MT) { return MT == 1 ? 3 : 2; }
+constexpr int kStages = 2;
+// CTAs per SM by the row tiles' registers (shared memory allows three).
+__host__ __device__ constexpr int ctas_of(int NB) { return NB <= 2 ? 3 : 2; }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __grid_constant__ Args A) {
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int RT = 16 * MT, kStages = stages_of(D, MT);
+    constexpr int RT = 8 * NB;
     constexpr int KW = keys_of_stage(D), NT = KW / 8, kStep = KW * kWarps;
     constexpr int kStageBytes = 2 * KW * D * 2;
     constexpr int kQueries = kStages + 1;     // query tiles: the loads run at most kStages items ahead
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *ring = smem + warp * kStages * kStageBytes;
     const uint32_t ring_at = tc::smem_u32(ring);
-    const uint32_t q_at = tc::smem_u32(smem + kWarps * kStages * kStageBytes), q_bytes = A.q_rows * D * 2;
+    const uint32_t q_at = tc::smem_u32(smem + kWarps * kStages * kStageBytes), q_bytes = RT * D * 2;
     float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes + kQueries * q_bytes);   // [kWarps][RT] (m, l)
     int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
     Batch S;
@@ -329,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         constexpr int CH = D / 8, RI = 32 / CH;
         const int rows = lp.b < 0 ? B * A.R : A.R, c = lane % CH;
 #pragma unroll
-        for (int j = 0; j < RT / kWarps / RI; ++j) {
-            const int rl = warp * (RT / kWarps) + j * RI + lane / CH, row = lp.tile * RT + rl;
-            if (rl >= A.q_rows) continue;
+        for (int j = 0; j < (RT + kWarps * RI - 1) / (kWarps * RI); ++j) {
+            const int rl = (j * kWarps + warp) * RI + lane / CH, row = lp.tile * RT + rl;
+            if (rl >= RT) continue;
             const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
             const int t = r / G;
             const bool ok = row < rows && t < S.fresh[b];
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
 
     // Without a prefix, the last of an item's CTAs to get here joins its parts: one
     // counter per item, left at zero.
-    auto join_last = [&](const Place &q, int rows, int filled) {
+    auto join_last = [&](const Place &q, int rows) {
         const int64_t s0 = int64_t(cum[q.b]) * Hkv * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
         const int64_t c0 = cta_of(s0, W, ctas);
         const int parts = int(cta_of(s0 + q.steps - 1, W, ctas) - c0) + 1;
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         __syncthreads();
         if (scratch[0]) {
             constexpr int CH = D / 4;
-            for (int i = threadIdx.x; i < filled * CH; i += kThreads) {
+            for (int i = threadIdx.x; i < RT * CH; i += kThreads) {
                 const int r = i / CH, c = (i % CH) * 4, row = q.tile * RT + r;
                 if (row >= rows) break;
                 float m = -INFINITY, l = 0.0f;
@@ -439,109 +446,126 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         __syncthreads();   // scratch[0] is free again
     };
 
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];
-    int lim[MT][2];
-    int nkeys = 0, mts = 1, first_step = 0, clear = 0;   // no row's limit lies below `clear`
-    bool upper = false;                                  // rows 8.. of a lone m16 tile exist
-    uint32_t q_now = 0;                                  // the item's queries
+    float o[D / 16][NB][4];
+    float m[NB][2], l[NB][2];
+    int lim[NB][2];
+    int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no row's limit lies below `clear`
+    uint32_t q_now = 0;                                    // the item's queries
     int cq = 0;
 
-    // The products of one stage with the item's first NM row tiles.
+    // The products of one stage with the item's first NM tiles of 8 rows.  Keys and
+    // columns of V are the m16 side, rows the n8 side: S^T = K Q^T, O^T += V^T P^T.  A
+    // thread's scores are those of rows 2 (lane % 4) + e, keys lane / 4 and + 8 of a
+    // tile; P^T becomes an operand by transposing its 8 x 8 blocks.
     auto products = [&](auto nm, uint32_t kaddr, int key0) {
-        constexpr int NM = decltype(nm)::value;
+        constexpr int NM = decltype(nm)::value, KM = KW / 16;
         const uint32_t vaddr = kaddr + KW * D * 2;
-        float s[NM][NT][4];
+        float s[KM][NM][4];
 #pragma unroll
-        for (int mt = 0; mt < NM; ++mt)
+        for (int km = 0; km < KM; ++km)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
-        const int krow = (lane >> 4) * 8 + (lane & 7), kch = (lane >> 3) & 1;
-        const int qrow = ((lane & 7) + ((lane >> 3) & 1) * 8) & (A.q_rows - 1), qch = lane >> 4;
+            for (int n = 0; n < NM; ++n) s[km][n][0] = s[km][n][1] = s[km][n][2] = s[km][n][3] = 0.0f;
+        const int arow = ((lane >> 3) & 1) * 8 + (lane & 7), ach = lane >> 4;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t qf[NM][4];
+        for (int k2 = 0; k2 < D / 32; ++k2) {     // two k16 steps
+            uint32_t qf[2][(NM + 1) / 2 * 2][2];
+            if (NM == 1) {
+                uint32_t f[4];
+                ldsm4(f, q_now + chunk_at<D>(lane & 7, 4 * k2 + (lane >> 3)));
+                qf[0][0][0] = f[0]; qf[0][0][1] = f[1]; qf[1][0][0] = f[2]; qf[1][0][1] = f[3];
+            } else {
 #pragma unroll
-            for (int mt = 0; mt < NM; ++mt) ldsm4(qf[mt], q_now + chunk_at<D>(mt * 16 + qrow, 2 * ks + qch));
+                for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int n2 = 0; n2 < NT / 2; ++n2) {
-                uint32_t kf[4];
-                ldsm4(kf, kaddr + chunk_at<D>(n2 * 16 + krow, 2 * ks + kch));
-#pragma unroll
-                for (int mt = 0; mt < NM; ++mt) {
-                    mma16816<T>(s[mt][2 * n2], qf[mt], kf[0], kf[1]);
-                    mma16816<T>(s[mt][2 * n2 + 1], qf[mt], kf[2], kf[3]);
-                }
+                    for (int n2 = 0; n2 < (NM + 1) / 2; ++n2) {
+                        uint32_t f[4];
+                        ldsm4(f, q_now + chunk_at<D>(n2 * 16 + (lane >> 4) * 8 + (lane & 7),
+                                                     2 * (2 * k2 + kk) + ((lane >> 3) & 1)));
+                        qf[kk][2 * n2][0] = f[0]; qf[kk][2 * n2][1] = f[1];
+                        qf[kk][2 * n2 + 1][0] = f[2]; qf[kk][2 * n2 + 1][1] = f[3];
+                    }
             }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int km = 0; km < KM; ++km) {
+                    uint32_t kf[4];
+                    ldsm4(kf, kaddr + chunk_at<D>(km * 16 + arow, 2 * (2 * k2 + kk) + ach));
+#pragma unroll
+                    for (int n = 0; n < NM; ++n) mma16816<T>(s[km][n], kf, qf[kk][n][0], qf[kk][n][1]);
+                }
         }
         if (A.flip | ~A.keep) {      // a scale that is not positive
 #pragma unroll
-            for (int mt = 0; mt < NM; ++mt)
+            for (int km = 0; km < KM; ++km)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NM; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        s[mt][n][e] = __uint_as_float((__float_as_uint(s[mt][n][e]) & A.keep) ^ (A.flip & 0x80000000u));
+                        s[km][n][e] = __uint_as_float((__float_as_uint(s[km][n][e]) & A.keep) ^ (A.flip & 0x80000000u));
         }
-        uint32_t pf[NM][NT / 2][4];
+        uint32_t pf[KM][NM][2];
         const bool masked = key0 + KW > clear;
+        float alpha[NM][2];
+        bool moved = false;
 #pragma unroll
-        for (int mt = 0; mt < NM; ++mt) {
-            float alpha[2] = {1.0f, 1.0f};
+        for (int n = 0; n < NM; ++n) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (MT == 1 && i == 1 && !upper) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) pf[mt][n >> 1][2 * (n & 1) + 1] = 0u;
-                    break;
-                }
+            for (int e = 0; e < 2; ++e) {
                 if (masked) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int km = 0; km < KM; ++km)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (key0 + n * 8 + 2 * (lane & 3) + e >= lim[mt][i]) s[mt][n][2 * i + e] = -INFINITY;
+                        for (int i = 0; i < 2; ++i)
+                            if (key0 + km * 16 + i * 8 + (lane >> 2) >= lim[n][e]) s[km][n][2 * i + e] = -INFINITY;
                 }
-                float mx = fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]);
+                float mx = fmaxf(s[0][n][e], s[0][n][2 + e]);
 #pragma unroll
-                for (int n = 1; n < NT; ++n) mx = max3(mx, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-                const float top = fmaxf(m[mt][i], mx * A.scale2), base = base_of(top);
-                alpha[i] = ex2(m[mt][i] - base);
-                m[mt][i] = top;
+                for (int km = 1; km < KM; ++km) mx = max3(mx, s[km][n][e], s[km][n][2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                const float top = fmaxf(m[n][e], mx * A.scale2), base = base_of(top);
+                alpha[n][e] = ex2(m[n][e] - base);
+                moved |= alpha[n][e] != 1.0f;
+                m[n][e] = top;
                 float sum = 0.0f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float e0 = ex2(fmaf(s[mt][n][2 * i], A.scale2, -base));
-                    const float e1 = ex2(fmaf(s[mt][n][2 * i + 1], A.scale2, -base));
-                    sum += e0 + e1;
-                    pf[mt][n >> 1][2 * (n & 1) + i] = pack16<T>(e0, e1);
-                }
-                l[mt][i] = l[mt][i] * alpha[i] + sum;
-            }
-            if (__any_sync(~0u, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+                for (int km = 0; km < KM; ++km)
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d) {
-                    o[mt][d][0] *= alpha[0];
-                    o[mt][d][1] *= alpha[0];
-                    o[mt][d][2] *= alpha[1];
-                    o[mt][d][3] *= alpha[1];
-                }
+                    for (int i = 0; i < 2; ++i) {
+                        float &v = s[km][n][2 * i + e];
+                        v = ex2(fmaf(v, A.scale2, -base));
+                        sum += v;
+                    }
+                l[n][e] = l[n][e] * alpha[n][e] + sum;
             }
+#pragma unroll
+            for (int km = 0; km < KM; ++km)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    pf[km][n][i] = transposed8(pack16<T>(s[km][n][2 * i], s[km][n][2 * i + 1]));
         }
-        const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
+        if (__any_sync(~0u, moved)) {
 #pragma unroll
-        for (int k2 = 0; k2 < NT / 2; ++k2)
+            for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int dn = 0; dn < D / 16; ++dn) {
-                uint32_t vf[4];
-                ldsm4t(vf, vaddr + chunk_at<D>(k2 * 16 + vrow, 2 * dn + vch));
-#pragma unroll
-                for (int mt = 0; mt < NM; ++mt) {
-                    mma16816<T>(o[mt][2 * dn], pf[mt][k2], vf[0], vf[1]);
-                    mma16816<T>(o[mt][2 * dn + 1], pf[mt][k2], vf[2], vf[3]);
+                for (int n = 0; n < NM; ++n) {
+                    o[d][n][0] *= alpha[n][0];
+                    o[d][n][1] *= alpha[n][1];
+                    o[d][n][2] *= alpha[n][0];
+                    o[d][n][3] *= alpha[n][1];
                 }
+        }
+        const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;
+#pragma unroll
+        for (int km = 0; km < KM; ++km)
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t vf[4];
+                ldsm4t(vf, vaddr + chunk_at<D>(km * 16 + vrow, 2 * d + vch));
+#pragma unroll
+                for (int n = 0; n < NM; ++n) mma16816<T>(o[d][n], vf, pf[km][n][0], pf[km][n][1]);
             }
     };
 
@@ -556,30 +580,30 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
             first_step = p.step;
             nkeys = keys_of(A, S, p).n;
             const int rows = p.b < 0 ? B * A.R : A.R;
-            mts = MT == 1 || rows - p.tile * RT <= 16 ? 1 : 2;
-            upper = rows - p.tile * RT > 8;
+            tiles = NB == 1 ? 1 : min(NB, (rows - p.tile * RT + 7) >> 3);
             clear = nkeys;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = p.tile * RT + mt * 16 + i * 8 + (lane >> 2);
-                    m[mt][i] = -INFINITY;
-                    l[mt][i] = 0.0f;
-                    lim[mt][i] = nkeys;
+                for (int e = 0; e < 2; ++e) {
+                    const int row = p.tile * RT + n * 8 + 2 * (lane & 3) + e;
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.0f;
+                    lim[n][e] = nkeys;
                     if (row < rows) {      // the others are never looked at
                         const int b = p.b < 0 ? row / A.R : p.b, t = (p.b < 0 ? row - b * A.R : row) / G;
-                        const int n = S.fresh[b], see = nkeys - n + t + 1;
-                        if (t >= n || see < 0) lim[mt][i] = 0;
-                        else if (p.b >= 0) lim[mt][i] = see;
+                        const int fresh_n = S.fresh[b], see = nkeys - fresh_n + t + 1;
+                        if (t >= fresh_n || see < 0) lim[n][e] = 0;
+                        else if (p.b >= 0) lim[n][e] = see;
                     }
-                    clear = min(clear, lim[mt][i]);
+                    clear = min(clear, lim[n][e]);
                 }
 #pragma unroll
-                for (int d = 0; d < D / 8; ++d) o[mt][d][0] = o[mt][d][1] = o[mt][d][2] = o[mt][d][3] = 0.0f;
-            }
+            for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-            for (int q = 4; q < 32; q <<= 1) clear = min(clear, __shfl_xor_sync(~0u, clear, q));
+                for (int n = 0; n < NB; ++n) o[d][n][0] = o[d][n][1] = o[d][n][2] = o[d][n][3] = 0.0f;
+            clear = min(clear, __shfl_xor_sync(~0u, clear, 1));
+            clear = min(clear, __shfl_xor_sync(~0u, clear, 2));
             q_now = q_at + cq * q_bytes;
             cq = cq + 1 == kQueries ? 0 : cq + 1;
             __syncthreads();               // the other warps' rows of the queries
@@ -588,8 +612,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
         const int key0 = p.step * kStep + warp * KW;
         uint8_t *st = ring + stage * kStageBytes;
         if (key0 < nkeys) {
-            if (MT == 1 || mts == 1) products(std::integral_constant<int, 1>{}, ring_at + stage * kStageBytes, key0);
-            else products(std::integral_constant<int, MT>{}, ring_at + stage * kStageBytes, key0);
+            const uint32_t kaddr = ring_at + stage * kStageBytes;
+            if (NB == 4 && tiles == 3) products(std::integral_constant<int, NB == 4 ? 3 : 1>{}, kaddr, key0);
+            else if (NB > 1 && tiles > NB / 2) products(std::integral_constant<int, NB>{}, kaddr, key0);
+            else products(std::integral_constant<int, NB == 4 ? 2 : 1>{}, kaddr, key0);
         }
         __syncwarp();   // every lane has read the stage
 
@@ -603,44 +629,48 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
             float *part = A.parts + slot * part_floats(RT, D);
             const int rows = p.b < 0 ? B * A.R : A.R;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt >= mts) break;
+            for (int half = 0; half < (NB + 1) / 2; ++half) {     // 16 rows at a time
+                if (half > 0 && tiles <= 2 * half) break;
                 float *mine = reinterpret_cast<float *>(st);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = i * 8 + (lane >> 2);
-                    float sum = l[mt][i];
-                    sum += __shfl_xor_sync(~0u, sum, 1);
-                    sum += __shfl_xor_sync(~0u, sum, 2);
-                    if ((lane & 3) == 0) {
-                        stats[(warp * RT + mt * 16 + r) * 2] = m[mt][i];
-                        stats[(warp * RT + mt * 16 + r) * 2 + 1] = sum;
-                    }
+                for (int n = 2 * half; n < (NB < 2 * half + 2 ? NB : 2 * half + 2); ++n)
 #pragma unroll
-                    for (int d = 0; d < D / 8; ++d)
-                        *reinterpret_cast<float2 *>(mine + r * D + ((d * 8 + 2 * (lane & 3)) ^ ((r & 7) << 3))) =
-                            make_float2(o[mt][d][2 * i], o[mt][d][2 * i + 1]);
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = (n - 2 * half) * 8 + 2 * (lane & 3) + e;
+                        float sum = l[n][e];
+                        sum += __shfl_xor_sync(~0u, sum, 4);
+                        sum += __shfl_xor_sync(~0u, sum, 8);
+                        sum += __shfl_xor_sync(~0u, sum, 16);
+                        if (lane < 4) {
+                            stats[(warp * RT + half * 16 + r) * 2] = m[n][e];
+                            stats[(warp * RT + half * 16 + r) * 2 + 1] = sum;
+                        }
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                mine[r * D + ((d * 16 + i * 8 + (lane >> 2)) ^ ((lane & 3) << 3))] = o[d][n][2 * i + e];
+                    }
                 __syncthreads();
                 constexpr int LR = D / 4, RW = 32 / LR;   // lanes of a row, rows of a warp pass
                 const float *all = reinterpret_cast<const float *>(smem + stage * kStageBytes);
-                for (int r = warp * RW + lane / LR; r < 16; r += kWarps * RW) {
-                    const int row = p.tile * RT + mt * 16 + r;
+                for (int r = warp * RW + lane / LR; r < (RT < 16 ? RT : 16); r += kWarps * RW) {
+                    const int row = p.tile * RT + half * 16 + r;
                     if (row >= rows) break;
                     float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * RT + mt * 16 + r) * 2]);
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * RT + half * 16 + r) * 2]);
                     const float base = base_of(top);
-                    const int c = (lane % LR) * 4, cs = c ^ ((r & 7) << 3);
+                    const int c = (lane % LR) * 4, cs = c ^ (((r >> 1) & 3) << 3);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float f = ex2(stats[(w * RT + mt * 16 + r) * 2] - base);
+                        const float f = ex2(stats[(w * RT + half * 16 + r) * 2] - base);
                         const float4 x = *reinterpret_cast<const float4 *>(
                             all + w * kStages * (kStageBytes / 4) + r * D + cs);
                         v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
-                        sum += f * stats[(w * RT + mt * 16 + r) * 2 + 1];
+                        sum += f * stats[(w * RT + half * 16 + r) * 2 + 1];
                     }
                     if (direct) {
                         const int t = row / G, g = row - t * G;
@@ -649,14 +679,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(D, MT)) attn_kernel(const __
                         store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                         if (J.lse && lane % LR == 0) J.lse[at] = lse_of(top, sum);
                     } else {
-                        *reinterpret_cast<float4 *>(part + (mt * 16 + r) * D + c) = v;
+                        *reinterpret_cast<float4 *>(part + (half * 16 + r) * D + c) = v;
                         if (lane % LR == 0)
-                            *reinterpret_cast<float2 *>(part + RT * D + (mt * 16 + r) * 2) = make_float2(top, sum);
+                            *reinterpret_cast<float2 *>(part + RT * D + (half * 16 + r) * 2) = make_float2(top, sum);
                     }
                 }
                 __syncthreads();
             }
-            if (!direct && J.batch.prefix_len == 0) join_last(p, rows, mts * 16);
+            if (!direct && J.batch.prefix_len == 0) join_last(p, rows);
             fresh = true;
         }
         load_next(stage);
@@ -792,8 +822,8 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 
 // Dynamic shared memory of a CTA: rings, query tiles, warps' (m, l), the batch.
 size_t smem_of(const Args &A) {
-    const int D = A.J.cache.head_dim, MT = A.RT / 16, stages = stages_of(D, MT);
-    return size_t(kWarps) * stages * (4 * keys_of_stage(D) * D) + size_t(stages + 1) * A.q_rows * D * 2 +
+    const int D = A.J.cache.head_dim;
+    return size_t(kWarps) * kStages * (4 * keys_of_stage(D) * D) + size_t(kStages + 1) * A.RT * D * 2 +
            kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
 }
 
@@ -806,8 +836,8 @@ Args layout(const trit_attn_job &J) {
     const bool on_tc = prefix_on_tensor_cores(J);
     if (on_tc) prefix_layout(A);
     const int64_t pre_rows = J.batch.prefix_len > 0 && !on_tc ? int64_t(J.batch.B) * A.R : 0;
-    A.RT = A.R > 16 || pre_rows > 16 ? 32 : 16;
-    A.q_rows = A.R <= 8 && pre_rows <= 8 ? 8 : A.RT;
+    const int64_t most_rows = pre_rows > A.R ? pre_rows : A.R;
+    A.RT = most_rows > 16 ? 32 : most_rows > 8 ? 16 : 8;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
     const int kStep = kWarps * keys_of_stage(J.cache.head_dim);
@@ -819,7 +849,7 @@ Args layout(const trit_attn_job &J) {
     const int64_t most = int64_t(J.cache.heads) * (int64_t(A.pre_tiles) * A.pre_steps +
                                                    int64_t(J.batch.B) * A.own_tiles * cap);
     int per_sm = int(kSmemPerSm / (smem_of(A) + 1024));   // resident together: no CTA waits for another's end
-    if (per_sm > ctas_of(J.cache.head_dim, A.RT / 16)) per_sm = ctas_of(J.cache.head_dim, A.RT / 16);
+    if (per_sm > ctas_of(A.RT / 8)) per_sm = ctas_of(A.RT / 8);
     const int64_t grid = int64_t(kSms) * (per_sm > 0 ? per_sm : 1);
     A.grid = int(most < grid ? most : grid);
     return A;
@@ -839,14 +869,14 @@ int64_t part_bytes(const Args &A) {
 
 int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_part_bytes(A); }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int NB>
 cudaError_t launch(const Args &A, cudaStream_t s) {
     const size_t smem = smem_of(A);
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     // the prefix kernel first: the next one depends on nothing of it and may start beside it
     if (A.tc_items) e = launch_prefix(A, s);
-    if (e == cudaSuccess) e = launch_pdl(attn_kernel<T, D, MT>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
+    if (e == cudaSuccess) e = launch_pdl(attn_kernel<T, D, NB>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
     if (e != cudaSuccess) return e;
     if (A.J.batch.prefix_len == 0) return cudaSuccess;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
@@ -856,8 +886,9 @@ cudaError_t launch(const Args &A, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_t(const Args &A, cudaStream_t s) {
-    if (A.J.cache.head_dim == 128) return A.RT == 16 ? launch<T, 128, 1>(A, s) : launch<T, 128, 2>(A, s);
-    return A.RT == 16 ? launch<T, 64, 1>(A, s) : launch<T, 64, 2>(A, s);
+    if (A.J.cache.head_dim == 128)
+        return A.RT == 8 ? launch<T, 128, 1>(A, s) : A.RT == 16 ? launch<T, 128, 2>(A, s) : launch<T, 128, 4>(A, s);
+    return A.RT == 8 ? launch<T, 64, 1>(A, s) : A.RT == 16 ? launch<T, 64, 2>(A, s) : launch<T, 64, 4>(A, s);
 }
 
 }  // namespace

@@ -27,7 +27,6 @@ struct Args {
     uint32_t flip, keep;     // on pairs of q: the sign of scale, and 0 where it is 0
     int32_t G, R;            // query heads per key head; rows per (sequence, key head)
     int32_t RT;              // rows of an item
-    int32_t q_rows;          // rows kept of its queries: 8 where no item has more, else RT
     int32_t own_tiles;       // row tiles per (sequence, key head)
     int32_t pre_tiles;       // row tiles of the prefix, per key head (0: no prefix item)
     int32_t pre_steps;       // steps of the prefix
