@@ -74,14 +74,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int clamped_len(const Args &A, int b, bool report) {
-    const int cap = A.J.batch.table_pages * A.J.cache.page_size;
-    const int n = A.J.batch.lens[b];
-    if (n >= 0 && n <= cap) return n;
-    if (report) raise_flag(A.err, TRIT_ERR_INDEX);
-    return n < 0 ? 0 : cap;
-}
-
 // Where a step of the work lies.
 struct Place {
     int b;         // -1: the prefix
@@ -245,9 +237,12 @@ __device__ __forceinline__ void load_stage(const Args &A, const Keys &K, const P
 template <int kStep>
 __device__ __forceinline__ void count_steps(const Args &A, const Batch &S, int32_t *scratch, bool report) {
     const int B = A.J.batch.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cap = A.J.batch.table_pages * A.J.cache.page_size;
     for (int i = tid; i < B; i += kThreads) {
-        S.len[i] = clamped_len(A, i, report);
-        S.fresh[i] = batch_new(A.J.batch, i);
+        const int n = A.J.batch.lens[i], m = batch_new(A.J.batch, i);
+        S.len[i] = n < 0 ? 0 : (n > cap ? cap : n);
+        S.fresh[i] = m;
+        if (report && (n < 0 || n > cap)) raise_flag(A.err, TRIT_ERR_INDEX);
     }
     __syncthreads();
     const int per = (B + kThreads - 1) / kThreads, from = tid * per;
@@ -310,6 +305,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     // after the prefix kernel nothing is left to wait for until the end
     if (!A.tc_items) pdl_wait();
     pdl_launch();
+    {   // the page table on its way to L2 while the lengths are: every CTA a few lines of it
+        const int64_t ints = int64_t(J.batch.B - 1) * J.batch.table_stride + J.batch.table_pages;
+        const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 32;
+        if (at < ints) asm volatile("prefetch.global.L2 [%0];" ::"l"(J.batch.table + at));
+    }
     count_steps<kStep>(A, S, scratch, blockIdx.x == 0);
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;

@@ -190,6 +190,10 @@ __device__ __forceinline__ void tma_page(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
+// The address of the tensor memory is in shared memory: a barrier of the softmax and
+// issuing warps.
+__device__ __forceinline__ void tmem_ready() { asm volatile("bar.sync 1, 320;" ::: "memory"); }
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap kmap,
@@ -236,15 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         *timed_out = 0;
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    tc_fence_before();
+    if (warp == kLoadWarp && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &vmap : &kmap) : "memory");
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     // the kernels behind this one start once every CTA has passed here, and rely on it
     // for all that came before
     pdl_wait();
@@ -261,6 +259,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ps = J.cache.page_size;
         const int rows = ps < kBlockKeys ? ps : kBlockKeys;      // keys of one copy
         const int npages = (P + ps - 1) / ps;
+        // page ids, 32 at a time: lane i holds the page of copy `have + i` of this CTA's keys,
+        // and the next 32 are on their way
+        const int per_block = kBlockKeys / rows;
+        const int first_page = ps <= kBlockKeys ? j0 * per_block : 0;
+        auto fetch = [&](int copy) {      // the page of this CTA's copy `copy`
+            const int i = ps <= kBlockKeys ? first_page + copy : (j0 + copy) / (ps / kBlockKeys);
+            return i < npages ? __ldg(J.batch.prefix_table + i) : -1;
+        };
+        int have = 0, ids = fetch(lane), ids_next = fetch(32 + lane);
         auto load = [&](int j, bool is_v, int at) -> bool {
             const int s = at % kRing;
             if (!warp_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) return false;
@@ -273,10 +280,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t *bar = clear ? tail : &full[s];
             uint8_t *st = ring + s * kTile;
             if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * D * 2);
-            __syncwarp();
-            for (int i = lane; i < copies * (D / 64); i += 32) {
-                const int c = i / (D / 64), half = i % (D / 64);
-                const int page = __ldg(J.batch.prefix_table + first + c);
+            if (j * per_block >= have + 32) {
+                have += 32;
+                ids = ids_next;
+                ids_next = fetch(have + 32 + lane);
+            }
+            // a single tile's V comes one block after the next K: its ids may have been passed
+            const int c = lane / (D / 64), half = lane % (D / 64);
+            int page = __shfl_sync(~0u, ids, (j * per_block + c - have) & 31);
+            if (j * per_block < have && c < copies) page = fetch(j * per_block + c);
+            if (c < copies) {
                 if (page < 0 || page >= J.cache.pages) raise_flag(A.err, TRIT_ERR_INDEX);   // reads as zeros
                 tma_page(st + half * (kBlockKeys * 128) + c * rows * 128, is_v ? &vmap : &kmap, half * 64,
                          key0 - first * ps, h, page, bar);
@@ -302,6 +315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kMmaWarp) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                         "r"(kTmemCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+            tc_fence_before();
+        }
+        tmem_ready();
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
         // stream s: S of its first block, then per block O += P V and S of the next,
         // which takes the place of P once that product has completed.  The whole warp
         // walks the loop (uniform values, so the operands are in uniform registers
@@ -375,27 +397,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int s = warp >> 2, r = threadIdx.x & 127;
         const uint32_t quarter = uint32_t((warp & 3) * 32) << 16;
-        {   // the query tile, a row per thread (half a row where the streams share a tile)
-            constexpr int CH = D / 8;
+        {   // the query tile: every lane finds one row, then the warp copies whole rows
+            constexpr int CH = D / 8, RI = 32 / CH;
             const int tile = 2 * group + (pair ? s : 0);
             uint8_t *dst = qs + (pair ? s * kTile : 0);
             const int fr = tile * kRows + r, rows = J.batch.B * A.R;
             const int b = fr / A.R, rr = fr - b * A.R, t = rr / A.G, g = rr - t * A.G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const T *>(J.q) + (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(h) * A.G + g) * D);
+            const int64_t mine_at = fr < rows ? (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(h) * A.G + g) * D : -1;
+            const int c = lane % CH;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                if (!pair && (c >= CH / 2) != (s == 1)) continue;
+            for (int j = 0; j < CH; ++j) {       // 32 rows, RI at a time (of a shared tile each stream takes half)
+                if (!pair && (j >= CH / 2) != (s == 1)) continue;
+                const int row = j * RI + lane / CH;
+                const int64_t at = __shfl_sync(~0u, mine_at, row);
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (fr < rows) v = __ldg(src + c);
+                if (at >= 0) v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) + at) + c);
                 v.x = (v.x & A.keep) ^ A.flip; v.y = (v.y & A.keep) ^ A.flip;
                 v.z = (v.z & A.keep) ^ A.flip; v.w = (v.w & A.keep) ^ A.flip;
-                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(r, c % 8)) = v;
+                const int at_row = (warp & 3) * 32 + row;
+                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(at_row, c % 8)) = v;
             }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
+        tmem_ready();     // after the queries: the allocation takes as long
+        tc_fence_after();
+        const uint32_t tmem = *tmem_slot;
         const float scale2 = A.scale2;
         const int mine = pair ? n : (n + 1 - s) / 2;       // this stream's blocks
         float m = -INFINITY, l = 0.0f;
@@ -494,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *timed_out) raise_flag(A.err, TRIT_ERR_TIMEOUT);
     if (warp == kMmaWarp) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols));
     }
 }
 
