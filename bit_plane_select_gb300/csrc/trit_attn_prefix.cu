@@ -36,8 +36,9 @@ using namespace tc;
 constexpr int kBlockKeys = 128;
 constexpr int kRows = 128;
 constexpr int kRing = 4;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;   // one issuing warp per stream: 8 and 9
-constexpr int kThreads = 384;      // 8 softmax warps, three of the roles above, an idle one
+constexpr int kMmaWarp = 8;       // 8 and 9: an issuing warp per stream
+constexpr int kLoadWarp = 10;     // 10 and 11: K's copies and V's
+constexpr int kThreads = 384;      // 8 softmax warps and the four above
 // Registers: launched with 168 a thread; the softmax warpgroups, which hold a row of
 // S, take 216 and the third keeps 72 (256 * 216 + 128 * 72 = 384 * 168).
 constexpr int kLaunchRegs = 168;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *pv_done = o_full + 2;      // stream's product into O has completed
     uint64_t *q_full = pv_done + 2;
     uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
+    constexpr int kBars = 2 * kRing + 12;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
     uint32_t *timed_out = tmem_slot + 1;
 
@@ -223,21 +225,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = j1 - j0;
     const bool pair = 2 * group + 1 < A.tc_tiles;     // two row tiles, or one over two streams
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kRing; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], pair ? 2 : 1);     // streams that read the tile
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&s_full[s], 1);
-            mbar_init(&p_full[2 * s], 4);
-            mbar_init(&p_full[2 * s + 1], 4);
-            mbar_init(&o_full[s], 1);
-            mbar_init(&pv_done[s], 1);
-        }
-        mbar_init(q_full, 8);
-        mbar_init(tail, 1);
-        *timed_out = 0;
+    if (warp == kMmaWarp && lane < kBars) {       // a barrier per lane, in the order above
+        const int i = lane;
+        const int count = i < kRing ? 1 : i < 2 * kRing ? (pair ? 2 : 1)     // empty: streams that read the tile
+                        : i < 2 * kRing + 2 ? 1 : i < 2 * kRing + 6 ? 4      // s_full, p_full (warps)
+                        : i < 2 * kRing + 10 ? 1 : i == 2 * kRing + 10 ? 8 : 1;   // o_full and pv_done, q_full (warps), tail
+        mbar_init(full + i, uint32_t(count));
+        if (i == 0) *timed_out = 0;
         fence_barrier_init();
     }
     if (warp == kLoadWarp && lane < 2)
@@ -254,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto v_at = [&](int j) { return pair ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2); };
 
     // every warp of a warpgroup gives up or takes the same number of registers
-    if (warp == kLoadWarp) {
+    if (warp >= kLoadWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int ps = J.cache.page_size;
         const int rows = ps < kBlockKeys ? ps : kBlockKeys;      // keys of one copy
@@ -268,50 +262,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             return i < npages ? __ldg(J.batch.prefix_table + i) : -1;
         };
         int have = 0, ids = fetch(lane), ids_next = fetch(32 + lane);
-        auto load = [&](int j, bool is_v, int at) -> bool {
-            const int s = at % kRing;
-            if (!warp_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) return false;
+        const bool is_v = warp > kLoadWarp;
+        const CUtensorMap *map = is_v ? &vmap : &kmap;
+        const int c = lane / (D / 64), half = lane % (D / 64);     // the lane's copy of a block
+        for (int j = 0; j < n; ++j) {
+            const int at = is_v ? v_at(j) : k_at(j), s = at % kRing;
             const int key0 = (j0 + j) * kBlockKeys;
             const int first = key0 / ps;
-            int copies = kBlockKeys / rows;
-            if (copies > npages - first) copies = npages - first;
+            const int copies = per_block < npages - first ? per_block : npages - first;
             const int keys = P - key0 < kBlockKeys ? P - key0 : kBlockKeys;
             const bool clear = is_v && keys < kBlockKeys;
             uint64_t *bar = clear ? tail : &full[s];
             uint8_t *st = ring + s * kTile;
-            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * D * 2);
             if (j * per_block >= have + 32) {
                 have += 32;
                 ids = ids_next;
                 ids_next = fetch(have + 32 + lane);
             }
-            // a single tile's V comes one block after the next K: its ids may have been passed
-            const int c = lane / (D / 64), half = lane % (D / 64);
-            int page = __shfl_sync(~0u, ids, (j * per_block + c - have) & 31);
-            if (j * per_block < have && c < copies) page = fetch(j * per_block + c);
-            if (c < copies) {
-                if (page < 0 || page >= J.cache.pages) raise_flag(A.err, TRIT_ERR_INDEX);   // reads as zeros
-                tma_page(st + half * (kBlockKeys * 128) + c * rows * 128, is_v ? &vmap : &kmap, half * 64,
-                         key0 - first * ps, h, page, bar);
-            }
+            const int page = __shfl_sync(~0u, ids, (j * per_block + c - have) & 31);
+            if (c < copies && (page < 0 || page >= J.cache.pages)) raise_flag(A.err, TRIT_ERR_INDEX);   // reads as zeros
+            if (!warp_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * D * 2);
+            __syncwarp();
+            if (c < copies)
+                tma_page(st + half * (kBlockKeys * 128) + c * rows * 128, map, half * 64, key0 - first * ps, h, page, bar);
             if (clear) {   // keys past the prefix get P = 0, which must not meet a NaN
-                if (!warp_wait(tail, 0, timed_out)) return false;
+                if (!warp_wait(tail, 0, timed_out)) break;
                 for (int i = lane; i < (kBlockKeys - keys) * (D / 8); i += 32) {
-                    const int r = keys + i / (D / 8), c = i % (D / 8);
-                    *reinterpret_cast<uint4 *>(st + (c / 8) * (kBlockKeys * 128) + r * 128 + (c % 8) * 16) =
+                    const int r = keys + i / (D / 8), ch = i % (D / 8);
+                    *reinterpret_cast<uint4 *>(st + (ch / 8) * (kBlockKeys * 128) + r * 128 + (ch % 8) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
             }
-            return true;
-        };
-        bool ok = pair ? true : load(0, false, 0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (pair) ok = load(j, false, k_at(j));
-            else if (j + 1 < n) ok = load(j + 1, false, k_at(j + 1));
-            ok = ok && load(j, true, v_at(j));
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -392,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ok) issue_s(i + 1);
             }
         }
-    } else if (warp < kMmaWarp) {
+    } else {
         // softmax: stream s, row r of its tile (tensor-memory lane r)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int s = warp >> 2, r = threadIdx.x & 127;
@@ -405,17 +390,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = fr / A.R, rr = fr - b * A.R, t = rr / A.G, g = rr - t * A.G;
             const int64_t mine_at = fr < rows ? (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(h) * A.G + g) * D : -1;
             const int c = lane % CH;
+            uint4 v[CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {       // every load before the first store: one latency
+                const int64_t at = __shfl_sync(~0u, mine_at, j * RI + lane / CH);
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (at >= 0) v[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) + at) + c);
+            }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {       // 32 rows, RI at a time (of a shared tile each stream takes half)
                 if (!pair && (j >= CH / 2) != (s == 1)) continue;
-                const int row = j * RI + lane / CH;
-                const int64_t at = __shfl_sync(~0u, mine_at, row);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (at >= 0) v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) + at) + c);
-                v.x = (v.x & A.keep) ^ A.flip; v.y = (v.y & A.keep) ^ A.flip;
-                v.z = (v.z & A.keep) ^ A.flip; v.w = (v.w & A.keep) ^ A.flip;
-                const int at_row = (warp & 3) * 32 + row;
-                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(at_row, c % 8)) = v;
+                const int row = (warp & 3) * 32 + j * RI + lane / CH;
+                v[j].x = (v[j].x & A.keep) ^ A.flip; v[j].y = (v[j].y & A.keep) ^ A.flip;
+                v[j].z = (v[j].z & A.keep) ^ A.flip; v[j].w = (v[j].w & A.keep) ^ A.flip;
+                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(row, c % 8)) = v[j];
             }
             fence_proxy_async();
             __syncwarp();
@@ -514,8 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m, l);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     }
     tc_fence_before();
     __syncthreads();
