@@ -393,16 +393,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v[CH];
 #pragma unroll
             for (int j = 0; j < CH; ++j) {       // every load before the first store: one latency
+                // (rows that are not there read row 0, without a branch that would wait for each load)
                 const int64_t at = __shfl_sync(~0u, mine_at, j * RI + lane / CH);
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (at >= 0) v[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) + at) + c);
+                v[j] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(J.q) + (at < 0 ? 0 : at)) + c);
             }
 #pragma unroll
             for (int j = 0; j < CH; ++j) {       // 32 rows, RI at a time (of a shared tile each stream takes half)
                 if (!pair && (j >= CH / 2) != (s == 1)) continue;
                 const int row = (warp & 3) * 32 + j * RI + lane / CH;
-                v[j].x = (v[j].x & A.keep) ^ A.flip; v[j].y = (v[j].y & A.keep) ^ A.flip;
-                v[j].z = (v[j].z & A.keep) ^ A.flip; v[j].w = (v[j].w & A.keep) ^ A.flip;
+                const uint32_t keep = tile * kRows + row < rows ? A.keep : 0u;
+                v[j].x = (v[j].x & keep) ^ A.flip; v[j].y = (v[j].y & keep) ^ A.flip;
+                v[j].z = (v[j].z & keep) ^ A.flip; v[j].w = (v[j].w & keep) ^ A.flip;
                 *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRows * 128) + sw128_off(row, c % 8)) = v[j];
             }
             fence_proxy_async();
