@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const int rl = (j * kWarps + warp) * RI + lane / CH, row = lp.tile * RT + rl;
             if (rl >= RT) continue;
             const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
-            const int t = r / G;
+            const int t = token_of(A, r);
             const bool ok = row < rows && t < S.fresh[b];
             const T *q = static_cast<const T *>(J.q);
             if (ok) q += (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(lp.h) * G + r - t * G) * D + c * 8;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     for (int k = 0; k < U; ++k) add_part(ml[k], x[k], base, l, v);
                 }
                 const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
-                const int t = row / G, g = row - t * G;
+                const int t = token_of(A, row), g = row - t * G;
                 const int64_t at = (int64_t(q.b) * J.batch.T + t) * J.q_heads + int64_t(q.h) * G + g;
                 store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                 if (J.lse && c == 0) J.lse[at] = lse_of(m, l);
@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const int rows = p.b < 0 ? B * A.R : A.R;
             tiles = NB == 1 ? 1 : min(NB, (rows - p.tile * RT + 7) >> 3);
             clear = nkeys;
+            const int fresh_own = p.b < 0 ? 0 : S.fresh[p.b];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -589,13 +590,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     const int row = p.tile * RT + n * 8 + 2 * (lane & 3) + e;
                     m[n][e] = -INFINITY;
                     l[n][e] = 0.0f;
-                    lim[n][e] = nkeys;
-                    if (row < rows) {      // the others are never looked at
-                        const int b = p.b < 0 ? row / A.R : p.b, t = (p.b < 0 ? row - b * A.R : row) / G;
-                        const int fresh_n = S.fresh[b], see = nkeys - fresh_n + t + 1;
-                        if (t >= fresh_n || see < 0) lim[n][e] = 0;
-                        else if (p.b >= 0) lim[n][e] = see;
+                    int see = nkeys;
+                    if (p.b >= 0) {
+                        const int t = token_of(A, row);
+                        see = t < fresh_own ? max(nkeys - fresh_own + t + 1, 0) : 0;
+                    } else if (row < rows) {
+                        const int b = row / A.R;
+                        if (token_of(A, row - b * A.R) >= S.fresh[b]) see = 0;
                     }
+                    lim[n][e] = row < rows ? see : nkeys;      // rows that are not there: never looked at
                     clear = min(clear, lim[n][e]);
                 }
 #pragma unroll
@@ -673,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                         sum += f * stats[(w * RT + half * 16 + r) * 2 + 1];
                     }
                     if (direct) {
-                        const int t = row / G, g = row - t * G;
+                        const int t = token_of(A, row), g = row - t * G;
                         const int64_t at = (int64_t(p.b) * J.batch.T + t) * J.q_heads + int64_t(p.h) * G + g;
                         const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
                         store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
@@ -837,6 +840,8 @@ Args layout(const trit_attn_job &J) {
     if (on_tc) prefix_layout(A);
     const int64_t pre_rows = J.batch.prefix_len > 0 && !on_tc ? int64_t(J.batch.B) * A.R : 0;
     const int64_t most_rows = pre_rows > A.R ? pre_rows : A.R;
+    A.g_inv = A.R < 65536 ? uint32_t(((int64_t(1) << 32) + A.G - 1) / A.G) : 0;
+    if (A.G == 1) A.g_inv = 0;
     A.RT = most_rows > 16 ? 32 : most_rows > 8 ? 16 : 8;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);

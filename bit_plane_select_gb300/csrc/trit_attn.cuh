@@ -26,6 +26,7 @@ struct Args {
     float scale2;            // |scale| log2(e) (1 where scale is 0)
     uint32_t flip, keep;     // on pairs of q: the sign of scale, and 0 where it is 0
     int32_t G, R;            // query heads per key head; rows per (sequence, key head)
+    uint32_t g_inv;          // ceil(2^32 / G) where that divides any row exactly, else 0
     int32_t RT;              // rows of an item
     int32_t own_tiles;       // row tiles per (sequence, key head)
     int32_t pre_tiles;       // row tiles of the prefix, per key head (0: no prefix item)
@@ -40,6 +41,11 @@ struct Args {
     int32_t tc_items, tc_splits;   // (head, pair) items, and parts of the keys each is cut into
     float *tc_parts;         // workspace: their partial results, [item][split][stream]
 };
+
+// Row r's token r / G: a high product with ceil(2^32 / G) is exact for r G < 2^32.
+__device__ __forceinline__ int token_of(const Args &A, int r) {
+    return A.g_inv ? int(__umulhi(uint32_t(r), A.g_inv)) : r / A.G;
+}
 
 // A partial result: RT x D sums, then RT pairs (m, l).
 __host__ __device__ inline int64_t part_floats(int RT, int D) { return int64_t(RT) * (D + 2); }
