@@ -149,8 +149,6 @@ def lib():
         L.trit_attn_workspace_bytes.restype = i64
         L.trit_attn_workspace_bytes.argtypes = [p]
         L.trit_attn_paged.argtypes = [p, p, p]
-        L.trit_verify_workspace_bytes.restype = i64
-        L.trit_verify_workspace_bytes.argtypes = [i64]
         L.trit_draft_verify.argtypes = [p, p, p]
         for name in ("trit_pack", "trit_unpack", "trit_verify", "trit_quant_act",
                      "trit_quant_act_many", "trit_gemv", "trit_gemm", "trit_gemm_many",

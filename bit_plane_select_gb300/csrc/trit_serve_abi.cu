@@ -109,20 +109,16 @@ TRIT_API trit_status trit_attn_paged(const trit_attn_job *job, uint32_t *err_fla
     return e == cudaSuccess ? TRIT_OK : abi_cuda_fail(e);
 }
 
-TRIT_API int64_t trit_verify_workspace_bytes(int64_t B) {
-    return B >= 1 && B <= 65535 ? B * 16 : -1;
-}
-
 TRIT_API trit_status trit_draft_verify(const trit_verify_job *job, uint32_t *err_flag,
                                        trit_stream_t stream) {
     if (!job || !err_ok(err_flag)) return TRIT_E_ARG;
     const trit_verify_job &J = *job;
-    if (!J.p || !J.q || !J.draft || !J.u || !J.race || !J.tokens || !J.accepted || !J.workspace || J.flags != 0)
+    if (!J.p || !J.q || !J.draft || !J.u || !J.race || !J.tokens || !J.accepted || J.flags != 0)
         return TRIT_E_ARG;
     if (J.dtype != TRIT_F32 && J.dtype != TRIT_BF16 && J.dtype != TRIT_F16) return TRIT_E_ARG;
     const uintptr_t e = J.dtype == TRIT_F32 ? 4 : 2;
     if (!aligned(J.p, e) || !aligned(J.q, e) || !aligned(J.draft, 4) || !aligned(J.n_draft, 4) || !aligned(J.u, 4) ||
-        !aligned(J.race, 4) || !aligned(J.tokens, 4) || !aligned(J.accepted, 4) || !aligned(J.workspace, 8))
+        !aligned(J.race, 4) || !aligned(J.tokens, 4) || !aligned(J.accepted, 4))
         return TRIT_E_ARG;
     if (J.p_seq_stride < 0 || J.p_tok_stride < 0 || J.q_seq_stride < 0 || J.q_tok_stride < 0 || J.race_stride < 0)
         return TRIT_E_ARG;

@@ -5,24 +5,20 @@
 // CTAs changes nothing in the answer.
 //
 // Bound by reading one row each of p, q and e (12 V bytes per sequence in
-// fp32).  A row is cut into chunks, one CTA each; every CTA finds the first
-// draft not kept by itself (two values per draft, one lane each), and the
-// CTAs of a sequence meet in one 64-bit maximum whose key orders by quotient
-// and then by the lower index.  The last CTA to arrive writes the answer and
-// leaves the workspace zeroed.
+// fp32), or for few sequences by latency.  A cluster of eight CTAs takes a
+// sequence: every CTA finds the first draft not kept by itself (two values per
+// draft, one lane each) while its first race numbers are on their way, reads
+// an eighth of the rows, and hands its best candidate -- a 64-bit key that
+// orders by quotient and then by the lower index -- to the first CTA's shared
+// memory, which writes the answer: no atomics, nothing kept between calls.
 #include "trit_serve.cuh"
 
 namespace trit {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPer = 16;      // values of each row in flight per thread
-
-struct Slot {                  // workspace of one sequence
-    unsigned long long best;   // (quotient bits << 32) | ~index; 0: no candidate yet
-    uint32_t arrived;
-    uint32_t pad_;
-};
+constexpr int kThreads = 512;
+constexpr int kCluster = 8;
+constexpr int kPer = 4;       // vectors of four of each row in flight per thread
 
 template <typename S>
 __device__ __forceinline__ float as_f32(S v);
@@ -33,9 +29,21 @@ __device__ __forceinline__ float as_f32<__half>(__half v) { return __half2float(
 template <>
 __device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// Four values at element 4 i of a row: one load where the row is aligned for it.
+template <typename S, bool VEC>
+__device__ __forceinline__ float4 load4(const S *row, int64_t i) {
+    if (!VEC) return make_float4(as_f32<S>(row[4 * i]), as_f32<S>(row[4 * i + 1]), as_f32<S>(row[4 * i + 2]),
+                                 as_f32<S>(row[4 * i + 3]));
+    if (sizeof(S) == 4) return __ldcs(reinterpret_cast<const float4 *>(row) + i);
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(row) + i);
+    const S *s = reinterpret_cast<const S *>(&v);
+    return make_float4(as_f32<S>(s[0]), as_f32<S>(s[1]), as_f32<S>(s[2]), as_f32<S>(s[3]));
+}
+
 // A lane's best candidate.  The quotient itself is formed only where the value can
 // win: r/e > s needs r > s e, up to three roundings (1 - 2^-22 covers them) and
-// the absolute error of a subnormal product (1e-37 covers it).
+// the absolute error of a subnormal product (1e-37 covers it).  Candidates come in
+// rising order of index, so the lowest of equal ones is kept.
 struct Best {
     float s;
     uint32_t i;
@@ -48,28 +56,40 @@ struct Best {
             }
         }
     }
+    __device__ __forceinline__ void see4(float4 r, float4 e, uint32_t at) {
+        see(r.x, e.x, at);
+        see(r.y, e.y, at + 1);
+        see(r.z, e.z, at + 2);
+        see(r.w, e.w, at + 3);
+    }
 };
 
-template <typename S>
-__device__ Best scan(const S *p, const S *q, const float *e, int64_t from, int64_t to, int tid) {
-    Best best{-1.0f, 0u};
-    for (int64_t i0 = from; i0 < to; i0 += kThreads * kPer) {
-        float r[kPer], w[kPer];
+// Candidates 4 i .. 4 i + 3 for i in [from, to), i = from + tid first; e0 holds the
+// first kPer vectors of e.
+template <typename S, bool VEC>
+__device__ __forceinline__ void scan(Best &best, const S *p, const S *q, const float *e, int64_t from, int64_t to,
+                                     int tid, float4 (&w)[kPer]) {
+    for (int64_t i0 = from + tid; i0 < to; i0 += kThreads * kPer) {
+        float4 a[kPer], b[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int64_t i = i0 + k * kThreads + tid;
-            r[k] = 0.0f;
-            w[k] = 1.0f;
-            if (i < to) {
-                r[k] = as_f32<S>(p[i]);
-                if (q) r[k] -= as_f32<S>(q[i]);
-                w[k] = e[i];
-            }
+            const int64_t i = i0 + k * kThreads < to ? i0 + k * kThreads : i0;   // again, not past the end
+            a[k] = load4<S, VEC>(p, i);
+            b[k] = q ? load4<S, VEC>(q, i) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) best.see(r[k], w[k], uint32_t(i0 + k * kThreads + tid));
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t i = i0 + k * kThreads < to ? i0 + k * kThreads : i0;
+            a[k].x -= b[k].x; a[k].y -= b[k].y; a[k].z -= b[k].z; a[k].w -= b[k].w;
+            best.see4(a[k], w[k], uint32_t(4 * i));
+        }
+        const int64_t next = i0 + kThreads * kPer;
+        if (next < to) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                w[k] = load4<float, VEC>(e, next + k * kThreads < to ? next + k * kThreads : next);
+        }
     }
-    return best;
 }
 
 __device__ __forceinline__ unsigned long long key_of(const Best &b) {
@@ -85,22 +105,36 @@ __device__ unsigned long long block_max(unsigned long long k, unsigned long long
     }
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = k;
     __syncthreads();
-    k = sh[0];
+    k = sh[threadIdx.x & (kThreads / 32 - 1)];
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) k = sh[w] > k ? sh[w] : k;
+    for (int o = kThreads / 64; o; o >>= 1) {
+        const unsigned long long v = __shfl_xor_sync(~0u, k, o);
+        k = v > k ? v : k;
+    }
     __syncthreads();
     return k;
 }
 
-template <typename S>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ trit_verify_job J,
-                                                          uint32_t *err, int64_t chunk) {
+template <typename S, bool VEC>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
+    verify_kernel(const __grid_constant__ trit_verify_job J, uint32_t *err) {
     __shared__ unsigned long long sh[kThreads / 32];
+    __shared__ unsigned long long keys[kCluster];     // in the first CTA: one per CTA
     __shared__ int sh_kept;
-    __shared__ bool sh_last;
-    const int b = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, tid = threadIdx.x;
+    pdl_wait();
+    pdl_launch();
     const S *P = static_cast<const S *>(J.p) + b * J.p_seq_stride;
     const S *Q = static_cast<const S *>(J.q) + b * J.q_seq_stride;
+    const float *e = J.race + b * J.race_stride;
+    const int64_t quads = J.V / 4, from = quads * rank / kCluster, to = quads * (rank + 1) / kCluster;
+    float4 w[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int64_t i = from + tid + k * kThreads;
+        w[k] = make_float4(1.f, 1.f, 1.f, 1.f);
+        if (from + tid < to) w[k] = load4<float, VEC>(e, i < to ? i : from + tid);
+    }
     int n = J.n_draft ? J.n_draft[b] : J.T;
     if (n < 0 || n > J.T) {
         if (tid == 0) raise_flag(err, TRIT_ERR_INDEX);
@@ -113,10 +147,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             bool keep = false;
             if (t < n) {
                 const int x = J.draft[int64_t(b) * J.T + t];
+                const float u = J.u[int64_t(b) * J.T + t];
                 if (x >= 0 && x < J.V) {
                     const float px = as_f32<S>(P[t * J.p_tok_stride + x]);
                     const float qx = as_f32<S>(Q[t * J.q_tok_stride + x]);
-                    keep = __fmul_rn(J.u[int64_t(b) * J.T + t], qx) < px;
+                    keep = __fmul_rn(u, qx) < px;
                 } else {
                     raise_flag(err, TRIT_ERR_INDEX);
                 }
@@ -130,20 +165,28 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     const int kept = sh_kept;
     const S *p = P + kept * J.p_tok_stride;
     const S *q = kept < n ? Q + kept * J.q_tok_stride : nullptr;
-    const float *e = J.race + b * J.race_stride;
-    const int64_t from = blockIdx.x * chunk, to = from + chunk < J.V ? from + chunk : J.V;
-    unsigned long long key = block_max(key_of(scan<S>(p, q, e, from, to, tid)), sh);
-    Slot *slot = static_cast<Slot *>(J.workspace) + b;
-    if (tid == 0) {
-        if (key) atomicMax(&slot->best, key);
-        __threadfence();
-        sh_last = atomicAdd(&slot->arrived, 1u) + 1 == gridDim.x;
+    Best best{-1.0f, 0u};
+    scan<S, VEC>(best, p, q, e, from, to, tid, w);
+    if (rank == kCluster - 1 && tid < J.V - 4 * quads) {      // the last V % 4
+        const int64_t i = 4 * quads + tid;
+        best.see(as_f32<S>(p[i]) - (q ? as_f32<S>(q[i]) : 0.0f), e[i], uint32_t(i));
     }
-    __syncthreads();
-    if (!sh_last) return;
-    __threadfence();
-    key = *reinterpret_cast<volatile unsigned long long *>(&slot->best);
-    if (key == 0 && q) key = block_max(key_of(scan<S>(p, nullptr, e, 0, J.V, tid)), sh);
+    unsigned long long key = block_max(key_of(best), sh);
+    if (tid == 0) {
+        uint32_t to_first;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_first) : "r"(uint32_t(__cvta_generic_to_shared(&keys[rank]))));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to_first), "l"(key) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+    key = 0;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) key = keys[k] > key ? keys[k] : key;
+    if (key == 0 && q) {      // the residual is empty: p decides
+        best = Best{-1.0f, 0u};
+        for (int64_t i = tid; i < J.V; i += kThreads) best.see(as_f32<S>(p[i]), e[i], uint32_t(i));
+        key = block_max(key_of(best), sh);
+    }
     for (int t = tid; t <= J.T; t += kThreads) {
         int v = -1;
         if (t < kept) v = J.draft[int64_t(b) * J.T + t];
@@ -153,28 +196,26 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (tid == 0) {
         J.accepted[b] = kept;
         if (!key) raise_flag(err, TRIT_ERR_EMPTY);
-        slot->best = 0;
-        slot->arrived = 0;
     }
+}
+
+template <typename S>
+cudaError_t launch(const trit_verify_job &J, uint32_t *err, cudaStream_t s) {
+    // vectors of four where every row starts on one
+    auto on = [](const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+    const bool vec = on(J.p, 4 * sizeof(S)) && on(J.q, 4 * sizeof(S)) && on(J.race, 16) &&
+                     ((J.p_seq_stride | J.p_tok_stride | J.q_seq_stride | J.q_tok_stride | J.race_stride) & 3) == 0;
+    const dim3 grid(unsigned(J.B) * kCluster), block(kThreads);
+    return vec ? launch_pdl(verify_kernel<S, true>, grid, block, 0, s, J, err)
+               : launch_pdl(verify_kernel<S, false>, grid, block, 0, s, J, err);
 }
 
 }  // namespace
 
 cudaError_t launch_draft_verify(const trit_verify_job &J, uint32_t *err, cudaStream_t s) {
-    const int64_t step = kThreads * kPer;
-    const int64_t most = (J.V + step - 1) / step;                    // chunks of one load round
-    int64_t chunks = (int64_t(device_sm_count()) * 8 + J.B - 1) / J.B;
-    if (chunks > most) chunks = most;
-    const int64_t rounds = (most + chunks - 1) / chunks;
-    const int64_t chunk = rounds * step;
-    const dim3 grid(unsigned((J.V + chunk - 1) / chunk), unsigned(J.B));
-    if (J.dtype == TRIT_F32)
-        verify_kernel<float><<<grid, kThreads, 0, s>>>(J, err, chunk);
-    else if (J.dtype == TRIT_BF16)
-        verify_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(J, err, chunk);
-    else
-        verify_kernel<__half><<<grid, kThreads, 0, s>>>(J, err, chunk);
-    return cudaGetLastError();
+    return J.dtype == TRIT_F32    ? launch<float>(J, err, s)
+           : J.dtype == TRIT_BF16 ? launch<__nv_bfloat16>(J, err, s)
+                                  : launch<__half>(J, err, s);
 }
 
 }  // namespace trit

@@ -17,7 +17,7 @@ from . import _check, _dev, _stream, lib
 
 __all__ = ["KvCache", "KvBatch", "Rope", "AppendJob", "AttnJob", "VerifyJob", "TritKvCache",
            "TritKvBatch", "TritKvAppendJob", "TritAttnJob", "TritVerifyJob", "trit_kv_append",
-           "trit_attn_paged", "trit_attn_workspace_bytes", "trit_draft_verify", "trit_verify_workspace_bytes", "ERR_INDEX", "ERR_EMPTY",
+           "trit_attn_paged", "trit_attn_workspace_bytes", "trit_draft_verify", "ERR_INDEX", "ERR_EMPTY",
            "ROPE_PAIRS", "MAX_SEQUENCES"]
 
 ERR_INDEX = 32
@@ -58,7 +58,7 @@ class TritAttnJob(ctypes.Structure):
 
 class TritVerifyJob(ctypes.Structure):
     _fields_ = [("p", _p), ("q", _p), ("draft", _p), ("n_draft", _p), ("u", _p), ("race", _p),
-                ("tokens", _p), ("accepted", _p), ("workspace", _p), ("p_seq_stride", _i64),
+                ("tokens", _p), ("accepted", _p), ("p_seq_stride", _i64),
                 ("p_tok_stride", _i64), ("q_seq_stride", _i64), ("q_tok_stride", _i64),
                 ("race_stride", _i64), ("V", _i64), ("B", _i32), ("T", _i32), ("dtype", _i32),
                 ("flags", _u32)]
@@ -253,10 +253,6 @@ def trit_attn_paged(job: AttnJob, err_flag: torch.Tensor, stream=None):
     return job.out
 
 
-def trit_verify_workspace_bytes(B: int) -> int:
-    return int(lib().trit_verify_workspace_bytes(B))
-
-
 class VerifyJob(_Job):
     """The arguments of trit_draft_verify: target probabilities p [B, T+1, V]
     and draft probabilities q [B, T, V] (fp32, bf16 or fp16), draft [B, T] int32,
@@ -269,14 +265,11 @@ class VerifyJob(_Job):
         dt, i32, f32 = (q.dtype,), (torch.int32,), (torch.float32,)
         if q.dtype not in _DTYPE:
             raise ValueError("q must be float32, bfloat16 or float16")
-        if trit_verify_workspace_bytes(B) < 0:
-            raise ValueError(f"{B} sequences: at most 65535 are supported")
-        self.workspace = _workspace(trit_verify_workspace_bytes(B), q.device)
         self.tokens, self.accepted = tokens, accepted
         c = TritVerifyJob(_ptr(p, "p", dt, (B, T + 1, V)), _ptr(q, "q", dt), _whole(draft, "draft", i32, (B, T)),
                           _whole(n_draft, "n_draft", i32, (B,), True), _whole(u, "u", f32, (B, T)),
                           _ptr(race, "race", f32, (B, V)), _whole(tokens, "tokens", i32, (B, T + 1)),
-                          _whole(accepted, "accepted", i32, (B,)), self.workspace.data_ptr(),
+                          _whole(accepted, "accepted", i32, (B,)),
                           p.stride(0), p.stride(1), q.stride(0), q.stride(1), race.stride(0), V, B, T,
                           _DTYPE[q.dtype], 0)
         self._bind(c, p, q, draft, u, race, tokens, accepted, n_draft)

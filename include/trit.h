@@ -699,8 +699,6 @@ TRIT_API trit_status trit_attn_paged(const trit_attn_job *job, uint32_t *err_fla
  *   draft [B][T] int32, n_draft [B] int32 or NULL (T), u [B][T] fp32, race [B][V] fp32
  *   tokens   [B][T+1] int32 out: the kept drafts, the next token, then -1
  *   accepted [B] int32 out: how many were kept
- *   workspace  trit_verify_workspace_bytes(B) bytes, 8-byte aligned, zeroed once
- *        before its first use; every call leaves it zeroed.
  * A draft outside [0, V) is not kept and an n_draft outside [0, T] is clamped,
  * both with TRIT_ERR_INDEX; a sequence without any candidate gets the token -1
  * and TRIT_ERR_EMPTY.
@@ -713,7 +711,6 @@ typedef struct trit_verify_job {
     const float *race;
     int32_t *tokens;
     int32_t *accepted;
-    void *workspace;
     int64_t p_seq_stride, p_tok_stride;   /* elements */
     int64_t q_seq_stride, q_tok_stride;
     int64_t race_stride;                  /* elements between sequences */
@@ -722,7 +719,6 @@ typedef struct trit_verify_job {
     int32_t dtype;
     uint32_t flags;                       /* must be 0 */
 } trit_verify_job;
-TRIT_API int64_t trit_verify_workspace_bytes(int64_t B);
 TRIT_API trit_status trit_draft_verify(const trit_verify_job *job, uint32_t *err_flag,
                                        trit_stream_t stream);
 

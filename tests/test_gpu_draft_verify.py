@@ -47,14 +47,13 @@ def check(t, p, q, draft, u, race, n=None, pad=0, twice=True):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     nd = None if n is None else torch.tensor(n, dtype=torch.int32, device="cuda")
     job = t.VerifyJob(strided(p), strided(q), draft.cuda(), u.cuda(), strided(race), tokens, accepted, n_draft=nd)
-    for _ in range(2 if twice else 1):       # the workspace is left ready for the next call
+    for _ in range(2 if twice else 1):
         t.trit_draft_verify(job, err)
     torch.cuda.synchronize()
     for b in range(B):
         nb = T if n is None else min(max(n[b], 0), T)
         want, k = ref.verify(p[b], q[b], draft[b], u[b], race[b], nb)
         assert tokens[b].tolist() == want and int(accepted[b]) == k, b
-    assert not bool(job.workspace.any())
     return int(err.item())
 
 

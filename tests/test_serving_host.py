@@ -125,7 +125,7 @@ def test_verify_refusals(trit):
     fn = trit.lib().trit_draft_verify
 
     def job(**kw):
-        a = dict(p=P, q=P, draft=P, n_draft=NULL, u=P, race=P, tokens=P, accepted=P, workspace=P,
+        a = dict(p=P, q=P, draft=P, n_draft=NULL, u=P, race=P, tokens=P, accepted=P,
                  p_seq_stride=500, p_tok_stride=100, q_seq_stride=400, q_tok_stride=100, race_stride=100, V=100,
                  B=2, T=4, dtype=0, flags=0)
         a.update(kw)
@@ -133,13 +133,12 @@ def test_verify_refusals(trit):
     half = ctypes.c_void_p((1 << 16) + 2)
     for kw, code in [(dict(p=NULL), ARG), (dict(q=NULL), ARG), (dict(draft=NULL), ARG), (dict(u=NULL), ARG),
                      (dict(race=NULL), ARG), (dict(tokens=NULL), ARG), (dict(accepted=NULL), ARG),
-                     (dict(workspace=NULL), ARG), (dict(workspace=ODD), ARG), (dict(p=half), ARG),
+                     (dict(accepted=NULL), ARG), (dict(p=half), ARG),
                      (dict(dtype=3), ARG), (dict(flags=1), ARG), (dict(p_tok_stride=-1), ARG), (dict(V=0), SHAPE),
                      (dict(B=0), SHAPE), (dict(B=65536), SHAPE), (dict(T=0), SHAPE), (dict(V=1 << 31), SHAPE)]:
         assert fn(ctypes.byref(job(**kw)), P, NULL) == code, kw
     assert fn(ctypes.byref(job()), NULL, NULL) == ARG
     assert fn(None, P, NULL) == ARG
-    assert trit.trit_verify_workspace_bytes(7) == 112 and trit.trit_verify_workspace_bytes(0) == -1
 
 
 def test_python_checks(trit):
