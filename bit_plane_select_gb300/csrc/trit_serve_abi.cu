@@ -80,7 +80,10 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
         return TRIT_E_ARG;
     if (J.rot < 0 || J.rot > J.cache.head_dim || J.rot % 8 || J.max_pos < 0 || (J.q && !heads_ok(J.q_heads, J.cache)))
         return TRIT_E_SHAPE;
-    if (int64_t(J.batch.B) * J.batch.T > (int64_t(1) << 24)) return TRIT_E_SHAPE;
+    // a warp per token and five vectors: counted in 32 bits
+    if (int64_t(J.batch.B) * J.batch.T > (int64_t(1) << 24) ||
+        int64_t(J.batch.B) * J.batch.T * ((J.q ? J.q_heads : 0) + 2 * J.cache.heads) > (int64_t(1) << 31))
+        return TRIT_E_SHAPE;
     if ((J.q_gain || J.k_gain) && (!isfinite(J.eps) || J.eps < 0.0f)) return TRIT_E_SCALE;
     st = abi_check_device();
     if (st != TRIT_OK) return st;

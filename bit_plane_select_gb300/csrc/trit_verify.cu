@@ -16,9 +16,12 @@
 namespace trit {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kCluster = 8;
-constexpr int kPer = 4;       // vectors of four of each row in flight per thread
+// Vectors of four of each row in flight per thread; 256 threads, six CTAs per SM
+// (192 sequences of 131072: 48.7 us; 512 threads, four vectors, two CTAs: 58.5 -- a
+// CTA reads nothing but race numbers until it knows its rows, so others have to)
+constexpr int kPer = 2;
 
 template <typename S>
 __device__ __forceinline__ float as_f32(S v);
@@ -116,7 +119,7 @@ __device__ unsigned long long block_max(unsigned long long k, unsigned long long
 }
 
 template <typename S, bool VEC>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6)
     verify_kernel(const __grid_constant__ trit_verify_job J, uint32_t *err) {
     __shared__ unsigned long long sh[kThreads / 32];
     __shared__ unsigned long long keys[kCluster];     // in the first CTA: one per CTA

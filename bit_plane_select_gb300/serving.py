@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dev, _stream, lib
+from . import _check, lib
 
 __all__ = ["KvCache", "KvBatch", "Rope", "AppendJob", "AttnJob", "VerifyJob", "TritKvCache",
            "TritKvBatch", "TritKvAppendJob", "TritAttnJob", "TritVerifyJob", "trit_kv_append",
@@ -174,10 +174,23 @@ def _token_rows(t, name, dtypes, B, T, heads, D):
 
 
 class _Job:
-    def _bind(self, c, *keep):
+    def _bind(self, name, device, c, *keep):
         self.c = c
-        self.ref = ctypes.c_void_p(ctypes.addressof(c))
+        self._name = name
+        self._fn = getattr(lib(), name)
+        self._at = ctypes.addressof(c)
+        self._device = device.index
         self._keep = keep
+
+    def _call(self, err_flag, stream):
+        """Launch on `stream` or the device's current stream (the raw handle: a
+        Stream object per call would cost as much as the launch)."""
+        if err_flag.dtype is not torch.int32 or not err_flag.is_cuda:
+            raise ValueError("err_flag must be an int32 CUDA tensor")
+        s = torch._C._cuda_getCurrentRawStream(self._device) if stream is None else stream.cuda_stream
+        status = self._fn(self._at, err_flag.data_ptr(), s)
+        if status:
+            _check(status, self._name)
 
 
 class AppendJob(_Job):
@@ -204,14 +217,13 @@ class AppendJob(_Job):
                             rope.max_pos, rope.eps, hq, rope.rot, _DTYPE[src],
                             ROPE_PAIRS if rope.pairs else 0, 0)
         self.q_out = q_out
-        self._bind(c, cache, batch, rope, q, k, v, q_out)
+        self._bind("trit_kv_append", k.device, c, cache, batch, rope, q, k, v, q_out)
 
 
 def trit_kv_append(job: AppendJob, err_flag: torch.Tensor, stream=None):
     """Norm and rotate the new tokens' q and k, write q to q_out and k, v to their
     cache slots (one launch).  Returns q_out."""
-    _check(lib().trit_kv_append(job.ref, _dev(err_flag, torch.int32, "err_flag"), _stream(stream)),
-           "trit_kv_append")
+    job._call(err_flag, stream)
     return job.q_out
 
 
@@ -243,13 +255,12 @@ class AttnJob(_Job):
         c.workspace = _whole(workspace, "workspace", (torch.uint8,), workspace.shape)
         c.workspace_bytes = workspace.numel()
         self.out, self.lse, self.workspace = out, lse, workspace
-        self._bind(c, cache, batch, q, out, lse, workspace)
+        self._bind("trit_attn_paged", q.device, c, cache, batch, q, out, lse, workspace)
 
 
 def trit_attn_paged(job: AttnJob, err_flag: torch.Tensor, stream=None):
     """Attention of the new tokens to the keys they see.  Returns out."""
-    _check(lib().trit_attn_paged(job.ref, _dev(err_flag, torch.int32, "err_flag"), _stream(stream)),
-           "trit_attn_paged")
+    job._call(err_flag, stream)
     return job.out
 
 
@@ -272,11 +283,10 @@ class VerifyJob(_Job):
                           _whole(accepted, "accepted", i32, (B,)),
                           p.stride(0), p.stride(1), q.stride(0), q.stride(1), race.stride(0), V, B, T,
                           _DTYPE[q.dtype], 0)
-        self._bind(c, p, q, draft, u, race, tokens, accepted, n_draft)
+        self._bind("trit_draft_verify", q.device, c, p, q, draft, u, race, tokens, accepted, n_draft)
 
 
 def trit_draft_verify(job: VerifyJob, err_flag: torch.Tensor, stream=None):
     """Keep drafts, draw the token after them.  Returns (tokens, accepted)."""
-    _check(lib().trit_draft_verify(job.ref, _dev(err_flag, torch.int32, "err_flag"), _stream(stream)),
-           "trit_draft_verify")
+    job._call(err_flag, stream)
     return job.tokens, job.accepted

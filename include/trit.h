@@ -624,7 +624,8 @@ typedef struct trit_kv_batch {
  *   q_out     [B][T][Hq][D], the cache's type
  *   cos, sin  [max_pos][rot/2] fp32; may be NULL when rot = 0
  * Pointers 16-byte aligned, token strides multiples of 16 bytes, rot a multiple
- * of 8 with rot <= D.  Asynchronous on `stream`.
+ * of 8 with rot <= D, B*T <= 2^24 and B*T*(Hq + 2 heads) <= 2^31.  Asynchronous
+ * on `stream`.
  */
 #define TRIT_ROPE_PAIRS 1u
 typedef struct trit_kv_append_job {
