@@ -6,17 +6,21 @@
 //
 // A stream of (Hq + 2 Hkv) D values per token, each read once and written
 // once: bound by memory for many tokens and by the latency of three dependent
-// loads (lengths, page id and table rows) for few.  A lane holds four
-// consecutive columns of a vector, so a warp takes 128 columns (one vector of
-// D = 128, two of 64) per step; a rotation partner is then a fixed number of
-// lanes away (rot/2 columns = rot/8 lanes) and the norm is a shuffle sum.
+// loads (lengths, page id and table rows) for few.  A lane holds eight (four)
+// consecutive columns of a vector, so a warp takes two vectors of D = 128 per
+// step, four of 64; a rotation partner is then a fixed number of lanes away
+// (rot/2 columns) and the norm is a shuffle sum.  Instructions count as well: at
+// 32768 tokens of 30 vectors with norms, four columns a lane took 168 us and eight
+// take 121 (6.4 TB/s).
 #include "trit_serve.cuh"
 
 namespace trit {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kGroups = 5;    // vector groups of a warp, all in flight together
+// Warp steps of a warp, all in flight together (measured at 32768 tokens of 30 vectors,
+// eight columns a lane: 2 steps 148 us, 3 steps 130, 5 steps 121).
+constexpr int kGroups = 5;
 
 struct AppendArgs {
     trit_kv_append_job J;
@@ -25,34 +29,48 @@ struct AppendArgs {
     int32_t page_shift;  // log2(page_size), or -1
 };
 
-template <typename S>
-struct Src;
-template <>
-struct Src<float> {
-    static __device__ __forceinline__ float4 load4(const float *p) {
-        return __ldg(reinterpret_cast<const float4 *>(p));
+// W consecutive values of a row, and their store.
+template <int W>
+__device__ __forceinline__ void load_row(const float *p, float (&x)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
+        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
     }
-};
-template <typename H>
-struct Src16 {
-    static __device__ __forceinline__ float4 load4(const H *p) {
+}
+template <int W, typename H>
+__device__ __forceinline__ void load_row(const H *p, float (&x)[W]) {
+    uint32_t w[W / 2];
+    if (W == 8) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = v.x; w[1] = v.y; w[W / 2 - 2] = v.z; w[W / 2 - 1] = v.w;
+    } else {
         const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        const float2 a = unpack16<H>(v.x), b = unpack16<H>(v.y);
-        return make_float4(a.x, a.y, b.x, b.y);
+        w[0] = v.x; w[1] = v.y;
     }
-};
-template <>
-struct Src<__half> : Src16<__half> {};
-template <>
-struct Src<__nv_bfloat16> : Src16<__nv_bfloat16> {};
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+        const float2 f = unpack16<H>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_row(T *p, const float (&y)[W]) {
+    uint32_t w[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) w[i] = pack16<T>(y[2 * i], y[2 * i + 1]);
+    if (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
 
-template <typename T, typename S, int D, bool PAIRS>
+template <typename T, typename S, int D, bool PAIRS, int W>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs A) {
     const trit_kv_append_job &J = A.J;
-    constexpr int L = D / 4;             // lanes of one head vector
+    constexpr int L = D / W;             // lanes of one head vector
     constexpr int V = 32 / L;            // vectors of a warp step
     const int lane = threadIdx.x & 31, sub = lane % L, which = lane / L;
-    const int warp = int(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);    // < 2^24 tokens * chunks
+    const int warp = int(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);    // < 2^31
     const int token = warp / A.chunks;
     pdl_wait();
     pdl_launch();
@@ -60,20 +78,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int first = (warp - token * A.chunks) * kGroups;
     const int b = token / J.batch.T, t = token - b * J.batch.T;
     const int Hq = J.q ? J.q_heads : 0, Hkv = J.cache.heads, all = Hq + 2 * Hkv;
-    const int j0 = sub * 4, half = J.rot / 2;
+    const int j0 = sub * W, half = J.rot / 2;
 
     // every value first: the rest of the token's loads depend on one another
-    float4 x[kGroups];
+    const S *qp = static_cast<const S *>(J.q) + token * J.q_stride + j0;
+    const S *kp = static_cast<const S *>(J.k) + token * J.k_stride + j0 - Hq * D;
+    const S *vp = static_cast<const S *>(J.v) + token * J.v_stride + j0 - (Hq + Hkv) * D;
+    float x[kGroups][W];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         int h = (first + g) * V + which;                    // vector of the token: q, k, v heads in turn
         h = h < all ? h : all - 1;
-        const bool is_q = h < Hq, is_k = h < Hq + Hkv;
-        const int hk = h - Hq - (is_k ? 0 : Hkv);
-        const S *p = is_q ? static_cast<const S *>(J.q) + token * J.q_stride + h * D
-                   : is_k ? static_cast<const S *>(J.k) + token * J.k_stride + hk * D
-                          : static_cast<const S *>(J.v) + token * J.v_stride + hk * D;
-        x[g] = Src<S>::load4(p + j0);
+        load_row<W>((h < Hq ? qp : h < Hq + Hkv ? kp : vp) + h * D, x[g]);
     }
 
     // where the token goes
@@ -83,22 +99,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     bool ok = t < n;
     int64_t slot_at = 0;
     const bool turns = j0 < J.rot;
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int CW = PAIRS ? W / 2 : W;
+    float c[CW], s[CW];
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        c[i] = 1.0f;
+        s[i] = 0.0f;
+    }
     if (ok) {
         const bool in = own >= 0 && (J.rot == 0 || pos < J.max_pos);
         // the lane's angles, and the page beside them
         if (in && turns) {
-            if (PAIRS) {
-                const float2 cc = __ldg(reinterpret_cast<const float2 *>(J.cos + pos * half + j0 / 2));
-                const float2 ss = __ldg(reinterpret_cast<const float2 *>(J.sin + pos * half + j0 / 2));
-                c[0] = c[1] = cc.x; c[2] = c[3] = cc.y;
-                s[0] = s[1] = ss.x; s[2] = s[3] = ss.y;
+            const int64_t at = pos * half + (PAIRS ? j0 / 2 : j0 < half ? j0 : j0 - half);
+            if (CW == 2) {
+                const float2 cc = __ldg(reinterpret_cast<const float2 *>(J.cos + at));
+                const float2 ss = __ldg(reinterpret_cast<const float2 *>(J.sin + at));
+                c[0] = cc.x; c[1] = cc.y;
+                s[0] = ss.x; s[1] = ss.y;
             } else {
-                const int j = j0 < half ? j0 : j0 - half;
-                const float4 cc = __ldg(reinterpret_cast<const float4 *>(J.cos + pos * half + j));
-                const float4 ss = __ldg(reinterpret_cast<const float4 *>(J.sin + pos * half + j));
-                c[0] = cc.x; c[1] = cc.y; c[2] = cc.z; c[3] = cc.w;
-                s[0] = ss.x; s[1] = ss.y; s[2] = ss.z; s[3] = ss.w;
+                load_row<CW < 4 ? 4 : CW>(J.cos + at, reinterpret_cast<float(&)[CW < 4 ? 4 : CW]>(c));
+                load_row<CW < 4 ? 4 : CW>(J.sin + at, reinterpret_cast<float(&)[CW < 4 ? 4 : CW]>(s));
             }
         }
         const int64_t col = own < 0 ? -1 : A.page_shift >= 0 ? own >> A.page_shift : own / J.cache.page_size;
@@ -108,65 +128,75 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if (!ok) raise_flag(A.err, TRIT_ERR_INDEX);
         slot_at = page * J.cache.page_stride + (own - col * J.cache.page_size) * J.cache.slot_stride;
     }
-    // the lane holding the rotation partners, and the sign of their sine
-    const int partner = !turns ? lane : (j0 < half ? lane + half / 4 : lane - half / 4);
-    const float sign = j0 < half ? -1.f : 1.f;
+    // the lane holding the rotation partners, and the sign of their sine (rot / 2 is a
+    // multiple of W here)
+    const int partner = !turns ? lane : (j0 < half ? lane + half / W : lane - half / W);
+    if (!PAIRS && j0 < half) {
+#pragma unroll
+        for (int i = 0; i < CW; ++i) s[i] = -s[i];
+    }
+    T *q_out = static_cast<T *>(J.q_out) + int64_t(token) * Hq * D + j0;
+    T *k_out = static_cast<T *>(J.cache.k) + slot_at + j0;
+    T *v_out = static_cast<T *>(J.cache.v) + slot_at + j0;
 
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         const int h = (first + g) * V + which;
-        const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hkv, live = h < all;
-        const int hk = h - Hq - (is_k ? 0 : Hkv);
-        float4 v = x[g];
-        const float *gain = is_q ? J.q_gain : is_k ? J.k_gain : nullptr;
+        const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
+        float(&v)[W] = x[g];
         if (J.q_gain || J.k_gain) {                         // uniform: every lane shuffles
-            float sum = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+            float sum = v[0] * v[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i) sum = fmaf(v[i], v[i], sum);
 #pragma unroll
             for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            const float *gain = is_q ? J.q_gain : is_v ? nullptr : J.k_gain;
             if (gain) {
-                const float r = __frsqrt_rn(sum * (1.0f / D) + J.eps);
-                const float4 gg = __ldg(reinterpret_cast<const float4 *>(gain + j0));
-                v.x = v.x * r * gg.x; v.y = v.y * r * gg.y; v.z = v.z * r * gg.z; v.w = v.w * r * gg.w;
+                const float r = rsqrtf(sum * (1.0f / D) + J.eps);
+                float gg[W];
+                load_row<W>(gain + j0, gg);
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] = v[i] * r * gg[i];
             }
         }
-        float4 y = v;
         if (PAIRS) {
-            if (turns && (is_q || is_k)) {
-                y.x = v.x * c[0] - v.y * s[0];
-                y.y = v.y * c[1] + v.x * s[1];
-                y.z = v.z * c[2] - v.w * s[2];
-                y.w = v.w * c[3] + v.z * s[3];
+            if (turns && !is_v) {
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) {
+                    const float a0 = v[2 * i], a1 = v[2 * i + 1];
+                    v[2 * i] = a0 * c[i % CW] - a1 * s[i % CW];
+                    v[2 * i + 1] = a1 * c[i % CW] + a0 * s[i % CW];
+                }
             }
         } else {
-            float4 o;
-            o.x = __shfl_sync(~0u, v.x, partner);
-            o.y = __shfl_sync(~0u, v.y, partner);
-            o.z = __shfl_sync(~0u, v.z, partner);
-            o.w = __shfl_sync(~0u, v.w, partner);
-            if (turns && (is_q || is_k)) {
-                y.x = v.x * c[0] + sign * (o.x * s[0]);
-                y.y = v.y * c[1] + sign * (o.y * s[1]);
-                y.z = v.z * c[2] + sign * (o.z * s[2]);
-                y.w = v.w * c[3] + sign * (o.w * s[3]);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float o = __shfl_sync(~0u, v[i], partner);
+                if (turns && !is_v) v[i] = v[i] * c[i % CW] + o * s[i % CW];
             }
         }
-        if (!live || (!ok && !is_q)) continue;
-        if (!ok) y = make_float4(0.f, 0.f, 0.f, 0.f);       // a padding token's query
-        T *out = is_q ? static_cast<T *>(J.q_out) + (int64_t(token) * Hq + h) * D
-                      : static_cast<T *>(is_k ? J.cache.k : J.cache.v) + slot_at + hk * J.cache.head_stride;
-        *reinterpret_cast<uint2 *>(out + j0) = make_uint2(pack16<T>(y.x, y.y), pack16<T>(y.z, y.w));
+        if (h >= all || (!ok && !is_q)) continue;
+        if (!ok) {                                          // a padding token's query
+#pragma unroll
+            for (int i = 0; i < W; ++i) v[i] = 0.0f;
+        }
+        store_row<W>(is_q ? q_out + h * D
+                          : is_v ? v_out + (h - Hq - Hkv) * J.cache.head_stride
+                                 : k_out + (h - Hq) * J.cache.head_stride,
+                     v);
     }
 }
 
 template <typename T, typename S, int D>
-cudaError_t launch_d(const AppendArgs &A, int64_t blocks, cudaStream_t s) {
-    if (A.J.flags & TRIT_ROPE_PAIRS)
-        return launch_pdl(append_kernel<T, S, D, true>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, A);
-    return launch_pdl(append_kernel<T, S, D, false>, dim3(unsigned(blocks)), dim3(kThreads), 0, s, A);
+cudaError_t launch_d(const AppendArgs &A, int W, int64_t blocks, cudaStream_t s) {
+    const dim3 grid{unsigned(blocks)}, block{kThreads};
+    if (A.J.flags & TRIT_ROPE_PAIRS) return launch_pdl(append_kernel<T, S, D, true, 8>, grid, block, 0, s, A);
+    return W == 8 ? launch_pdl(append_kernel<T, S, D, false, 8>, grid, block, 0, s, A)
+                  : launch_pdl(append_kernel<T, S, D, false, 4>, grid, block, 0, s, A);
 }
 template <typename T, typename S>
-cudaError_t launch_s(const AppendArgs &A, int64_t blocks, cudaStream_t s) {
-    return A.J.cache.head_dim == 128 ? launch_d<T, S, 128>(A, blocks, s) : launch_d<T, S, 64>(A, blocks, s);
+cudaError_t launch_s(const AppendArgs &A, int W, int64_t blocks, cudaStream_t s) {
+    return A.J.cache.head_dim == 128 ? launch_d<T, S, 128>(A, W, blocks, s) : launch_d<T, S, 64>(A, W, blocks, s);
 }
 
 }  // namespace
@@ -176,7 +206,9 @@ cudaError_t launch_kv_append(const trit_kv_append_job &J, uint32_t *err, cudaStr
     A.J = J;
     A.err = err;
     const int vectors = (J.q ? J.q_heads : 0) + 2 * J.cache.heads;
-    const int per_step = J.cache.head_dim == 128 ? 1 : 2;
+    // eight columns a lane, except where halves of the rotation do not start on eight
+    const int W = (J.flags & TRIT_ROPE_PAIRS) || J.rot % 16 == 0 ? 8 : 4;
+    const int per_step = 32 * W / J.cache.head_dim;
     const int steps = (vectors + per_step - 1) / per_step;
     A.chunks = (steps + kGroups - 1) / kGroups;
     A.page_shift = -1;
@@ -185,10 +217,10 @@ cudaError_t launch_kv_append(const trit_kv_append_job &J, uint32_t *err, cudaStr
     const int64_t warps = int64_t(J.batch.B) * J.batch.T * A.chunks;
     const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (J.cache.dtype == TRIT_BF16)
-        return J.src_dtype == TRIT_F32 ? launch_s<__nv_bfloat16, float>(A, blocks, s)
-                                       : launch_s<__nv_bfloat16, __nv_bfloat16>(A, blocks, s);
-    return J.src_dtype == TRIT_F32 ? launch_s<__half, float>(A, blocks, s)
-                                   : launch_s<__half, __half>(A, blocks, s);
+        return J.src_dtype == TRIT_F32 ? launch_s<__nv_bfloat16, float>(A, W, blocks, s)
+                                       : launch_s<__nv_bfloat16, __nv_bfloat16>(A, W, blocks, s);
+    return J.src_dtype == TRIT_F32 ? launch_s<__half, float>(A, W, blocks, s)
+                                   : launch_s<__half, __half>(A, W, blocks, s);
 }
 
 }  // namespace trit
