@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
-    const int64_t ctas = W < gridDim.x ? W : gridDim.x;      // that have a share: at least a step each
+    const int64_t ctas = sharing(W, gridDim.x);      // that have a share: at least a step each
     const int64_t lo = blockIdx.x < ctas ? quot(W * blockIdx.x, ctas) : W;
     const int64_t hi = blockIdx.x < ctas ? quot(W * (blockIdx.x + 1), ctas) : W;
 
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     const int c0 = A.cum[b], n = A.cum[b + 1] - c0;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(A.cum[J.batch.B]) * Hkv * A.own_tiles;
-    const int64_t ctas = W < A.grid ? W : A.grid;
+    const int64_t ctas = sharing(W, A.grid);
     const int tile = r / RT, rl = r - tile * RT;
     int64_t first = 0;
     int own = 0;

@@ -60,6 +60,14 @@ __host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
            int64_t(h) * A.pre_tiles + tile;
 }
 
+// How many CTAs of the grid take a share of W steps: one per SM while there is a step
+// for each, more of them from four steps each on (32 sequences of about 500 keys, 1250
+// steps: 21.9 us with 304 CTAs, 27.5 with 456, 26.5 with 152).
+__host__ __device__ inline int64_t sharing(int64_t W, int64_t grid) {
+    const int64_t few = W < kSms ? W : kSms, many = W / 4 > few ? W / 4 : few;
+    return many < grid ? many : grid;
+}
+
 // The CTA whose share [W c / ctas, W (c + 1) / ctas) holds step u of W; ctas <= W,
 // so that no share is empty and an item's CTAs are consecutive.
 // Quotients here are 32-bit wherever the operands are (a 64-bit division takes

@@ -585,11 +585,15 @@ void prefix_layout(Args &A) {
     A.tc_tiles = int((rows + kRows - 1) / kRows);
     A.tc_groups = (A.tc_tiles + 1) / 2;
     A.tc_items = A.tc_groups * J.cache.heads;
-    // Splits by a cost model in us (measured): a CTA costs about 4 and 1.6 per block
-    // of a pair (0.8 of a single tile), the join reads and this kernel writes every part.
-    const bool single = A.tc_tiles == 1;
-    const double per_block = single ? 0.8 : 1.6;
-    const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 8 / 4e6 * (single ? 2 : 1);
+    // Splits by a cost model in us, fitted to sweeps: a CTA costs about 4, and per block
+    // 1.6 for a pair of tiles, 1.2 for one (1.0 and 0.8 where D = 64); every part is
+    // written here and read by the join; and half the CTAs' fixed time is taken
+    // from the sequences' own keys.  (480 rows, 63 blocks: 11, 13, 15 splits 44.5, 43.9, 45.7
+    // us in all; 192 rows of D = 64, 47 blocks: 9, 12, 16 splits 44.6, 43.6, 45.6.)
+    const bool single = A.tc_tiles == 1, wide = J.cache.head_dim == 128;
+    const double per_block = wide ? (single ? 1.2 : 1.6) : (single ? 0.8 : 1.0);
+    const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 8 / 5e6 * (single ? 2 : 1) +
+                             0.5 * 4 * A.tc_items / kSms;
     double best = 0;
     int splits = 0;
     for (int s = 1; s <= nb && s * A.tc_items <= (A.tc_items > kSms ? 4 * A.tc_items : 2 * kSms); ++s) {
