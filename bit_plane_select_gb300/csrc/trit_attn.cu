@@ -837,7 +837,6 @@ Args layout(const trit_attn_job &J) {
     A.G = J.q_heads / J.cache.heads;
     A.R = J.batch.T * A.G;
     const bool on_tc = prefix_on_tensor_cores(J);
-    if (on_tc) prefix_layout(A);
     const int64_t pre_rows = J.batch.prefix_len > 0 && !on_tc ? int64_t(J.batch.B) * A.R : 0;
     const int64_t most_rows = pre_rows > A.R ? pre_rows : A.R;
     A.g_inv = A.R < 65536 ? uint32_t(((int64_t(1) << 32) + A.G - 1) / A.G) : 0;
@@ -855,8 +854,15 @@ Args layout(const trit_attn_job &J) {
                                                    int64_t(J.batch.B) * A.own_tiles * cap);
     int per_sm = int(kSmemPerSm / (smem_of(A) + 1024));   // resident together: no CTA waits for another's end
     if (per_sm > ctas_of(A.RT / 8)) per_sm = ctas_of(A.RT / 8);
-    const int64_t grid = int64_t(kSms) * (per_sm > 0 ? per_sm : 1);
+    if (per_sm < 1) per_sm = 1;
+    const int resident = per_sm;
+    // beside the prefix kernel two are better than three where D = 128 (32 sequences 21.9
+    // against 27.5 us, 256 sequences 174 against 176; D = 64, which computes more per
+    // byte: 50.7 against 46.2; without a prefix: two long sequences 106 against 102)
+    if (on_tc && J.cache.head_dim == 128 && per_sm > 2) per_sm = 2;
+    const int64_t grid = int64_t(kSms) * per_sm;
     A.grid = int(most < grid ? most : grid);
+    if (on_tc) prefix_layout(A, kSms - (A.grid + resident - 1) / resident);
     return A;
 }
 

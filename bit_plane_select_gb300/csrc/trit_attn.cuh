@@ -111,7 +111,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // trit_attn_prefix.cu: whether the prefix runs there, its layout, its launch.
 bool prefix_on_tensor_cores(const trit_attn_job &J);
-void prefix_layout(Args &A);
+void prefix_layout(Args &A, int spare);     // spare: SMs the own keys' grid leaves free
 int64_t prefix_part_bytes(const Args &A);
 cudaError_t launch_prefix(const Args &A, cudaStream_t s);
 

@@ -578,7 +578,7 @@ bool prefix_on_tensor_cores(const trit_attn_job &J) {
     return J.batch.prefix_len > 0 && rows > 32 && pow2 && C.page_size >= 16 && strides;
 }
 
-void prefix_layout(Args &A) {
+void prefix_layout(Args &A, int spare) {
     const trit_attn_job &J = A.J;
     const int64_t rows = int64_t(J.batch.B) * A.R;
     const int nb = int((J.batch.prefix_len + kBlockKeys - 1) / kBlockKeys);
@@ -588,7 +588,9 @@ void prefix_layout(Args &A) {
     // Splits by a cost model in us, fitted to sweeps: a CTA costs about 4, and per block
     // 1.6 for a pair of tiles, 1.2 for one (1.0 and 0.8 where D = 64); every part is
     // written here and read by the join; and half the CTAs' fixed time is taken
-    // from the sequences' own keys.  (480 rows, 63 blocks: 11, 13, 15 splits 44.5, 43.9, 45.7
+    // from the sequences' own keys, as is 4 more where their grid cannot start
+    // beside this one (32 sequences of 5 key heads: 10 splits, 50 CTAs, 23.1 us, 11 splits
+    // 27.1).  (480 rows, 63 blocks: 11, 13, 15 splits 44.5, 43.9, 45.7
     // us in all; 192 rows of D = 64, 47 blocks: 9, 12, 16 splits 44.6, 43.6, 45.6.)
     const bool single = A.tc_tiles == 1, wide = J.cache.head_dim == 128;
     const double per_block = wide ? (single ? 1.2 : 1.6) : (single ? 0.8 : 1.0);
@@ -598,7 +600,8 @@ void prefix_layout(Args &A) {
     int splits = 0;
     for (int s = 1; s <= nb && s * A.tc_items <= (A.tc_items > kSms ? 4 * A.tc_items : 2 * kSms); ++s) {
         const int waves = (s * A.tc_items + kSms - 1) / kSms;
-        const double cost = waves * (4 + (nb + s - 1) / s * per_block) + s * per_split;
+        const double cost = waves * (4 + (nb + s - 1) / s * per_block) + s * per_split +
+                            (s * A.tc_items > spare ? 4 : 0);
         if (splits == 0 || cost < best) {
             best = cost;
             splits = s;
