@@ -273,3 +273,92 @@ class LayerChain:
             b += 4 * no + 4 + 8 * nf                 # gate/up: o's f read, scale, a_gate + a_up
             b += 8 * nf + 4 + 8 * nd                 # down: a_gate + a_up read, scale
         return b
+
+
+class ServedStack:
+    """Ternary layers with attention between their products, for a batch of
+    sequences that decode (or verify drafts) behind a shared prefix.  Per layer:
+      1. norm folded into the quantiser, q, k and v products,
+      2. trit_kv_append: rotation, optional head norms, the cache append,
+      3. trit_attn_paged (fp32 out), quantised, the o product, residual;
+      4. norm folded into the quantiser, gate and up, trit_intmlp_quant, the down
+         product, residual.
+    Each layer owns a paged cache; a plan (see `plan`) holds the buffers and
+    prepared lists of one KvBatch, so the prefix's prompt and the decode steps
+    are two plans over the same caches.
+
+    weights: per layer, name -> (int8 [N, K] tensor, w_scale) for q, k, v, o, gate,
+    up, down, plus "attn_gain" and "mlp_gain" (fp32 [K] norm gains).  rope: a
+    Rope; pages and page_size: of every layer's cache."""
+
+    NAMES = LayerChain.NAMES
+
+    def __init__(self, weights, head_dim: int, rope, pages: int, page_size: int,
+                 dtype=torch.bfloat16, eps: float = 1e-5, device="cuda"):
+        from . import KvCache
+        self.device, self.head_dim, self.rope, self.eps = torch.device(device), head_dim, rope, float(eps)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.layers = []
+        for lw in weights:
+            P, S, shape = {}, {}, {}
+            for name in self.NAMES:
+                w, ws = lw[name]
+                planes, err = trit_pack(w.to(self.device), ws)
+                if int(err.item()) != 0:
+                    raise ValueError(f"{name}: non-ternary weights")
+                P[name], S[name], shape[name] = planes, float(ws), tuple(w.shape)
+            K, F = shape["q"][1], shape["gate"][0]
+            heads = {n: shape[n][0] // head_dim for n in ("q", "k", "v")}
+            if (shape["o"] != (K, shape["q"][0]) or shape["k"] != shape["v"] or shape["gate"] != (F, K) or
+                    shape["up"] != (F, K) or shape["down"] != (K, F) or shape["k"][1] != K or
+                    any(heads[n] * head_dim != shape[n][0] for n in heads)):
+                raise ValueError("layer shapes do not chain")
+            cache = [torch.zeros((pages, heads["k"], page_size, head_dim), dtype=dtype, device=self.device)
+                     for _ in range(2)]
+            gains = [lw[g].to(device=self.device, dtype=torch.float32) for g in ("attn_gain", "mlp_gain")]
+            self.layers.append({"P": P, "S": S, "K": K, "F": F, "heads": heads, "cache": KvCache(*cache),
+                                "attn_gain": gains[0], "mlp_gain": gains[1]})
+
+    def plan(self, batch):
+        """Buffers and prepared calls for the T new tokens of every sequence of `batch`."""
+        from . import AppendJob, AttnJob
+        M, D, dev = batch.B * batch.T, self.head_dim, self.device
+
+        def buf(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+        plan = []
+        for L in self.layers:
+            K, F, hq, hk, P, S = L["K"], L["F"], L["heads"]["q"], L["heads"]["k"], L["P"], L["S"]
+            B = {"x_i8": buf(M, k_pad(K), dtype=torch.int8), "s": buf(M), "a_i8": buf(M, k_pad(hq * D), dtype=torch.int8),
+                 "sa": buf(M), "h_i8": buf(M, k_pad(F), dtype=torch.int8), "sh": buf(M),
+                 "q": buf(M, hq * D), "k": buf(M, hk * D), "v": buf(M, hk * D), "o": buf(M, K), "down": buf(M, K),
+                 "gate": buf(M, F, dtype=torch.int32), "up": buf(M, F, dtype=torch.int32),
+                 "q_rot": buf(batch.B, batch.T, hq, D, dtype=L["cache"].k.dtype), "attn": buf(batch.B, batch.T, hq, D)}
+            B["qkv_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, None, B[n]) for n in "qkv"])
+            B["o_list"] = ProjList([(P["o"], S["o"], B["a_i8"], B["sa"], hq * D, None, B["o"])])
+            B["gu_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, B[n], None) for n in ("gate", "up")])
+            B["down_list"] = ProjList([(P["down"], S["down"], B["h_i8"], B["sh"], F, None, B["down"])])
+            B["append"] = AppendJob(L["cache"], batch, self.rope, B["q"], B["k"], B["v"], B["q_rot"])
+            B["attend"] = AttnJob(L["cache"], batch, B["q_rot"], B["attn"])
+            plan.append(B)
+        return plan
+
+    def step(self, plan, x, stream=None):
+        """x [B*T, K] fp32, the new tokens' rows, through every layer in place."""
+        from . import (trit_attn_paged, trit_intmlp_quant, trit_kv_append, trit_quant_act,
+                       trit_quant_act_folded)
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
+            for L, B in zip(self.layers, plan):
+                trit_quant_act_folded(x, L["attn_gain"], self.eps, B["x_i8"], B["s"], self.err)
+                trit_gemm_many(B["qkv_list"], self.err)
+                trit_kv_append(B["append"], self.err)
+                trit_attn_paged(B["attend"], self.err)
+                trit_quant_act(B["attn"].view(x.shape[0], -1), B["a_i8"], B["sa"], self.err)
+                trit_gemm_many(B["o_list"], self.err)
+                x += B["o"]
+                trit_quant_act_folded(x, L["mlp_gain"], self.eps, B["x_i8"], B["s"], self.err)
+                trit_gemm_many(B["gu_list"], self.err)
+                trit_intmlp_quant(B["gate"], B["up"], L["S"]["gate"], L["S"]["up"], B["s"], B["h_i8"], B["sh"])
+                trit_gemm_many(B["down_list"], self.err)
+                x += B["down"]
+        return x
