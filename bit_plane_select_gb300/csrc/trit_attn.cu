@@ -2,12 +2,13 @@
 // prefix read once for the batch.
 //
 // The keys of every item (trit_attn.cuh) are cut into steps of 64 (128 where D = 64), all steps of
-// the call are laid end to end, and each of a fixed grid of CTAs takes an equal
-// run of them, whatever the lengths (which only the device knows): a CTA's run
-// may end one item, cover several and begin another.  Items a CTA does not
-// finish alone leave partial results, joined by the last of the item's CTAs where
+// the call are laid end to end and cut into equal chunks, whatever the lengths
+// (which only the device knows): one per CTA, or several taken in turn by the CTAs that
+// start while the prefix kernel of trit_attn_prefix.cu still runs.  A chunk
+// may end one item, cover several and begin another.  Items that do not lie in one
+// chunk leave partial results, joined by the last of the item's CTAs where
 // there is no prefix and by a second launch where there is one (a prefix
-// part belongs to many sequences).
+// part belongs to many sequences).  Which CTA takes a chunk changes no result.
 //
 // Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
 // reading K and V: 4 D bytes a key against 4 D R flops.  A step's keys go 16
@@ -281,7 +282,8 @@ constexpr int kStages = 2;
 // CTAs per SM by the row tiles' registers (shared memory allows three).
 __host__ __device__ constexpr int ctas_of(int NB) { return NB <= 2 ? 3 : 2; }
 
-template <typename T, int D, int NB>
+// TURNS: chunks may be taken in turn (the host knows whether they can be).
+template <typename T, int D, int NB, bool TURNS>
 __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int RT = 8 * NB;
@@ -296,8 +298,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     const uint32_t q_at = tc::smem_u32(smem + kWarps * kStages * kStageBytes), q_bytes = RT * D * 2;
     float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes + kQueries * q_bytes);   // [kWarps][RT] (m, l)
     int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
+    volatile int32_t *taken = scratch + kWarps;      // [4]: chunk of this CTA's n-th turn at n % 4
     Batch S;
-    S.cum = scratch + kWarps;
+    S.cum = scratch + kWarps + 4;
     S.len = S.cum + A.J.batch.B + 1;
     S.fresh = S.len + A.J.batch.B;
     const int32_t *cum = S.cum;
@@ -314,13 +317,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
-    const int64_t ctas = sharing(W, gridDim.x);      // that have a share: at least a step each
-    const int64_t lo = blockIdx.x < ctas ? quot(W * blockIdx.x, ctas) : W;
-    const int64_t hi = blockIdx.x < ctas ? quot(W * (blockIdx.x + 1), ctas) : W;
+    // this CTA's first chunk, and the end of the one at hand
+    const int64_t count = chunk_count(A, W);
+    const bool turns = TURNS && lean(A, W);
+    const int64_t lo = blockIdx.x < count ? chunk_start(blockIdx.x, W, count) : W;
+    int64_t hi = blockIdx.x < count ? chunk_start(blockIdx.x + 1, W, count) : W;
 
     // the ring runs ahead of the products, across items: keys and values by stage, and
     // an item's queries with its first stage (each warp a quarter of the rows)
-    int64_t lu = lo;
+    int64_t lu = lo, lhi = hi;
+    int lord = 0;                 // the chunk's number in this CTA
     Place lp = {};
     Keys lk = {};
     Pages lpages = {};
@@ -349,13 +355,24 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         lq = lq + 1 == kQueries ? 0 : lq + 1;
     };
     auto load_next = [&](int stage) {
-        if (lu < hi) {
+        if (lu < lhi) {
             if (lnew) {
                 load_queries();
                 lnew = false;
             }
             load_stage<D>(A, lk, lpages, lp.h, lp.step, warp, ring_at + stage * kStageBytes, lane);
-            if (++lu < hi) {
+            if (++lu == lhi && turns) {
+                ++lord;
+                const int next = taken[lord & 3];
+                if (next < count) {
+                    lu = chunk_start(next, W, count);
+                    lhi = chunk_start(next + 1, W, count);
+                    lp = place_of(A, cum, lu);
+                    lk = keys_of(A, S, lp);
+                    lpages = pages_of<D>(A, lk, lp.step, warp, lane);
+                    lnew = true;
+                }
+            } else if (lu < lhi) {
                 if (++lp.step == lp.steps) {
                     next_item(A, S, lp);
                     lk = keys_of(A, S, lp);
@@ -385,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         }
     }
     if (lo >= hi) {
-        if (A.tc_items) pdl_wait();
+        if (A.tc_items && blockIdx.x == 0) pdl_wait();     // see the end
         return;
     }
 
@@ -393,13 +410,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     // counter per item, left at zero.
     auto join_last = [&](const Place &q, int rows) {
         const int64_t s0 = int64_t(cum[q.b]) * Hkv * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
-        const int64_t c0 = cta_of(s0, W, ctas);
-        const int parts = int(cta_of(s0 + q.steps - 1, W, ctas) - c0) + 1;
-        uint32_t *count = A.count + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
+        const int64_t c0 = chunk_of(s0, W, count);
+        const int parts = int(chunk_of(s0 + q.steps - 1, W, count) - c0) + 1;
+        uint32_t *arrived = A.count + 1 + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
         if (threadIdx.x == 0) {
             __threadfence();
-            const bool last = atomicAdd(count, 1u) + 1 == uint32_t(parts);
-            if (last) *count = 0;
+            const bool last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
+            if (last) *arrived = 0;
             __threadfence();
             scratch[0] = last;
         }
@@ -570,13 +587,29 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     };
 
     int64_t u = lo;
+    // chunks taken in turn: this CTA's second one, and its third on the way
+    int64_t chunk = blockIdx.x, chunk_lo = lo;
+    int ord = 0, ticket = 0;
+    if (turns && threadIdx.x == 0) {
+        taken[1] = int(gridDim.x + atomicAdd(A.count, 1u));
+        ticket = int(gridDim.x + atomicAdd(A.count, 1u));
+    }
     bool fresh = true;
     int stage = 0;
     while (u < hi) {
         tc::cp_async_wait<kStages - 1>();
         if (fresh) {
             fresh = false;
-            if (u != lo) next_item(A, S, p);
+            if (u == chunk_lo) {
+                // a chunk begins (its place is set): the turn after next is known to all
+                // from the barrier below on, a chunk's length before it is needed
+                if (turns && threadIdx.x == 0) {
+                    taken[(ord + 2) & 3] = ticket;
+                    ticket = int(gridDim.x + atomicAdd(A.count, 1u));
+                }
+            } else {
+                next_item(A, S, p);
+            }
             first_step = p.step;
             nkeys = keys_of(A, S, p).n;
             const int rows = p.b < 0 ? B * A.R : A.R;
@@ -628,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const bool whole = starts && ends;
             const bool direct = whole && p.b >= 0 && J.batch.prefix_len == 0;
             const int64_t slot = whole ? (p.b < 0 ? slot_prefix(A, p.h, p.tile) : slot_own(A, p.b, p.h, p.tile))
-                                       : 2 * int64_t(blockIdx.x) + (starts ? 1 : 0);
+                                       : 2 * chunk + (starts ? 1 : 0);
             float *part = A.parts + slot * part_floats(RT, D);
             const int rows = p.b < 0 ? B * A.R : A.R;
 #pragma unroll
@@ -695,11 +728,21 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         load_next(stage);
         if (++stage == kStages) stage = 0;
         ++p.step;
-        ++u;
+        if (++u == hi && turns) {
+            ++ord;
+            const int next = taken[ord & 3];
+            if (next < count) {
+                chunk = next;
+                u = chunk_lo = chunk_start(next, W, count);
+                hi = chunk_start(next + 1, W, count);
+                p = place_of(A, cum, u);
+            }
+        }
     }
     tc::cp_async_wait<0>();
-    // the join reads this grid's partial results and the prefix kernel's: end after both
-    if (A.tc_items) pdl_wait();
+    // the join waits for this grid alone and reads the prefix kernel's results too: one CTA
+    // ends after that kernel
+    if (A.tc_items && blockIdx.x == 0) pdl_wait();
 }
 
 // Joins the partial results of a call with a prefix: four rows of one
@@ -719,20 +762,21 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     const int tid = threadIdx.x % D, part0 = threadIdx.x / D;            // the group's first part
     const int r4 = row4 * 4 + (tid & 3), c = tid >> 2;                    // columns 4c ..
     const int r = r4 < A.R ? r4 : A.R - 1;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = 0;      // the chunks taken, for the next call
     const int t = r / G, g = r - t * G;
 
     // the own item's parts
     const int c0 = A.cum[b], n = A.cum[b + 1] - c0;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(A.cum[J.batch.B]) * Hkv * A.own_tiles;
-    const int64_t ctas = sharing(W, A.grid);
+    const int64_t count = chunk_count(A, W);
     const int tile = r / RT, rl = r - tile * RT;
     int64_t first = 0;
     int own = 0;
     if (n > 0) {
         const int64_t s0 = pre + (int64_t(c0) * Hkv * A.own_tiles) + (int64_t(h) * A.own_tiles + tile) * n;
-        first = cta_of(s0, W, ctas);
-        own = int(cta_of(s0 + n - 1, W, ctas) - first) + 1;
+        first = chunk_of(s0, W, count);
+        own = int(chunk_of(s0 + n - 1, W, count) - first) + 1;
     }
     // the prefix's
     const int64_t fr = int64_t(b) * A.R + r;
@@ -744,14 +788,14 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
         prl = int(fr - int64_t(ptile) * kTcRows);
         pfirst = int64_t(h * A.tc_groups + group) * A.tc_splits * 2 + (pair ? ptile & 1 : 0);
         pstep = pair ? 2 : 1;
-        prefix = pair ? A.tc_splits : 2 * A.tc_splits;
+        prefix = pair ? splits_of(A, W) : 2 * splits_of(A, W);
         if (t >= batch_new(J.batch, b)) prefix = 0;        // padding: that kernel does not look
     } else if (A.pre_tiles) {
         pitem = int(fr) / RT;
         prl = int(fr - int64_t(pitem) * RT);
         const int64_t s0 = (int64_t(h) * A.pre_tiles + pitem) * A.pre_steps;
-        pfirst = cta_of(s0, W, ctas);
-        prefix = int(cta_of(s0 + A.pre_steps - 1, W, ctas) - pfirst) + 1;
+        pfirst = chunk_of(s0, W, count);
+        prefix = int(chunk_of(s0 + A.pre_steps - 1, W, count) - pfirst) + 1;
     }
     const int total = own + prefix;
     float m = -INFINITY, l = 0.0f;
@@ -827,7 +871,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 size_t smem_of(const Args &A) {
     const int D = A.J.cache.head_dim;
     return size_t(kWarps) * kStages * (4 * keys_of_stage(D) * D) + size_t(kStages + 1) * A.RT * D * 2 +
-           kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
+           kWarps * A.RT * 8 + (kWarps + 4) * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
 }
 
 // The work's layout from the job's sizes; the grid that a call would use.
@@ -845,6 +889,7 @@ Args layout(const trit_attn_job &J) {
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
     const int kStep = kWarps * keys_of_stage(J.cache.head_dim);
+    A.own_step = kStep;
     A.pre_steps = on_tc ? 0 : int((J.batch.prefix_len + kStep - 1) / kStep);
     A.page_shift = -1;
     for (int s = 0; s < 31; ++s)
@@ -856,21 +901,24 @@ Args layout(const trit_attn_job &J) {
     if (per_sm > ctas_of(A.RT / 8)) per_sm = ctas_of(A.RT / 8);
     if (per_sm < 1) per_sm = 1;
     const int resident = per_sm;
-    // beside the prefix kernel two are better than three where D = 128 (32 sequences 21.9
-    // against 27.5 us, 256 sequences 174 against 176; D = 64, which computes more per
-    // byte: 50.7 against 46.2; without a prefix: two long sequences 106 against 102)
-    if (on_tc && J.cache.head_dim == 128 && per_sm > 2) per_sm = 2;
     const int64_t grid = int64_t(kSms) * per_sm;
     A.grid = int(most < grid ? most : grid);
-    if (on_tc) prefix_layout(A, kSms - (A.grid + resident - 1) / resident);
+    // beside the prefix kernel two CTAs per SM share short work better than three where
+    // D = 128 (D = 64, which computes more per byte: 50.7 against 46.2 us for 96 sequences;
+    // without a prefix: two long sequences 106 against 102)
+    const int two = 2 * kSms;
+    A.spread = on_tc && J.cache.head_dim == 128 && A.grid > two ? two : A.grid;
+    A.chunks = on_tc ? 4 * A.grid : A.grid;
+    if (on_tc) prefix_layout(A, kSms - (A.spread + resident - 1) / resident, most);
+    if (!A.tc_lean) A.grid = A.chunks = A.spread;     // no chunks in turn
     return A;
 }
 
-// [B + 1] sums of steps, then one counter per own item.
+// [B + 1] sums of steps, then the chunks taken and one counter per own item.
 int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
 int64_t head_bytes(const Args &A) {
     const int64_t items = int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles;
-    return cum_bytes(A.J) + (items * 4 + 255) / 256 * 256;
+    return cum_bytes(A.J) + ((items + 1) * 4 + 255) / 256 * 256;
 }
 
 int64_t part_bytes(const Args &A) {
@@ -883,11 +931,12 @@ int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_
 template <typename T, int D, int NB>
 cudaError_t launch(const Args &A, cudaStream_t s) {
     const size_t smem = smem_of(A);
-    cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    const auto kernel = A.tc_lean ? attn_kernel<T, D, NB, true> : attn_kernel<T, D, NB, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     // the prefix kernel first: the next one depends on nothing of it and may start beside it
     if (A.tc_items) e = launch_prefix(A, s);
-    if (e == cudaSuccess) e = launch_pdl(attn_kernel<T, D, NB>, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
+    if (e == cudaSuccess) e = launch_pdl(kernel, dim3(unsigned(A.grid)), dim3(kThreads), smem, s, A);
     if (e != cudaSuccess) return e;
     if (A.J.batch.prefix_len == 0) return cudaSuccess;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);

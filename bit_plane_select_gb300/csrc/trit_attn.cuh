@@ -31,15 +31,19 @@ struct Args {
     int32_t own_tiles;       // row tiles per (sequence, key head)
     int32_t pre_tiles;       // row tiles of the prefix, per key head (0: no prefix item)
     int32_t pre_steps;       // steps of the prefix
-    int32_t grid;            // CTAs the work is cut over
+    int32_t grid;            // CTAs of the own-keys kernel
+    int32_t spread, chunks;  // most chunks of one each per CTA, and of several
     int32_t page_shift;      // log2(page_size), or -1
     int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
-    uint32_t *count;         // workspace: arrivals per own item, zero between calls
+    uint32_t *count;         // workspace: chunks taken, then arrivals per own item; zero between calls
     float *parts;            // workspace: the partial results
     // the prefix on the tensor cores (tc_items = 0: its items are above, with the own ones)
     int32_t tc_tiles, tc_groups;   // 128-row tiles per key head, and pairs of them
     int32_t tc_items, tc_splits;   // (head, pair) items, and parts of the keys each is cut into
-    float *tc_parts;         // workspace: their partial results, [item][split][stream]
+    int32_t tc_lean;         // the same beside much work of the sequences' own, or 0
+    int64_t tc_lean_from;    // steps from which that is so
+    int32_t own_step;        // keys of an own step
+    float *tc_parts;         // workspace: their partial results, [item][tc_splits][stream]
 };
 
 // Row r's token r / G: a high product with ceil(2^32 / G) is exact for r G < 2^32.
@@ -50,35 +54,47 @@ __device__ __forceinline__ int token_of(const Args &A, int r) {
 // A partial result: RT x D sums, then RT pairs (m, l).
 __host__ __device__ inline int64_t part_floats(int RT, int D) { return int64_t(RT) * (D + 2); }
 
-// Slots of partial results: CTA c's first and last unfinished items at 2c and
-// 2c + 1, then one per own item and per prefix item finished by a single CTA.
+// Slots of partial results: chunk c's first and last unfinished items at 2c and
+// 2c + 1, then one per own item and per prefix item that lies in a single chunk.
 __host__ __device__ inline int64_t slot_own(const Args &A, int b, int h, int tile) {
-    return 2 * int64_t(A.grid) + (int64_t(b) * A.J.cache.heads + h) * A.own_tiles + tile;
+    return 2 * int64_t(A.chunks) + (int64_t(b) * A.J.cache.heads + h) * A.own_tiles + tile;
 }
 __host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
-    return 2 * int64_t(A.grid) + int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles +
+    return 2 * int64_t(A.chunks) + int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles +
            int64_t(h) * A.pre_tiles + tile;
 }
 
-// How many CTAs of the grid take a share of W steps: one per SM while there is a step
-// for each, more of them from four steps each on (32 sequences of about 500 keys, 1250
-// steps: 21.9 us with 304 CTAs, 27.5 with 456, 26.5 with 152).
-__host__ __device__ inline int64_t sharing(int64_t W, int64_t grid) {
-    const int64_t few = W < kSms ? W : kSms, many = W / 4 > few ? W / 4 : few;
-    return many < grid ? many : grid;
-}
-
-// The CTA whose share [W c / ctas, W (c + 1) / ctas) holds step u of W; ctas <= W,
-// so that no share is empty and an item's CTAs are consecutive.
 // Quotients here are 32-bit wherever the operands are (a 64-bit division takes
 // hundreds of SM-clocks).
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
     return a / b;
 }
-__device__ __forceinline__ int64_t cta_of(int64_t u, int64_t W, int64_t ctas) {
-    return quot((u + 1) * ctas - 1, W);
+
+// Where the sequences' own keys take at least as long as the prefix, the prefix kernel
+// runs on about half of the SMs (tc_lean parts per item instead of tc_splits) and the
+// own keys' chunks are taken in turn, by the CTAs beside it first and by those that
+// start as it ends: its tensor work then runs under their memory traffic (256 sequences of
+// about 850 keys behind 32768: 150 us against 174).  W is known on the device
+// only; every kernel decides alike.
+__device__ __forceinline__ bool lean(const Args &A, int64_t W) { return A.tc_lean > 0 && W >= A.tc_lean_from; }
+__device__ __forceinline__ int splits_of(const Args &A, int64_t W) { return lean(A, W) ? A.tc_lean : A.tc_splits; }
+
+// How many chunks W steps are cut into: chunk c of n is [W c / n, W (c + 1) / n), n <= W, so
+// that none is empty and an item's chunks are consecutive.
+//  - One chunk per CTA: one CTA per SM while there is a step for each, more of them
+//    from four steps each on (32 sequences of about 500 keys behind a prefix, 1250
+//    steps: 21.9 us with 304 CTAs, 27.5 with 456, 26.5 with 152; four steps a chunk,
+//    taken in turn: 37).
+//  - Beside a lean prefix kernel (below): chunks of 16 steps, taken in turn.
+__device__ __forceinline__ int64_t chunk_count(const Args &A, int64_t W) {
+    int64_t n = W / 4 > kSms ? W / 4 : kSms;
+    if (n > A.spread) n = A.spread;
+    if (lean(A, W)) n = W / 16 < A.chunks ? W / 16 : A.chunks;
+    return n < W ? n : W;
 }
+__device__ __forceinline__ int64_t chunk_start(int64_t c, int64_t W, int64_t n) { return n ? quot(W * c, n) : 0; }
+__device__ __forceinline__ int64_t chunk_of(int64_t u, int64_t W, int64_t n) { return quot((u + 1) * n - 1, W); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -111,7 +127,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // trit_attn_prefix.cu: whether the prefix runs there, its layout, its launch.
 bool prefix_on_tensor_cores(const trit_attn_job &J);
-void prefix_layout(Args &A, int spare);     // spare: SMs the own keys' grid leaves free
+// spare: SMs the own keys' grid leaves free; most: own steps if every length were the
+// table's.
+void prefix_layout(Args &A, int spare, int64_t most);
 int64_t prefix_part_bytes(const Args &A);
 cudaError_t launch_prefix(const Args &A, cudaStream_t s);
 

@@ -43,6 +43,7 @@ constexpr int kThreads = 384;      // 8 softmax warps and the four above
 // S, take 216 and the third keeps 72 (256 * 216 + 128 * 72 = 384 * 168).
 constexpr int kLaunchRegs = 168;
 constexpr int kTmemCols = 512;     // S of the two streams at 0 and 128, O at 256 and 384
+constexpr int kLeanCtas = 84;      // of a lean launch (80 of 20 items: 4 splits 150 us, 5 164, 3 191)
 constexpr float kGrow = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 template <int D>
@@ -221,7 +222,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = item % A.tc_groups, h = item / A.tc_groups;
     const int P = int(J.batch.prefix_len);
     const int nb = (P + kBlockKeys - 1) / kBlockKeys;
-    const int j0 = int(int64_t(nb) * split / A.tc_splits), j1 = int(int64_t(nb) * (split + 1) / A.tc_splits);
+    int splits = A.tc_splits;
+    if (A.tc_lean) {      // the own steps decide: each warp adds them up
+        pdl_wait();
+        const int cap = J.batch.table_pages * J.cache.page_size;
+        int64_t steps = 0;
+        for (int i = lane; i < J.batch.B; i += 32) {
+            int len = J.batch.lens[i];
+            len = len < 0 ? 0 : (len > cap ? cap : len);
+            steps += (len + A.own_step - 1) / A.own_step;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) steps += __shfl_xor_sync(~0u, steps, o);
+        splits = splits_of(A, steps * J.cache.heads * A.own_tiles);
+        if (split >= splits) return;
+    }
+    const int j0 = int(int64_t(nb) * split / splits), j1 = int(int64_t(nb) * (split + 1) / splits);
     const int n = j1 - j0;
     const bool pair = 2 * group + 1 < A.tc_tiles;     // two row tiles, or one over two streams
 
@@ -578,7 +594,7 @@ bool prefix_on_tensor_cores(const trit_attn_job &J) {
     return J.batch.prefix_len > 0 && rows > 32 && pow2 && C.page_size >= 16 && strides;
 }
 
-void prefix_layout(Args &A, int spare) {
+void prefix_layout(Args &A, int spare, int64_t most) {
     const trit_attn_job &J = A.J;
     const int64_t rows = int64_t(J.batch.B) * A.R;
     const int nb = int((J.batch.prefix_len + kBlockKeys - 1) / kBlockKeys);
@@ -608,6 +624,14 @@ void prefix_layout(Args &A, int spare) {
         }
     }
     A.tc_splits = splits;
+    // an own step is 32 KB, about 1/183 us at the rate these kernels reach
+    A.tc_lean = kLeanCtas / A.tc_items;
+    if (A.tc_lean < 1 || A.tc_lean >= splits) A.tc_lean = 0;
+    // -- and two chunks of 16 for every CTA, or the turns only cost (96 sequences of D = 64,
+    // 4300 steps: 53 us against 43)
+    A.tc_lean_from = int64_t(best * 183);
+    if (A.tc_lean_from < 32 * int64_t(A.grid)) A.tc_lean_from = 32 * int64_t(A.grid);
+    if (most < A.tc_lean_from) A.tc_lean = 0;      // cannot be reached: nothing to look up
 }
 
 cudaError_t launch_prefix(const Args &A, cudaStream_t s) {

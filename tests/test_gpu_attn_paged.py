@@ -167,6 +167,25 @@ def test_long_prefix_many_rows(t, case, sharp):
     assert err == 0
 
 
+@pytest.mark.parametrize("case", [
+    ([500 + i for i in range(34)], 4, [1 + i % 4 for i in range(34)], 20, 20, 64, 64, HF, 3969, False),
+    ([900 - 20 * i for i in range(40)], 1, None, 32, 16, 128, 32, BF, 2111, True),
+    ([0, 2500] * 20, 1, [0, 1] * 20, 24, 12, 128, 16, HF, 1500, False),
+    ([5] * 39 + [60000], 1, None, 8, 8, 64, 64, BF, 1000, False),      # a table far wider than most lengths
+])
+def test_much_own_work_beside_a_prefix(t, case):
+    """The prefix cut into fewer parts and the own keys' chunks taken in turn; twice, so that what a
+    call leaves for the next is seen."""
+    lens, T, new, hq, hkv, D, page, dt, prefix, nhd = case
+    c = build_case(lens, T, new, hq, hkv, D, page, dt, prefix, nhd, seed=prefix)
+    err, job = run(t, c, dt)
+    assert err == 0
+    first = job.out.clone()
+    t.trit_attn_paged(job, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(first, job.out)        # who takes a chunk changes no result
+
+
 def test_zero_scale(t):
     """Every visible key weighs the same."""
     for lens in ([5, 9], [3] * 40):
