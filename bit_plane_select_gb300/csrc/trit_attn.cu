@@ -3,12 +3,12 @@
 //
 // The keys of every item (trit_attn.cuh) are cut into steps of 64 (128 where D = 64), all steps of
 // the call are laid end to end and cut into equal chunks, whatever the lengths
-// (which only the device knows): one per CTA, or several taken in turn by the CTAs that
-// start while the prefix kernel of trit_attn_prefix.cu still runs.  A chunk
+// (which only the device knows), one per CTA; beside the prefix kernel of
+// trit_attn_prefix.cu, as many as its CTAs leave room for.  A chunk
 // may end one item, cover several and begin another.  Items that do not lie in one
 // chunk leave partial results, joined by the last of the item's CTAs where
 // there is no prefix and by a second launch where there is one (a prefix
-// part belongs to many sequences).  Which CTA takes a chunk changes no result.
+// part belongs to many sequences).
 //
 // Few rows share a key (R = T Hq/Hkv, 4 in a plain decode step), so the cost is
 // reading K and V: 4 D bytes a key against 4 D R flops.  A step's keys go 16
@@ -282,8 +282,7 @@ constexpr int kStages = 2;
 // CTAs per SM by the row tiles' registers (shared memory allows three).
 __host__ __device__ constexpr int ctas_of(int NB) { return NB <= 2 ? 3 : 2; }
 
-// TURNS: chunks may be taken in turn (the host knows whether they can be).
-template <typename T, int D, int NB, bool TURNS>
+template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int RT = 8 * NB;
@@ -298,9 +297,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     const uint32_t q_at = tc::smem_u32(smem + kWarps * kStages * kStageBytes), q_bytes = RT * D * 2;
     float *stats = reinterpret_cast<float *>(smem + kWarps * kStages * kStageBytes + kQueries * q_bytes);   // [kWarps][RT] (m, l)
     int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
-    volatile int32_t *taken = scratch + kWarps;      // [4]: chunk of this CTA's n-th turn at n % 4
     Batch S;
-    S.cum = scratch + kWarps + 4;
+    S.cum = scratch + kWarps;
     S.len = S.cum + A.J.batch.B + 1;
     S.fresh = S.len + A.J.batch.B;
     const int32_t *cum = S.cum;
@@ -317,16 +315,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
     const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
     const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
-    // this CTA's first chunk, and the end of the one at hand
+    // this CTA's chunk
     const int64_t count = chunk_count(A, W);
-    const bool turns = TURNS && lean(A, W);
     const int64_t lo = blockIdx.x < count ? chunk_start(blockIdx.x, W, count) : W;
-    int64_t hi = blockIdx.x < count ? chunk_start(blockIdx.x + 1, W, count) : W;
+    const int64_t hi = blockIdx.x < count ? chunk_start(blockIdx.x + 1, W, count) : W;
 
     // the ring runs ahead of the products, across items: keys and values by stage, and
     // an item's queries with its first stage (each warp a quarter of the rows)
-    int64_t lu = lo, lhi = hi;
-    int lord = 0;                 // the chunk's number in this CTA
+    int64_t lu = lo;
     Place lp = {};
     Keys lk = {};
     Pages lpages = {};
@@ -355,24 +351,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         lq = lq + 1 == kQueries ? 0 : lq + 1;
     };
     auto load_next = [&](int stage) {
-        if (lu < lhi) {
+        if (lu < hi) {
             if (lnew) {
                 load_queries();
                 lnew = false;
             }
             load_stage<D>(A, lk, lpages, lp.h, lp.step, warp, ring_at + stage * kStageBytes, lane);
-            if (++lu == lhi && turns) {
-                ++lord;
-                const int next = taken[lord & 3];
-                if (next < count) {
-                    lu = chunk_start(next, W, count);
-                    lhi = chunk_start(next + 1, W, count);
-                    lp = place_of(A, cum, lu);
-                    lk = keys_of(A, S, lp);
-                    lpages = pages_of<D>(A, lk, lp.step, warp, lane);
-                    lnew = true;
-                }
-            } else if (lu < lhi) {
+            if (++lu < hi) {
                 if (++lp.step == lp.steps) {
                     next_item(A, S, lp);
                     lk = keys_of(A, S, lp);
@@ -412,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         const int64_t s0 = int64_t(cum[q.b]) * Hkv * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
         const int64_t c0 = chunk_of(s0, W, count);
         const int parts = int(chunk_of(s0 + q.steps - 1, W, count) - c0) + 1;
-        uint32_t *arrived = A.count + 1 + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
+        uint32_t *arrived = A.count + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
         if (threadIdx.x == 0) {
             __threadfence();
             const bool last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
@@ -587,29 +572,13 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     };
 
     int64_t u = lo;
-    // chunks taken in turn: this CTA's second one, and its third on the way
-    int64_t chunk = blockIdx.x, chunk_lo = lo;
-    int ord = 0, ticket = 0;
-    if (turns && threadIdx.x == 0) {
-        taken[1] = int(gridDim.x + atomicAdd(A.count, 1u));
-        ticket = int(gridDim.x + atomicAdd(A.count, 1u));
-    }
     bool fresh = true;
     int stage = 0;
     while (u < hi) {
         tc::cp_async_wait<kStages - 1>();
         if (fresh) {
             fresh = false;
-            if (u == chunk_lo) {
-                // a chunk begins (its place is set): the turn after next is known to all
-                // from the barrier below on, a chunk's length before it is needed
-                if (turns && threadIdx.x == 0) {
-                    taken[(ord + 2) & 3] = ticket;
-                    ticket = int(gridDim.x + atomicAdd(A.count, 1u));
-                }
-            } else {
-                next_item(A, S, p);
-            }
+            if (u != lo) next_item(A, S, p);
             first_step = p.step;
             nkeys = keys_of(A, S, p).n;
             const int rows = p.b < 0 ? B * A.R : A.R;
@@ -661,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const bool whole = starts && ends;
             const bool direct = whole && p.b >= 0 && J.batch.prefix_len == 0;
             const int64_t slot = whole ? (p.b < 0 ? slot_prefix(A, p.h, p.tile) : slot_own(A, p.b, p.h, p.tile))
-                                       : 2 * chunk + (starts ? 1 : 0);
+                                       : 2 * int64_t(blockIdx.x) + (starts ? 1 : 0);
             float *part = A.parts + slot * part_floats(RT, D);
             const int rows = p.b < 0 ? B * A.R : A.R;
 #pragma unroll
@@ -728,16 +697,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         load_next(stage);
         if (++stage == kStages) stage = 0;
         ++p.step;
-        if (++u == hi && turns) {
-            ++ord;
-            const int next = taken[ord & 3];
-            if (next < count) {
-                chunk = next;
-                u = chunk_lo = chunk_start(next, W, count);
-                hi = chunk_start(next + 1, W, count);
-                p = place_of(A, cum, u);
-            }
-        }
+        ++u;
     }
     tc::cp_async_wait<0>();
     // the join waits for this grid alone and reads the prefix kernel's results too: one CTA
@@ -762,7 +722,6 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
     const int tid = threadIdx.x % D, part0 = threadIdx.x / D;            // the group's first part
     const int r4 = row4 * 4 + (tid & 3), c = tid >> 2;                    // columns 4c ..
     const int r = r4 < A.R ? r4 : A.R - 1;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *A.count = 0;      // the chunks taken, for the next call
     const int t = r / G, g = r - t * G;
 
     // the own item's parts
@@ -871,7 +830,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 size_t smem_of(const Args &A) {
     const int D = A.J.cache.head_dim;
     return size_t(kWarps) * kStages * (4 * keys_of_stage(D) * D) + size_t(kStages + 1) * A.RT * D * 2 +
-           kWarps * A.RT * 8 + (kWarps + 4) * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
+           kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
 }
 
 // The work's layout from the job's sizes; the grid that a call would use.
@@ -903,22 +862,16 @@ Args layout(const trit_attn_job &J) {
     const int resident = per_sm;
     const int64_t grid = int64_t(kSms) * per_sm;
     A.grid = int(most < grid ? most : grid);
-    // beside the prefix kernel two CTAs per SM share short work better than three where
-    // D = 128 (D = 64, which computes more per byte: 50.7 against 46.2 us for 96 sequences;
-    // without a prefix: two long sequences 106 against 102)
-    const int two = 2 * kSms;
-    A.spread = on_tc && J.cache.head_dim == 128 && A.grid > two ? two : A.grid;
-    A.chunks = on_tc ? 4 * A.grid : A.grid;
-    if (on_tc) prefix_layout(A, kSms - (A.spread + resident - 1) / resident, most);
-    if (!A.tc_lean) A.grid = A.chunks = A.spread;     // no chunks in turn
+    A.resident = resident;
+    if (on_tc) prefix_layout(A, most);     // and the grid, beside it
     return A;
 }
 
-// [B + 1] sums of steps, then the chunks taken and one counter per own item.
+// [B + 1] sums of steps, then one counter per own item.
 int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
 int64_t head_bytes(const Args &A) {
     const int64_t items = int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles;
-    return cum_bytes(A.J) + ((items + 1) * 4 + 255) / 256 * 256;
+    return cum_bytes(A.J) + (items * 4 + 255) / 256 * 256;
 }
 
 int64_t part_bytes(const Args &A) {
@@ -931,7 +884,7 @@ int64_t bytes_of(const Args &A) { return head_bytes(A) + part_bytes(A) + prefix_
 template <typename T, int D, int NB>
 cudaError_t launch(const Args &A, cudaStream_t s) {
     const size_t smem = smem_of(A);
-    const auto kernel = A.tc_lean ? attn_kernel<T, D, NB, true> : attn_kernel<T, D, NB, false>;
+    const auto kernel = attn_kernel<T, D, NB>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     // the prefix kernel first: the next one depends on nothing of it and may start beside it

@@ -14,6 +14,7 @@ namespace trit {
 namespace attn {
 
 constexpr int kSms = 152;           // the grids are cut for this many
+constexpr int kPlans = 8;
 constexpr int kTcRows = 128;       // rows of a tile of the tensor-core prefix kernel
 
 // Rows: row r = t*G + g of a (sequence, key head) pair is token t and query
@@ -31,17 +32,18 @@ struct Args {
     int32_t own_tiles;       // row tiles per (sequence, key head)
     int32_t pre_tiles;       // row tiles of the prefix, per key head (0: no prefix item)
     int32_t pre_steps;       // steps of the prefix
-    int32_t grid;            // CTAs of the own-keys kernel
-    int32_t spread, chunks;  // most chunks of one each per CTA, and of several
+    int32_t grid;            // CTAs of the own-keys kernel, a chunk of the work each at most
+    int32_t resident;        // of which so many fit an SM together
     int32_t page_shift;      // log2(page_size), or -1
     int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
-    uint32_t *count;         // workspace: chunks taken, then arrivals per own item; zero between calls
+    uint32_t *count;         // workspace: arrivals per own item, zero between calls
     float *parts;            // workspace: the partial results
     // the prefix on the tensor cores (tc_items = 0: its items are above, with the own ones)
     int32_t tc_tiles, tc_groups;   // 128-row tiles per key head, and pairs of them
-    int32_t tc_items, tc_splits;   // (head, pair) items, and parts of the keys each is cut into
-    int32_t tc_lean;         // the same beside much work of the sequences' own, or 0
-    int64_t tc_lean_from;    // steps from which that is so
+    int32_t tc_items, tc_splits;   // (head, pair) items, and the most parts each is cut into
+    int32_t tc_plans;              // parts by the own steps W: tc_parts_for[i] from tc_from[i] on
+    int32_t tc_parts_for[kPlans];
+    int64_t tc_from[kPlans];
     int32_t own_step;        // keys of an own step
     float *tc_parts;         // workspace: their partial results, [item][tc_splits][stream]
 };
@@ -57,10 +59,10 @@ __host__ __device__ inline int64_t part_floats(int RT, int D) { return int64_t(R
 // Slots of partial results: chunk c's first and last unfinished items at 2c and
 // 2c + 1, then one per own item and per prefix item that lies in a single chunk.
 __host__ __device__ inline int64_t slot_own(const Args &A, int b, int h, int tile) {
-    return 2 * int64_t(A.chunks) + (int64_t(b) * A.J.cache.heads + h) * A.own_tiles + tile;
+    return 2 * int64_t(A.grid) + (int64_t(b) * A.J.cache.heads + h) * A.own_tiles + tile;
 }
 __host__ __device__ inline int64_t slot_prefix(const Args &A, int h, int tile) {
-    return 2 * int64_t(A.chunks) + int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles +
+    return 2 * int64_t(A.grid) + int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles +
            int64_t(h) * A.pre_tiles + tile;
 }
 
@@ -71,26 +73,30 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
     return a / b;
 }
 
-// Where the sequences' own keys take at least as long as the prefix, the prefix kernel
-// runs on about half of the SMs (tc_lean parts per item instead of tc_splits) and the
-// own keys' chunks are taken in turn, by the CTAs beside it first and by those that
-// start as it ends: its tensor work then runs under their memory traffic (256 sequences of
-// about 850 keys behind 32768: 150 us against 174).  W is known on the device
-// only; every kernel decides alike.
-__device__ __forceinline__ bool lean(const Args &A, int64_t W) { return A.tc_lean > 0 && W >= A.tc_lean_from; }
-__device__ __forceinline__ int splits_of(const Args &A, int64_t W) { return lean(A, W) ? A.tc_lean : A.tc_splits; }
+// Parts of a prefix item beside W own steps.  The prefix kernel takes whole SMs and the
+// own-keys kernel the others, so that tensor work and memory traffic overlap; the
+// more own steps, the fewer SMs (prefix_layout).  W is known on the device only, and every
+// kernel decides alike.
+__device__ __forceinline__ int splits_of(const Args &A, int64_t W) {
+    int s = A.tc_parts_for[0];
+#pragma unroll
+    for (int i = 1; i < kPlans; ++i)
+        if (i < A.tc_plans && W >= A.tc_from[i]) s = A.tc_parts_for[i];
+    return s;
+}
 
 // How many chunks W steps are cut into: chunk c of n is [W c / n, W (c + 1) / n), n <= W, so
-// that none is empty and an item's chunks are consecutive.
-//  - One chunk per CTA: one CTA per SM while there is a step for each, more of them
-//    from four steps each on (32 sequences of about 500 keys behind a prefix, 1250
-//    steps: 21.9 us with 304 CTAs, 27.5 with 456, 26.5 with 152; four steps a chunk,
-//    taken in turn: 37).
-//  - Beside a lean prefix kernel (below): chunks of 16 steps, taken in turn.
+// that none is empty and an item's chunks are consecutive.  One per SM while there is a
+// step for each, more of them from four steps each on (32 sequences of about 500 keys
+// behind a prefix, 1250 steps: 21.9 us with 304, 27.5 with 456, 26.5 with 152), and
+// no more than fit beside the prefix kernel.
 __device__ __forceinline__ int64_t chunk_count(const Args &A, int64_t W) {
     int64_t n = W / 4 > kSms ? W / 4 : kSms;
-    if (n > A.spread) n = A.spread;
-    if (lean(A, W)) n = W / 16 < A.chunks ? W / 16 : A.chunks;
+    if (n > A.grid) n = A.grid;
+    if (A.tc_items) {
+        const int64_t free = int64_t(kSms - A.tc_items * splits_of(A, W)) * A.resident;
+        if (free > 0 && n > free) n = free;
+    }
     return n < W ? n : W;
 }
 __device__ __forceinline__ int64_t chunk_start(int64_t c, int64_t W, int64_t n) { return n ? quot(W * c, n) : 0; }
@@ -127,9 +133,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // trit_attn_prefix.cu: whether the prefix runs there, its layout, its launch.
 bool prefix_on_tensor_cores(const trit_attn_job &J);
-// spare: SMs the own keys' grid leaves free; most: own steps if every length were the
-// table's.
-void prefix_layout(Args &A, int spare, int64_t most);
+// most: the own steps if every length were the table's.  Sets the grid of the own-keys
+// kernel too.
+void prefix_layout(Args &A, int64_t most);
 int64_t prefix_part_bytes(const Args &A);
 cudaError_t launch_prefix(const Args &A, cudaStream_t s);
 

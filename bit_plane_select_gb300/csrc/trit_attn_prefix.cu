@@ -43,7 +43,6 @@ constexpr int kThreads = 384;      // 8 softmax warps and the four above
 // S, take 216 and the third keeps 72 (256 * 216 + 128 * 72 = 384 * 168).
 constexpr int kLaunchRegs = 168;
 constexpr int kTmemCols = 512;     // S of the two streams at 0 and 128, O at 256 and 384
-constexpr int kLeanCtas = 84;      // of a lean launch (80 of 20 items: 4 splits 150 us, 5 164, 3 191)
 constexpr float kGrow = 8.0f;      // log2 of the growth of a maximum that O tolerates
 
 template <int D>
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int P = int(J.batch.prefix_len);
     const int nb = (P + kBlockKeys - 1) / kBlockKeys;
     int splits = A.tc_splits;
-    if (A.tc_lean) {      // the own steps decide: each warp adds them up
+    if (A.tc_plans > 1) {      // the own steps decide: each warp adds them up
         pdl_wait();
         const int cap = J.batch.table_pages * J.cache.page_size;
         int64_t steps = 0;
@@ -258,10 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch();
 
-    // a block's place in the ring's order of use: K0 V0 K1 V1 ... for a pair,
-    // K0 K1 V0 K2 V1 ... for one tile on two streams
+    // A block's place in the ring's order of use: K0 V0 K1 V1 ... for a pair, K0 K1 V0 K2 V1 ...
+    // for one tile on two streams.  A wait by parity is sound only if the use before it on
+    // the same stage has completed for the waiter: for a pair both streams consume every
+    // tile; for one tile every stage serves one stream (K of odd blocks 1, of even ones 3, V
+    // of odd blocks 0, of even ones 2) but for K0, which the second stream waits for before it
+    // starts.  (The last V keeps its place behind a K that is not there.)
     auto k_at = [&](int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
-    auto v_at = [&](int j) { return pair ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2); };
+    auto v_at = [&](int j) { return pair ? 2 * j + 1 : 2 * j + 2; };
 
     // every warp of a warpgroup gives up or takes the same number of registers
     if (warp >= kLoadWarp) {
@@ -594,44 +597,67 @@ bool prefix_on_tensor_cores(const trit_attn_job &J) {
     return J.batch.prefix_len > 0 && rows > 32 && pow2 && C.page_size >= 16 && strides;
 }
 
-void prefix_layout(Args &A, int spare, int64_t most) {
+void prefix_layout(Args &A, int64_t most) {
     const trit_attn_job &J = A.J;
     const int64_t rows = int64_t(J.batch.B) * A.R;
     const int nb = int((J.batch.prefix_len + kBlockKeys - 1) / kBlockKeys);
     A.tc_tiles = int((rows + kRows - 1) / kRows);
     A.tc_groups = (A.tc_tiles + 1) / 2;
     A.tc_items = A.tc_groups * J.cache.heads;
-    // Splits by a cost model in us, fitted to sweeps: a CTA costs about 4, and per block
-    // 1.6 for a pair of tiles, 1.2 for one (1.0 and 0.8 where D = 64); every part is
-    // written here and read by the join; and half the CTAs' fixed time is taken
-    // from the sequences' own keys, as is 4 more where their grid cannot start
-    // beside this one (32 sequences of 5 key heads: 10 splits, 50 CTAs, 23.1 us, 11 splits
-    // 27.1).  (480 rows, 63 blocks: 11, 13, 15 splits 44.5, 43.9, 45.7
-    // us in all; 192 rows of D = 64, 47 blocks: 9, 12, 16 splits 44.6, 43.6, 45.6.)
+    // The parts s each item is cut into, by a model in us fitted to sweeps.  The prefix
+    // kernel's items * s CTAs take an SM each: 4 us and, per block of 128 keys, 2.0 for a
+    // pair of tiles (1.6 where D = 64) or 1.2 for one (0.9).  The own-keys kernel's CTAs
+    // beside it: 8 us and 1.25 per step (1.43 where D = 64, 2.2 for more than 16 rows).
+    // Every part is written and read once more.  Measured in all, s by its neighbours: 24 x 5
+    // drafts 5, 6, 7: 44.0, 41.0, 43.0 us; 96 sequences of D = 64 3, 4, 5: 42.2, 38.3,
+    // 40.4; 256 sequences behind 32768 keys 3, 4, 5: 196, 151, 165.
     const bool single = A.tc_tiles == 1, wide = J.cache.head_dim == 128;
-    const double per_block = wide ? (single ? 1.2 : 1.6) : (single ? 0.8 : 1.0);
-    const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 8 / 5e6 * (single ? 2 : 1) +
-                             0.5 * 4 * A.tc_items / kSms;
-    double best = 0;
-    int splits = 0;
-    for (int s = 1; s <= nb && s * A.tc_items <= (A.tc_items > kSms ? 4 * A.tc_items : 2 * kSms); ++s) {
-        const int waves = (s * A.tc_items + kSms - 1) / kSms;
-        const double cost = waves * (4 + (nb + s - 1) / s * per_block) + s * per_split +
-                            (s * A.tc_items > spare ? 4 : 0);
-        if (splits == 0 || cost < best) {
-            best = cost;
-            splits = s;
-        }
+    const double per_block = wide ? (single ? 1.2 : 2.0) : (single ? 0.9 : 1.6);
+    const double per_step = A.RT > 16 ? 2.2 : wide ? 1.25 : 1.43;
+    const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 4 / 5e6 * (single ? 2 : 1);
+    // (this runs in every call: the terms without W once, then a few operations each)
+    constexpr int kMost = 64;
+    double prefix[kMost + 1], per_own[kMost + 1];
+    int top = 0;
+    for (int s = 1; s <= nb && s <= kMost && (s == 1 || s * A.tc_items <= kSms - 8); ++s) {
+        const int ctas = s * A.tc_items, waves = (ctas + kSms - 1) / kSms;
+        const int beside = kSms - ctas > 8 ? kSms - ctas : 8;
+        prefix[s] = waves * (4 + (nb + s - 1) / s * per_block);
+        per_own[s] = per_step / (double(beside) * A.resident);
+        top = s;
     }
-    A.tc_splits = splits;
-    // an own step is 32 KB, about 1/183 us at the rate these kernels reach
-    A.tc_lean = kLeanCtas / A.tc_items;
-    if (A.tc_lean < 1 || A.tc_lean >= splits) A.tc_lean = 0;
-    // -- and two chunks of 16 for every CTA, or the turns only cost (96 sequences of D = 64,
-    // 4300 steps: 53 us against 43)
-    A.tc_lean_from = int64_t(best * 183);
-    if (A.tc_lean_from < 32 * int64_t(A.grid)) A.tc_lean_from = 32 * int64_t(A.grid);
-    if (most < A.tc_lean_from) A.tc_lean = 0;      // cannot be reached: nothing to look up
+    auto cost = [&](int s, double W) {
+        const double floor = per_step * (W < 4 * kSms ? W / kSms : 4);    // chunks are not cut shorter
+        double own = W * per_own[s];
+        own = 8 + (own > floor ? own : floor);
+        return (prefix[s] > own ? prefix[s] : own) + s * per_split;
+    };
+    auto best = [&](double W) {
+        int parts = 1;
+        for (int s = 2; s <= top; ++s)
+            if (cost(s, W) < cost(parts, W)) parts = s;
+        return parts;
+    };
+    const double widest = 1.25 * double(most);
+    const int half = best(double(most) / 2);      // for half of the tables' room
+    // fewer parts as the own steps grow: the steps from which each number is best, or one
+    // number where that costs no more than 4 us at either end (adding the steps up, and CTAs
+    // that then have no part, cost 1.5)
+    const bool one = cost(half, 0) < cost(best(0), 0) + 4 && cost(half, widest) < cost(best(widest), widest) + 4;
+    A.tc_plans = 1;
+    A.tc_parts_for[0] = A.tc_splits = one ? half : best(0);
+    A.tc_from[0] = 0;
+    for (double W = 256; !one && W < widest && A.tc_plans < kPlans; W *= 1.3) {
+        const int s = best(W);
+        if (s == A.tc_parts_for[A.tc_plans - 1]) continue;
+        A.tc_parts_for[A.tc_plans] = s;
+        A.tc_from[A.tc_plans++] = int64_t(W);
+        if (s > A.tc_splits) A.tc_splits = s;
+    }
+    // the own-keys kernel's grid: what fits beside those parts (a CTA without a chunk would
+    // run last, on an SM it has to wait for)
+    const int64_t fit = int64_t(kSms - A.tc_items * half) * A.resident;
+    if (fit >= kSms && fit < A.grid) A.grid = int(fit);
 }
 
 cudaError_t launch_prefix(const Args &A, cudaStream_t s) {

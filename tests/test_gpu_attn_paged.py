@@ -276,3 +276,21 @@ def test_offsets_past_32_bits(t):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     check(c, out, None)
+
+
+@pytest.mark.parametrize("B,page,D,prefix,own", [(40, 16, 128, 1500, 2500), (40, 64, 64, 1537, 2500),
+                                                 (70, 32, 128, 2300, 900), (33, 128, 64, 9000, 40)])
+def test_calls_repeat_bit_for_bit(t, B, page, D, prefix, own):
+    """No result depends on when a copy lands or which CTA is first: the prefix kernel beside
+    much and little memory traffic, one and two row tiles."""
+    c = build_case([own - 7 * (i % 5) for i in range(B)], 1, None, 24, 12, D, page, HF, prefix)
+    c["out_dt"] = HF
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    job = make_job(t, c, HF)
+    first = None
+    for _ in range(40):
+        t.trit_attn_paged(job, err)
+        torch.cuda.synchronize()
+        first = (job.out.clone(), job.lse.clone()) if first is None else first
+        assert torch.equal(first[0], job.out) and torch.equal(first[1], job.lse)
+    assert int(err.item()) == 0 and bool(first[0].isfinite().all())
