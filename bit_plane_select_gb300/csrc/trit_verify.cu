@@ -16,12 +16,14 @@
 namespace trit {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kCluster = 8;
-// Vectors of four of each row in flight per thread; 256 threads, six CTAs per SM
-// (192 sequences of 131072: 48.7 us; 512 threads, four vectors, two CTAs: 58.5 -- a
-// CTA reads nothing but race numbers until it knows its rows, so others have to)
-constexpr int kPer = 2;
+constexpr int kPer = 2;       // vectors of four of each row in flight per thread
+
+// Threads of a CTA (NT): 256, six CTAs per SM, where there are sequences enough (192 of
+// 131072 tokens: 48.7 us; 512 threads, four vectors, two CTAs: 58.5 -- a CTA reads
+// nothing but race numbers until it knows its rows, so others have to); 512 and 1024
+// where few CTAs have long rows (eight sequences of 131072: 7.9 us against 14.2; one of
+// 32000, four vectors a thread already with 256: 4.9 against 4.1, so not there).
 
 template <typename S>
 __device__ __forceinline__ float as_f32(S v);
@@ -69,7 +71,7 @@ struct Best {
 
 // Candidates 4 i .. 4 i + 3 for i in [from, to), i = from + tid first; e0 holds the
 // first kPer vectors of e.
-template <typename S, bool VEC>
+template <typename S, bool VEC, int kThreads>
 __device__ __forceinline__ void scan(Best &best, const S *p, const S *q, const float *e, int64_t from, int64_t to,
                                      int tid, float4 (&w)[kPer]) {
     for (int64_t i0 = from + tid; i0 < to; i0 += kThreads * kPer) {
@@ -100,6 +102,7 @@ __device__ __forceinline__ unsigned long long key_of(const Best &b) {
                       : (static_cast<unsigned long long>(__float_as_uint(b.s)) << 32) | (0xffffffffu - b.i);
 }
 
+template <int kThreads>
 __device__ unsigned long long block_max(unsigned long long k, unsigned long long *sh) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -118,8 +121,8 @@ __device__ unsigned long long block_max(unsigned long long k, unsigned long long
     return k;
 }
 
-template <typename S, bool VEC>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6)
+template <typename S, bool VEC, int kThreads>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kThreads == 256 ? 6 : 1536 / kThreads)
     verify_kernel(const __grid_constant__ trit_verify_job J, uint32_t *err) {
     __shared__ unsigned long long sh[kThreads / 32];
     __shared__ unsigned long long keys[kCluster];     // in the first CTA: one per CTA
@@ -169,12 +172,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6)
     const S *p = P + kept * J.p_tok_stride;
     const S *q = kept < n ? Q + kept * J.q_tok_stride : nullptr;
     Best best{-1.0f, 0u};
-    scan<S, VEC>(best, p, q, e, from, to, tid, w);
+    scan<S, VEC, kThreads>(best, p, q, e, from, to, tid, w);
     if (rank == kCluster - 1 && tid < J.V - 4 * quads) {      // the last V % 4
         const int64_t i = 4 * quads + tid;
         best.see(as_f32<S>(p[i]) - (q ? as_f32<S>(q[i]) : 0.0f), e[i], uint32_t(i));
     }
-    unsigned long long key = block_max(key_of(best), sh);
+    unsigned long long key = block_max<kThreads>(key_of(best), sh);
     if (tid == 0) {
         uint32_t to_first;
         asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_first) : "r"(uint32_t(__cvta_generic_to_shared(&keys[rank]))));
@@ -188,7 +191,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6)
     if (key == 0 && q) {      // the residual is empty: p decides
         best = Best{-1.0f, 0u};
         for (int64_t i = tid; i < J.V; i += kThreads) best.see(as_f32<S>(p[i]), e[i], uint32_t(i));
-        key = block_max(key_of(best), sh);
+        key = block_max<kThreads>(key_of(best), sh);
     }
     for (int t = tid; t <= J.T; t += kThreads) {
         int v = -1;
@@ -202,15 +205,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 6)
     }
 }
 
-template <typename S>
-cudaError_t launch(const trit_verify_job &J, uint32_t *err, cudaStream_t s) {
+template <typename S, int NT>
+cudaError_t launch_nt(const trit_verify_job &J, uint32_t *err, cudaStream_t s) {
     // vectors of four where every row starts on one
     auto on = [](const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
     const bool vec = on(J.p, 4 * sizeof(S)) && on(J.q, 4 * sizeof(S)) && on(J.race, 16) &&
                      ((J.p_seq_stride | J.p_tok_stride | J.q_seq_stride | J.q_tok_stride | J.race_stride) & 3) == 0;
-    const dim3 grid(unsigned(J.B) * kCluster), block(kThreads);
-    return vec ? launch_pdl(verify_kernel<S, true>, grid, block, 0, s, J, err)
-               : launch_pdl(verify_kernel<S, false>, grid, block, 0, s, J, err);
+    const dim3 grid(unsigned(J.B) * kCluster), block(NT);
+    return vec ? launch_pdl(verify_kernel<S, true, NT>, grid, block, 0, s, J, err)
+               : launch_pdl(verify_kernel<S, false, NT>, grid, block, 0, s, J, err);
+}
+template <typename S>
+cudaError_t launch(const trit_verify_job &J, uint32_t *err, cudaStream_t s) {
+    const int64_t sms = device_sm_count(), ctas = int64_t(J.B) * kCluster;
+    if (J.V <= 65536 || ctas > 2 * sms) return launch_nt<S, 256>(J, err, s);
+    return ctas <= sms ? launch_nt<S, 1024>(J, err, s) : launch_nt<S, 512>(J, err, s);
 }
 
 }  // namespace

@@ -60,7 +60,8 @@ def check(t, p, q, draft, u, race, n=None, pad=0, twice=True):
 @pytest.mark.parametrize("B,T,V,dtype,pad", [
     (1, 1, 1, torch.float32, 0), (3, 2, 2, torch.float32, 1), (5, 4, 37, torch.float32, 0),
     (1, 4, 32000, torch.float32, 0), (7, 3, 50257, torch.float32, 0), (4, 8, 4096, torch.bfloat16, 8),
-    (9, 33, 130, torch.float16, 0), (2, 70, 999, torch.float32, 3), (300, 1, 65, torch.bfloat16, 0)])
+    (9, 33, 130, torch.float16, 0), (2, 70, 999, torch.float32, 3), (300, 1, 65, torch.bfloat16, 0),
+    (2, 3, 70000, torch.float32, 0), (25, 2, 65541, torch.float16, 3), (30, 1, 66000, torch.bfloat16, 0)])
 def test_matches_the_plain_form(t, B, T, V, dtype, pad):
     for seed, alpha in ((1, 0.5), (2, 0.97)):
         x = inputs(B, T, V, dtype, seed, alpha)
