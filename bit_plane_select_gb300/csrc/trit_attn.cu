@@ -134,7 +134,8 @@ __device__ __forceinline__ void next_item(const Args &A, const Batch &S, Place &
     p.steps = S.cum[p.b + 1] - S.cum[p.b];
 }
 
-// The keys of a place: their page table and how many there are.
+// The keys of a place: their page table, and how many its row tile sees: the tiles of a
+// long chunk of new tokens read no further than their last token.
 struct Keys {
     const int32_t *table;
     int n;
@@ -146,7 +147,8 @@ __device__ __forceinline__ Keys keys_of(const Args &A, const Batch &S, const Pla
         k.n = int(A.J.batch.prefix_len);
     } else {
         k.table = A.J.batch.table + p.b * A.J.batch.table_stride;
-        k.n = S.len[p.b];
+        const int last = token_of(A, min((p.tile + 1) * A.RT, A.R) - 1);
+        k.n = max(0, min(S.len[p.b], S.len[p.b] - S.fresh[p.b] + last + 1));
     }
     return k;
 }
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const int rows = p.b < 0 ? B * A.R : A.R;
             tiles = NB == 1 ? 1 : min(NB, (rows - p.tile * RT + 7) >> 3);
             clear = nkeys;
-            const int fresh_own = p.b < 0 ? 0 : S.fresh[p.b];
+            const int fresh_own = p.b < 0 ? 0 : S.fresh[p.b], len_own = p.b < 0 ? 0 : S.len[p.b];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     int see = nkeys;
                     if (p.b >= 0) {
                         const int t = token_of(A, row);
-                        see = t < fresh_own ? max(nkeys - fresh_own + t + 1, 0) : 0;
+                        see = t < fresh_own ? max(len_own - fresh_own + t + 1, 0) : 0;
                     } else if (row < rows) {
                         const int b = row / A.R;
                         if (token_of(A, row - b * A.R) >= S.fresh[b]) see = 0;

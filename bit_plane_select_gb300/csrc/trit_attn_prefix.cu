@@ -18,10 +18,14 @@
 // only when a row's maximum grew by more than 2^8 since its base was fixed; until
 // then P may exceed 1 (at most 2^8) and both l and O carry the same base.
 //
-// Each item (256 or 128 rows of a head) is cut along the keys into `splits`
-// parts, one CTA each; the partial results (unnormalised O, base, l) are joined with the
+// Each item (256 or 128 rows of a head) is cut along the keys into parts, one CTA
+// each, as many as prefix_layout finds best beside the sequences' own keys; the partial results (unnormalised O, base, l) are joined with the
 // sequences' own by the join kernel.  They are stored four columns by row,
 // [D/4][128] float4, so that a warp's 32 rows store 512 contiguous bytes.
+//
+// Measured: 1024 rows of D = 128 on each of 5 heads against 32768 keys, 80 CTAs: 142 us
+// alone, 605 TFLOP/s on 80 of 152 SMs, the tensor pipe busy 54% of the time; what bounds it
+// is the chain of a stream's block (S, softmax, P V, S), about 3500 SM-clocks.
 #include <cuda.h>
 
 #include "trit_attn.cuh"

@@ -120,6 +120,8 @@ CASES = [
     ([9, 40, 8], 8, [8, 3, 0], 20, 5, 128, 16, BF, 0, False),   # 32 rows
     ([40, 9], 9, None, 5, 1, 64, 24, HF, 0, False),             # 45 rows: two row tiles
     ([3000], 1, None, 8, 2, 128, 64, HF, 0, False),             # one item over many CTAs
+    ([150, 131], 130, [130, 77], 8, 2, 64, 16, BF, 0, False),   # a chunk of prompt: many row tiles
+    ([40, 33], 33, [33, 20], 4, 4, 128, 8, HF, 5, True),
     ([5, 3], 1, None, 20, 5, 128, 64, BF, 130, False),          # with a prefix
     ([5, 0, 77], 1, [1, 0, 1], 20, 5, 128, 64, BF, 1, False),
     ([0, 0], 1, [1, 1], 8, 2, 64, 16, HF, 500, False),          # nothing of their own
