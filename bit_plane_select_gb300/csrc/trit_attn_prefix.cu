@@ -210,12 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kTile);
     uint64_t *empty = full + kRing;
     uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
-    uint64_t *p_full = s_full + 2;       // [stream][half]: P of the first, second 64 keys is
-    uint64_t *o_full = p_full + 4;       // stream's O is finished
+    uint64_t *p_full = s_full + 2;       // [stream][quarter]: P of 32 keys each is
+    uint64_t *o_full = p_full + 8;       // stream's O is finished
     uint64_t *pv_done = o_full + 2;      // stream's product into O has completed
     uint64_t *q_full = pv_done + 2;
     uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
-    constexpr int kBars = 2 * kRing + 12;
+    constexpr int kBars = 2 * kRing + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
     uint32_t *timed_out = tmem_slot + 1;
 
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp && lane < kBars) {       // a barrier per lane, in the order above
         const int i = lane;
         const int count = i < kRing ? 1 : i < 2 * kRing ? (pair ? 2 : 1)     // empty: streams that read the tile
-                        : i < 2 * kRing + 2 ? 1 : i < 2 * kRing + 6 ? 4      // s_full, p_full (warps)
-                        : i < 2 * kRing + 10 ? 1 : i == 2 * kRing + 10 ? 8 : 1;   // o_full and pv_done, q_full (warps), tail
+                        : i < 2 * kRing + 2 ? 1 : i < 2 * kRing + 10 ? 4      // s_full, p_full (warps)
+                        : i < 2 * kRing + 14 ? 1 : i == 2 * kRing + 14 ? 8 : 1;   // o_full and pv_done, q_full (warps), tail
         mbar_init(full + i, uint32_t(count));
         if (i == 0) *timed_out = 0;
         fence_barrier_init();
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pipe together and then the exponentials together (measured: 4100 SM-clocks a
         // block pair in step)
         if (s == 1) {
-            ok = ok && warp_wait(&p_full[1], 0, timed_out);
+            ok = ok && warp_wait(&p_full[3], 0, timed_out);
             if (n >= 8) ok = ok && warp_wait(&p_full[0], 1, timed_out);
         }
         if (ok && mine > 0) {
@@ -377,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(&full[st], (at / kRing) & 1, timed_out);
             const uint32_t b = rv + st * (kTile >> 4);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                ok = ok && warp_wait(&p_full[2 * s + half], i & 1, timed_out);
+            for (int part = 0; part < 4; ++part) {
+                ok = ok && warp_wait(&p_full[4 * s + part], i & 1, timed_out);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
-                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                    for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
                         mma_ts(o, sp + kk * 8, b + kk * (2048 >> 4), idesc_o<T, D>(), i > 0 || kk > 0);
                 }
                 __syncwarp();
@@ -498,12 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w[c] = pack16<T>(e0, e1);
                 }
                 tmem_st16(sa + q * 16, w);
-                if (q & 1) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * s + (q >> 1)]);
-                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[4 * s + q]);
             }
             const float2 t = unpack2(add2(sum[0], sum[1]));
             l += t.x + t.y;
