@@ -23,9 +23,10 @@
 // sequences' own by the join kernel.  They are stored four columns by row,
 // [D/4][128] float4, so that a warp's 32 rows store 512 contiguous bytes.
 //
-// Measured: 1024 rows of D = 128 on each of 5 heads against 32768 keys, 80 CTAs: 142 us
-// alone, 605 TFLOP/s on 80 of 152 SMs, the tensor pipe busy 54% of the time; what bounds it
-// is the chain of a stream's block (S, softmax, P V, S), about 3500 SM-clocks.
+// Measured: 1024 rows of D = 128 on each of 5 heads against 32768 keys, on 80 of 152 SMs,
+// beside the sequences' own keys: 138 us in all, 640 TFLOP/s, most of it here; what bounds
+// it is the chain of a stream's block (S, softmax, P V, S).  P goes to the products in
+// quarters of 32 keys (in halves: 151 us).
 #include <cuda.h>
 
 #include "trit_attn.cuh"
@@ -607,14 +608,15 @@ void prefix_layout(Args &A, int64_t most) {
     A.tc_groups = (A.tc_tiles + 1) / 2;
     A.tc_items = A.tc_groups * J.cache.heads;
     // The parts s each item is cut into, by a model in us fitted to sweeps.  The prefix
-    // kernel's items * s CTAs take an SM each: 4 us and, per block of 128 keys, 2.0 for a
-    // pair of tiles (1.6 where D = 64) or 1.2 for one (0.9).  The own-keys kernel's CTAs
+    // kernel's items * s CTAs take an SM each: 4 us and, per block of 128 keys, 1.6 for a
+    // pair of tiles (1.3 where D = 64) or 1.2 for one (0.9).  The own-keys kernel's CTAs
     // beside it: 8 us and 1.25 per step (1.43 where D = 64, 2.2 for more than 16 rows).
-    // Every part is written and read once more.  Measured in all, s by its neighbours: 24 x 5
-    // drafts 5, 6, 7: 44.0, 41.0, 43.0 us; 96 sequences of D = 64 3, 4, 5: 42.2, 38.3,
-    // 40.4; 256 sequences behind 32768 keys 3, 4, 5: 196, 151, 165.
+    // Every part is written and read once more.  (2.0 and 1.6, or 1.4 and 1.1, per block
+    // choose parts that take 41.4 instead of 39.8 us for 24 x 5 drafts and 41.7 or 44.4 instead of
+    // 39.6 for 96 sequences of D = 64.  256 sequences behind 32768 keys, before P went in
+    // quarters, 3, 4, 5 parts: 196, 151, 165.)
     const bool single = A.tc_tiles == 1, wide = J.cache.head_dim == 128;
-    const double per_block = wide ? (single ? 1.2 : 2.0) : (single ? 0.9 : 1.6);
+    const double per_block = wide ? (single ? 1.2 : 1.6) : (single ? 0.9 : 1.3);
     const double per_step = A.RT > 16 ? 2.2 : wide ? 1.25 : 1.43;
     const double per_split = double(rows) * J.cache.heads * J.cache.head_dim * 4 / 5e6 * (single ? 2 : 1);
     // (this runs in every call: the terms without W once, then a few operations each)
