@@ -526,6 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         *reinterpret_cast<float2 *>(part + kRows * D + 2 * r) = make_float2(m, l);
     }
+    if (*reinterpret_cast<volatile uint32_t *>(timed_out)) {
+        // a wait gave up: copies and products still in flight land in microseconds; give
+        // them 2 ms before this CTA's memory is anyone else's
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 2000000ull) __nanosleep(1000);
+    }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *timed_out) raise_flag(A.err, TRIT_ERR_TIMEOUT);
