@@ -603,7 +603,10 @@ bool prefix_on_tensor_cores(const trit_attn_job &J) {
     const bool strides = C.slot_stride >= C.head_dim && (C.heads == 1 || C.head_stride >= C.head_dim) &&
                          (C.pages == 1 || C.page_stride >= C.head_dim) && C.slot_stride < most &&
                          C.head_stride < most && C.page_stride < most;
-    return J.batch.prefix_len > 0 && rows > 32 && pow2 && C.page_size >= 16 && strides;
+    // From 17 rows: 20 rows behind 4096 and 32768 keys 16.3 and 32.4 us here, 21.0 and 34.6 on the
+    // other path; 32 rows 17.5 and 33.5 against 18.4 and 41.6; 64 rows 19.8 and 36.2 against
+    // 26.5 and 54.7 (in all, 33 to 900 own keys).  Fewer leave most of 128 lanes empty.
+    return J.batch.prefix_len > 0 && rows > 16 && pow2 && C.page_size >= 16 && strides;
 }
 
 void prefix_layout(Args &A, int64_t most) {
