@@ -282,7 +282,7 @@ __device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float 
 
 constexpr int kStages = 2;
 // CTAs per SM by the row tiles' registers (shared memory allows three).
-__host__ __device__ constexpr int ctas_of(int NB) { return NB <= 2 ? 3 : 2; }
+__host__ __device__ constexpr int ctas_of(int NB) { return NB <= 2 ? kMostCtas : 2; }
 
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __grid_constant__ Args A) {
@@ -393,13 +393,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         return;
     }
 
-    // Without a prefix, the last of an item's CTAs to get here joins its parts: one
-    // counter per item, left at zero.
+    // Without a prefix, the last of an item's CTAs to get here joins its parts and leaves
+    // the item's counter at zero.  The counter is that of the item's first chunk: no other
+    // item begins there and ends elsewhere.
     auto join_last = [&](const Place &q, int rows) {
         const int64_t s0 = int64_t(cum[q.b]) * Hkv * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
         const int64_t c0 = chunk_of(s0, W, count);
         const int parts = int(chunk_of(s0 + q.steps - 1, W, count) - c0) + 1;
-        uint32_t *arrived = A.count + (int64_t(q.b) * Hkv + q.h) * A.own_tiles + q.tile;
+        uint32_t *arrived = A.count + c0;
         if (threadIdx.x == 0) {
             __threadfence();
             const bool last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
@@ -869,12 +870,11 @@ Args layout(const trit_attn_job &J) {
     return A;
 }
 
-// [B + 1] sums of steps, then one counter per own item.
-int64_t cum_bytes(const trit_attn_job &J) { return ((int64_t(J.batch.B) + 1) * 4 + 255) / 256 * 256; }
-int64_t head_bytes(const Args &A) {
-    const int64_t items = int64_t(A.J.batch.B) * A.J.cache.heads * A.own_tiles;
-    return cum_bytes(A.J) + (items * 4 + 255) / 256 * 256;
-}
+// The workspace: a counter per chunk, [B + 1] sums of steps, partial results.  The counters
+// alone carry over from call to call, so they have the same place and room in every
+// layout and nothing else is written there: jobs of any sizes may use one workspace in turn.
+constexpr int64_t kCountBytes = (kSms * kMostCtas * 4 + 255) / 256 * 256;
+int64_t head_bytes(const Args &A) { return kCountBytes + ((int64_t(A.J.batch.B) + 1) * 4 + 255) / 256 * 256; }
 
 int64_t part_bytes(const Args &A) {
     const int64_t slots = slot_prefix(A, 0, 0) + int64_t(A.J.cache.heads) * A.pre_tiles;
@@ -919,9 +919,9 @@ cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_
     A.scale2 = J.scale == 0.0f ? 1.0f : fabsf(J.scale) * 1.4426950408889634f;
     A.flip = J.scale < 0.0f ? 0x80008000u : 0u;
     A.keep = J.scale == 0.0f ? 0u : 0xffffffffu;
-    A.cum = static_cast<int32_t *>(J.workspace);
     uint8_t *ws = static_cast<uint8_t *>(J.workspace);
-    A.count = reinterpret_cast<uint32_t *>(ws + attn::cum_bytes(J));
+    A.count = reinterpret_cast<uint32_t *>(ws);
+    A.cum = reinterpret_cast<int32_t *>(ws + attn::kCountBytes);
     A.parts = reinterpret_cast<float *>(ws + attn::head_bytes(A));
     A.tc_parts = A.parts + attn::part_bytes(A) / 4;
     return J.cache.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A, s) : attn::launch_t<__half>(A, s);

@@ -15,6 +15,7 @@ namespace attn {
 
 constexpr int kSms = 152;           // the grids are cut for this many
 constexpr int kPlans = 8;
+constexpr int kMostCtas = 3;       // CTAs of the own-keys kernel per SM, at most
 constexpr int kTcRows = 128;       // rows of a tile of the tensor-core prefix kernel
 
 // Rows: row r = t*G + g of a (sequence, key head) pair is token t and query
@@ -35,8 +36,8 @@ struct Args {
     int32_t grid;            // CTAs of the own-keys kernel, a chunk of the work each at most
     int32_t resident;        // of which so many fit an SM together
     int32_t page_shift;      // log2(page_size), or -1
+    uint32_t *count;         // workspace: arrivals, by an item's first chunk; zero between calls
     int32_t *cum;            // workspace: [B + 1] steps of the sequences before b
-    uint32_t *count;         // workspace: arrivals per own item, zero between calls
     float *parts;            // workspace: the partial results
     // the prefix on the tensor cores (tc_items = 0: its items are above, with the own ones)
     int32_t tc_tiles, tc_groups;   // 128-row tiles per key head, and pairs of them

@@ -238,7 +238,7 @@ class AttnJob(_Job):
     token rows may be strided views) and out [B, T, Hq, D] (the cache's type or
     fp32), optionally lse [B, T, Hq] fp32; scale defaults to 1/sqrt(D).  The
     workspace is made here (or given: zeroed once, at least
-    trit_attn_workspace_bytes)."""
+    trit_attn_workspace_bytes; jobs of any sizes may share one, one call at a time)."""
 
     def __init__(self, cache: KvCache, batch: KvBatch, q, out, lse=None, scale=None, workspace=None):
         B, T, D, dt = batch.B, batch.T, cache.k.shape[3], cache.k.dtype

@@ -663,7 +663,8 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
  *   lse  [B][T][Hq] fp32, or NULL
  *   workspace  trit_attn_workspace_bytes(job) bytes (its pointers are not read),
  *        16-byte aligned, zeroed once before its first use; every call leaves it
- *        ready for the next.  Calls that may run at the same time need one each.
+ *        ready for the next, of the same sizes or others that it has room for.  Calls
+ *        that may run at the same time need one each.
  */
 typedef struct trit_attn_job {
     trit_kv_cache cache;
