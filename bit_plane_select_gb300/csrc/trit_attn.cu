@@ -51,6 +51,17 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
+// Whether one of two 16-bit values is an infinity or NaN, and a pair with such values
+// replaced by 0.
+template <typename T>
+__host__ __device__ constexpr uint32_t inf_bits() { return 0x7c00u; }
+template <>
+__host__ __device__ constexpr uint32_t inf_bits<__nv_bfloat16>() { return 0x7f80u; }
+template <typename T>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
+    constexpr uint32_t kInf = inf_bits<T>();
+    return ((v & 0x7fffu) >= kInf ? 0u : v & 0xffffu) | (((v >> 16) & 0x7fffu) >= kInf ? 0u : v & 0xffff0000u);
+}
 // The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
 __device__ __forceinline__ uint32_t transposed8(uint32_t v) {
     uint32_t d;
@@ -272,7 +283,8 @@ __device__ __forceinline__ void count_steps(const Args &A, const Batch &S, int32
 }
 
 // One part joined to l and v, which are against `base`.  A part without keys
-// (m = -inf, l = 0) holds no sums: its o was never written.
+// (m = -inf, l = 0) holds no sums: its o was never written, or is that of a row that
+// sees none of the keys, summed up all the same.
 __device__ __forceinline__ void add_part(float2 ml, float4 x, float base, float &l, float4 &v) {
     if (ml.x == -INFINITY && ml.y == 0.0f) return;
     const float f = ex2(ml.x - base);
@@ -454,9 +466,67 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     float o[D / 16][NB][4];
     float m[NB][2], l[NB][2];
     int lim[NB][2];
-    int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no row's limit lies below `clear`
+    uint32_t blind = 0;      // the thread's rows that see none of the item's keys
+    int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no limit lies below `clear`
     uint32_t q_now = 0;                                    // the item's queries
     int cq = 0;
+
+    // A stage that some rows see in part only: an infinity or NaN of V must not reach the rows that
+    // its key is hidden from, and their P = 0 would not keep it away (0 * inf is NaN).  Such
+    // values are added to the rows that do see them one by one, and are 0 in the stage from
+    // there on.  Looking for them costs eight 16-byte reads a lane in those stages alone (none in
+    // a step of one token per sequence; 24 sequences of 1 to 5 drafts 40.6 -> 41.1 us).
+    auto hide_nonfinite = [&](auto nm, uint8_t *v, int key0, const auto &pf) {
+        constexpr int NM = decltype(nm)::value;
+        uint4 *v16 = reinterpret_cast<uint4 *>(v);
+        constexpr int kPerLane = KW * D / 8 / 32;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const uint4 x = v16[i * 32 + lane];
+            const uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+            bad |= (top & 0xffffu) >= inf_bits<T>() || (top >> 16) >= inf_bits<T>();
+        }
+        if (!__any_sync(~0u, bad)) return;
+#pragma unroll 1
+        for (int k = 0; k < KW; ++k) {
+            float p[NM][2];       // of this key and the thread's rows 2 (lane % 4) + e
+#pragma unroll
+            for (int n = 0; n < NM; ++n) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int i = 0; i < KW / 8; ++i)
+                    w |= pf[i >> 1][n][i & 1] & (k >> 3 == i ? ~0u : 0u);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 two = unpack16<T>(__shfl_sync(~0u, w, (2 * (lane & 3) + e) * 4 + ((k & 7) >> 1)));
+                    p[n][e] = k & 1 ? two.y : two.x;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x = *reinterpret_cast<const uint16_t *>(v + chunk_at<D>(k, 2 * d + i) + 2 * (lane >> 2));
+                    if ((x & 0x7fffu) < inf_bits<T>()) continue;
+#pragma unroll
+                    for (int n = 0; n < NM; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (key0 + k < lim[n][e]) o[d][n][2 * i + e] += p[n][e] * unpack16<T>(x).x;
+                }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < kPerLane; ++i) {
+            uint4 x = v16[i * 32 + lane];
+            x.x = finite_pair<T>(x.x); x.y = finite_pair<T>(x.y);
+            x.z = finite_pair<T>(x.z); x.w = finite_pair<T>(x.w);
+            v16[i * 32 + lane] = x;
+        }
+        __syncwarp();
+    };
 
     // The products of one stage with the item's first NM tiles of 8 rows.  Keys and
     // columns of V are the m16 side, rows the n8 side: S^T = K Q^T, O^T += V^T P^T.  A
@@ -562,6 +632,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     o[d][n][3] *= alpha[n][1];
                 }
         }
+        if (masked && clear < nkeys)       // (what follows nkeys is zeros)
+            hide_nonfinite(nm, ring + (vaddr - ring_at), key0, pf);
         const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
         for (int km = 0; km < KM; ++km)
@@ -587,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
             const int rows = p.b < 0 ? B * A.R : A.R;
             tiles = NB == 1 ? 1 : min(NB, (rows - p.tile * RT + 7) >> 3);
             clear = nkeys;
+            blind = 0;
             const int fresh_own = p.b < 0 ? 0 : S.fresh[p.b], len_own = p.b < 0 ? 0 : S.len[p.b];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
@@ -595,16 +668,22 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     const int row = p.tile * RT + n * 8 + 2 * (lane & 3) + e;
                     m[n][e] = -INFINITY;
                     l[n][e] = 0.0f;
-                    int see = nkeys;
+                    // rows that see no key (padding, tokens before own key 0) or are not there
+                    // have no limit, so that they ask for no masks: what they sum up is left out
+                    int see = 0;
                     if (p.b >= 0) {
                         const int t = token_of(A, row);
-                        see = t < fresh_own ? max(len_own - fresh_own + t + 1, 0) : 0;
+                        if (t < fresh_own) see = len_own - fresh_own + t + 1;
                     } else if (row < rows) {
                         const int b = row / A.R;
-                        if (token_of(A, row - b * A.R) >= S.fresh[b]) see = 0;
+                        if (token_of(A, row - b * A.R) < S.fresh[b]) see = nkeys;
                     }
-                    lim[n][e] = row < rows ? see : nkeys;      // rows that are not there: never looked at
-                    clear = min(clear, lim[n][e]);
+                    if (row >= rows || see <= 0) {
+                        blind |= 1u << (2 * n + e);
+                        see = nkeys;
+                    }
+                    lim[n][e] = see;
+                    clear = min(clear, see);
                 }
 #pragma unroll
             for (int d = 0; d < D / 16; ++d)
@@ -650,8 +729,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                         sum += __shfl_xor_sync(~0u, sum, 8);
                         sum += __shfl_xor_sync(~0u, sum, 16);
                         if (lane < 4) {
-                            stats[(warp * RT + half * 16 + r) * 2] = m[n][e];
-                            stats[(warp * RT + half * 16 + r) * 2 + 1] = sum;
+                            const bool none = (blind >> (2 * n + e)) & 1;
+                            stats[(warp * RT + half * 16 + r) * 2] = none ? -INFINITY : m[n][e];
+                            stats[(warp * RT + half * 16 + r) * 2 + 1] = none ? 0.0f : sum;
                         }
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d)
@@ -674,11 +754,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                     float sum = 0.0f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float f = ex2(stats[(w * RT + half * 16 + r) * 2] - base);
-                        const float4 x = *reinterpret_cast<const float4 *>(
+                        const float2 ml = *reinterpret_cast<const float2 *>(stats + (w * RT + half * 16 + r) * 2);
+                        float4 x = *reinterpret_cast<const float4 *>(
                             all + w * kStages * (kStageBytes / 4) + r * D + cs);
+                        // as add_part, without a branch that the next warp's loads would wait for
+                        const bool none = ml.x == -INFINITY && ml.y == 0.0f;
+                        x.x = none ? 0.0f : x.x; x.y = none ? 0.0f : x.y;
+                        x.z = none ? 0.0f : x.z; x.w = none ? 0.0f : x.w;
+                        const float f = ex2(ml.x - base);
                         v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
-                        sum += f * stats[(w * RT + half * 16 + r) * 2 + 1];
+                        sum += f * ml.y;
                     }
                     if (direct) {
                         const int t = token_of(A, row), g = row - t * G;
