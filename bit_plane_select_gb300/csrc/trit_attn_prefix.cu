@@ -216,8 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *pv_done = o_full + 2;      // stream's product into O has completed
     uint64_t *q_full = pv_done + 2;
     uint64_t *tail = q_full + 1;         // the last V block's copies, before its end is cleared
-    constexpr int kBars = 2 * kRing + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
+    uint64_t *go = tail + 1;             // the second stream may start
+    constexpr int kBars = 2 * kRing + 17;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(go + 1);
     uint32_t *timed_out = tmem_slot + 1;
 
     const trit_attn_job &J = A.J;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = lane;
         const int count = i < kRing ? 1 : i < 2 * kRing ? (pair ? 2 : 1)     // empty: streams that read the tile
                         : i < 2 * kRing + 2 ? 1 : i < 2 * kRing + 10 ? 4      // s_full, p_full (warps)
-                        : i < 2 * kRing + 14 ? 1 : i == 2 * kRing + 14 ? 8 : 1;   // o_full and pv_done, q_full (warps), tail
+                        : i < 2 * kRing + 14 ? 1 : i == 2 * kRing + 14 ? 8 : 1;   // o_full and pv_done, q_full (warps), tail, go
         mbar_init(full + i, uint32_t(count));
         if (i == 0) *timed_out = 0;
         fence_barrier_init();
@@ -267,7 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the same stage has completed for the waiter: for a pair both streams consume every
     // tile; for one tile every stage serves one stream (K of odd blocks 1, of even ones 3, V
     // of odd blocks 0, of even ones 2) but for K0, which the second stream waits for before it
-    // starts.  (The last V keeps its place behind a K that is not there.)
+    // starts.  (The last V keeps its place behind a K that is not there.)  That wait is on a
+    // barrier of its own, which completes once: the first stream's barriers go on without the
+    // second, and a phase that it did not look at in time would not come again.
     auto k_at = [&](int j) { return pair ? 2 * j : (j == 0 ? 0 : 2 * j - 1); };
     auto v_at = [&](int j) { return pair ? 2 * j + 1 : 2 * j + 2; };
 
@@ -364,11 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = warp_wait(q_full, 0, timed_out);
         // the streams start half a block apart: in step, they would want the tensor
         // pipe together and then the exponentials together (measured: 4100 SM-clocks a
-        // block pair in step)
-        if (s == 1) {
-            ok = ok && warp_wait(&p_full[3], 0, timed_out);
-            if (n >= 8) ok = ok && warp_wait(&p_full[0], 1, timed_out);
-        }
+        // block pair in step): with the first stream's second block, or behind its first where
+        // there are few
+        const int go_block = n >= 8 ? 1 : 0, go_part = n >= 8 ? 0 : 3;
+        if (s == 1) ok = ok && warp_wait(go, 0, timed_out);
         if (ok && mine > 0) {
             ok = k_there(0);
             if (ok) issue_s(0);
@@ -381,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int part = 0; part < 4; ++part) {
                 ok = ok && warp_wait(&p_full[4 * s + part], i & 1, timed_out);
                 if (!ok) break;
+                if (s == 0 && i == go_block && part == go_part && lane == 0) mbar_arrive(go);
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
