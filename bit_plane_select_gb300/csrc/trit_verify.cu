@@ -128,6 +128,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kTh
     __shared__ unsigned long long keys[kCluster];     // in the first CTA: one per CTA
     __shared__ int sh_kept;
     const int b = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, tid = threadIdx.x;
+    // the first CTA's shared memory may be written once it is known to run: arrive here, wait before the store
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     pdl_wait();
     pdl_launch();
     const S *P = static_cast<const S *>(J.p) + b * J.p_seq_stride;
@@ -178,6 +180,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kTh
         best.see(as_f32<S>(p[i]) - (q ? as_f32<S>(q[i]) : 0.0f), e[i], uint32_t(i));
     }
     unsigned long long key = block_max<kThreads>(key_of(best), sh);
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (tid == 0) {
         uint32_t to_first;
         asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_first) : "r"(uint32_t(__cvta_generic_to_shared(&keys[rank]))));
