@@ -191,10 +191,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, kTh
     key = 0;
 #pragma unroll
     for (int k = 0; k < kCluster; ++k) key = keys[k] > key ? keys[k] : key;
-    if (key == 0 && q) {      // the residual is empty: p decides
+    if (key == 0 && q) {      // no candidate: where the residual is nowhere positive, p decides
         best = Best{-1.0f, 0u};
-        for (int64_t i = tid; i < J.V; i += kThreads) best.see(as_f32<S>(p[i]), e[i], uint32_t(i));
-        key = block_max<kThreads>(key_of(best), sh);
+        int positive = 0;
+        for (int64_t i = tid; i < J.V; i += kThreads) {
+            const float pi = as_f32<S>(p[i]);
+            positive |= pi - as_f32<S>(q[i]) > 0.0f;
+            best.see(pi, e[i], uint32_t(i));
+        }
+        if (!__syncthreads_or(positive)) key = block_max<kThreads>(key_of(best), sh);
     }
     for (int t = tid; t <= J.T; t += kThreads) {
         int v = -1;
