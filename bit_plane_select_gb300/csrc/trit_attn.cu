@@ -394,10 +394,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
         for (int b = blockIdx.x; b < B; b += gridDim.x) {
             if (cum[b] != cum[b + 1]) continue;
             const int64_t at = int64_t(b) * J.batch.T * J.q_heads;
-            const int rows = J.batch.T * J.q_heads;
-            for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads)
-                store_out<T>(J, at * D + int64_t(i) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-            for (int i = threadIdx.x; J.lse && i < rows; i += kThreads) J.lse[at + i] = -INFINITY;
+            const int64_t rows = int64_t(J.batch.T) * J.q_heads;      // times D: more than 31 bits
+            for (int64_t i = threadIdx.x; i < rows * (D / 4); i += kThreads)
+                store_out<T>(J, at * D + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+            for (int64_t i = threadIdx.x; J.lse && i < rows; i += kThreads) J.lse[at + i] = -INFINITY;
         }
     }
     if (lo >= hi) {
