@@ -253,7 +253,7 @@ __device__ __forceinline__ void count_steps(const Args &A, const Batch &S, int32
     const int B = A.J.batch.B, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cap = A.J.batch.table_pages * A.J.cache.page_size;
     for (int i = tid; i < B; i += kThreads) {
-        const int n = A.J.batch.lens[i], m = batch_new(A.J.batch, i);
+        const int n = A.J.batch.lens[i], m = batch_new(A.J.batch, i, report ? A.err : nullptr);
         S.len[i] = n < 0 ? 0 : (n > cap ? cap : n);
         S.fresh[i] = m;
         if (report && (n < 0 || n > cap)) raise_flag(A.err, TRIT_ERR_INDEX);

@@ -14,10 +14,13 @@ __device__ __forceinline__ void raise_flag(uint32_t *err, uint32_t bit) {
     if ((*reinterpret_cast<volatile uint32_t *>(err) & bit) == 0) atomicOr(err, bit);
 }
 
-// The number of valid new tokens of sequence b, clamped to [0, T].
-__device__ __forceinline__ int batch_new(const trit_kv_batch &B, int b) {
-    int n = B.new_lens ? B.new_lens[b] : B.T;
-    return n < 0 ? 0 : (n > B.T ? B.T : n);
+// The number of valid new tokens of sequence b, clamped to [0, T]; with an `err`, a
+// number outside that range is flagged there.
+__device__ __forceinline__ int batch_new(const trit_kv_batch &B, int b, uint32_t *err = nullptr) {
+    const int n = B.new_lens ? B.new_lens[b] : B.T;
+    if (n >= 0 && n <= B.T) return n;
+    if (err) raise_flag(err, TRIT_ERR_INDEX);
+    return n < 0 ? 0 : B.T;
 }
 
 // Two fp32 values as a pair of 16-bit ones, x in the low half, rounded to nearest even.

@@ -592,8 +592,9 @@ typedef struct trit_kv_cache {
  * table[b * table_stride + i / page_size].  lens counts the new tokens too: of
  * n = new_lens[b] (T where new_lens is NULL), token t < n is own key
  * i = lens[b] - n + t at position prefix_len + i, and sees the whole prefix
- * and own keys 0..i.  Tokens t >= n are padding.  Tables, lens and new_lens are
- * read by the kernels when they run; prefix_len is fixed by the call.
+ * and own keys 0..i.  Tokens t >= n are padding.  A new_lens[b] outside [0, T] is
+ * clamped, with TRIT_ERR_INDEX.  Tables, lens and new_lens are read by the kernels
+ * when they run; prefix_len is fixed by the call.
  */
 typedef struct trit_kv_batch {
     const int32_t *prefix_table;  /* [prefix_pages]; may be NULL when prefix_len = 0 */
