@@ -300,7 +300,7 @@ template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __grid_constant__ Args A) {
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int RT = 8 * NB;
-    constexpr int KW = keys_of_stage(D), NT = KW / 8, kStep = KW * kWarps;
+    constexpr int KW = keys_of_stage(D), kStep = KW * kWarps;
     constexpr int kStageBytes = 2 * KW * D * 2;
     constexpr int kQueries = kStages + 1;     // query tiles: the loads run at most kStages items ahead
     static_assert(kStageBytes >= 16 * D * 4, "a stage holds one m16 tile of fp32 sums");

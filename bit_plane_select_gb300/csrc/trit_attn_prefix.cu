@@ -164,13 +164,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *v) {
         : TRIT_R8(v, 0), TRIT_R8(v, 8), TRIT_R8(v, 16), TRIT_R8(v, 24)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::TRIT_W8(v, 0),
-        TRIT_W8(v, 8), TRIT_W8(v, 16), TRIT_W8(v, 24), "r"(addr)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"

@@ -67,6 +67,7 @@ __device__ __forceinline__ void store_row(T *p, const float (&y)[W]) {
 template <typename T, typename S, int D, bool PAIRS, int W>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs A) {
     const trit_kv_append_job &J = A.J;
+    static_assert(W == 8 || (W == 4 && !PAIRS), "angles are read four at a time");
     constexpr int L = D / W;             // lanes of one head vector
     constexpr int V = 32 / L;            // vectors of a warp step
     const int lane = threadIdx.x & 31, sub = lane % L, which = lane / L;
@@ -112,15 +113,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         // the lane's angles, and the page beside them
         if (in && turns) {
             const int64_t at = pos * half + (PAIRS ? j0 / 2 : j0 < half ? j0 : j0 - half);
-            if (CW == 2) {
-                const float2 cc = __ldg(reinterpret_cast<const float2 *>(J.cos + at));
-                const float2 ss = __ldg(reinterpret_cast<const float2 *>(J.sin + at));
-                c[0] = cc.x; c[1] = cc.y;
-                s[0] = ss.x; s[1] = ss.y;
-            } else {
-                load_row<CW < 4 ? 4 : CW>(J.cos + at, reinterpret_cast<float(&)[CW < 4 ? 4 : CW]>(c));
-                load_row<CW < 4 ? 4 : CW>(J.sin + at, reinterpret_cast<float(&)[CW < 4 ? 4 : CW]>(s));
-            }
+            load_row<CW>(J.cos + at, c);
+            load_row<CW>(J.sin + at, s);
         }
         const int64_t col = own < 0 ? -1 : A.page_shift >= 0 ? own >> A.page_shift : own / J.cache.page_size;
         int page = -1;
