@@ -297,27 +297,41 @@ class ServedStack:
                  dtype=torch.bfloat16, eps: float = 1e-5, device="cuda"):
         from . import KvCache
         self.device, self.head_dim, self.rope, self.eps = torch.device(device), head_dim, rope, float(eps)
-        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.layers = []
-        for lw in weights:
-            P, S, shape = {}, {}, {}
+        sizes = self._sizes(weights, head_dim)
+        for lw, (K, F, heads) in zip(weights, sizes):
+            P, S = {}, {}
             for name in self.NAMES:
                 w, ws = lw[name]
                 planes, err = trit_pack(w.to(self.device), ws)
                 if int(err.item()) != 0:
                     raise ValueError(f"{name}: non-ternary weights")
-                P[name], S[name], shape[name] = planes, float(ws), tuple(w.shape)
-            K, F = shape["q"][1], shape["gate"][0]
-            heads = {n: shape[n][0] // head_dim for n in ("q", "k", "v")}
-            if (shape["o"] != (K, shape["q"][0]) or shape["k"] != shape["v"] or shape["gate"] != (F, K) or
-                    shape["up"] != (F, K) or shape["down"] != (K, F) or shape["k"][1] != K or
-                    any(heads[n] * head_dim != shape[n][0] for n in heads)):
-                raise ValueError("layer shapes do not chain")
+                P[name], S[name] = planes, float(ws)
             cache = [torch.zeros((pages, heads["k"], page_size, head_dim), dtype=dtype, device=self.device)
                      for _ in range(2)]
             gains = [lw[g].to(device=self.device, dtype=torch.float32) for g in ("attn_gain", "mlp_gain")]
             self.layers.append({"P": P, "S": S, "K": K, "F": F, "heads": heads, "cache": KvCache(*cache),
                                 "attn_gain": gains[0], "mlp_gain": gains[1]})
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    @classmethod
+    def _sizes(cls, weights, head_dim: int):
+        """(K, F, heads) of every layer: each fits itself, and all take rows of one width."""
+        sizes = []
+        for lw in weights:
+            shape = {name: tuple(lw[name][0].shape) for name in cls.NAMES}
+            K, F = shape["q"][1], shape["gate"][0]
+            heads = {n: shape[n][0] // head_dim for n in ("q", "k", "v")}
+            if (shape["o"] != (K, shape["q"][0]) or shape["k"] != shape["v"] or shape["gate"] != (F, K) or
+                    shape["up"] != (F, K) or shape["down"] != (K, F) or shape["k"][1] != K or
+                    any(heads[n] * head_dim != shape[n][0] for n in heads) or (sizes and K != sizes[0][0])):
+                raise ValueError("layer shapes do not chain")
+            if any(lw[g].numel() != K for g in ("attn_gain", "mlp_gain")):
+                raise ValueError(f"a layer's gains must hold {K} values")
+            sizes.append((K, F, heads))
+        if not sizes:
+            raise ValueError("a stack needs a layer")
+        return sizes
 
     def plan(self, batch):
         """Buffers and prepared calls for the T new tokens of every sequence of `batch`."""
@@ -347,6 +361,8 @@ class ServedStack:
         """x [B*T, K] fp32, the new tokens' rows, through every layer in place."""
         from . import (trit_attn_paged, trit_intmlp_quant, trit_kv_append, trit_quant_act,
                        trit_quant_act_folded)
+        if len(plan) != len(self.layers) or tuple(x.shape) != tuple(plan[0]["o"].shape):
+            raise ValueError("x must be [B*T, K] of the plan's batch")
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
             for L, B in zip(self.layers, plan):
                 trit_quant_act_folded(x, L["attn_gain"], self.eps, B["x_i8"], B["s"], self.err)
