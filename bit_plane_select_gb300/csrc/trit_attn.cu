@@ -20,6 +20,8 @@
 // live in registers and O is only rescaled when a maximum moved.
 // P is rounded to the cache's 16-bit type for the second product: relative
 // 2^-9 (bf16) or 2^-12 (fp16) of each term on average, the size of the output's own rounding.
+// Two sequences of 110500 and 131001 keys of 5 heads of 128, 618 MB: 102 to 104 us, 6.0
+// TB/s, 90% of a copy's rate.
 #include <type_traits>
 
 #include "trit_attn.cuh"
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
     // its key is hidden from, and their P = 0 would not keep it away (0 * inf is NaN).  Such
     // values are added to the rows that do see them one by one, and are 0 in the stage from
     // there on.  Looking for them costs eight 16-byte reads a lane in those stages alone (none in
-    // a step of one token per sequence; 24 sequences of 1 to 5 drafts 40.6 -> 41.1 us).
+    // a step of one token per sequence; 24 sequences of 1 to 5 drafts 40.4 -> 41.5 us).
     auto hide_nonfinite = [&](auto nm, uint8_t *v, int key0, const auto &pf) {
         constexpr int NM = decltype(nm)::value;
         uint4 *v16 = reinterpret_cast<uint4 *>(v);

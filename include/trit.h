@@ -653,9 +653,12 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
  *     lse = ln sum_j exp(scale * q.k_j),
  * query head h reading key head h / (Hq / heads).  Products are formed by 16-bit
  * tensor-core instructions with fp32 sums; maxima, sums and partial outputs are
- * fp32.  A row that sees no key (padding, or nothing cached) gives out = 0 and
+ * fp32.  For the second product exp(..) is rounded to the cache's type, whatever
+ * out's type (the sum it is divided by is not): up to 2^-8 (bf16) or 2^-11 (fp16) of each
+ * term.  A row that sees no key (padding, or nothing cached) gives out = 0 and
  * lse = -inf.  Keys past a sequence's length are never read: their slots may
- * hold anything.  lens[b] outside [0, table_pages * page_size] or a page id
+ * hold anything, and a later token's keys and values change nothing of an earlier
+ * one.  lens[b] outside [0, table_pages * page_size] or a page id
  * outside the cache sets TRIT_ERR_INDEX (the length is clamped, the page's keys
  * read as zeros).
  *   q    token (b, t) at (b*T + t) * q_stride elements: Hq vectors of D of the
