@@ -29,41 +29,6 @@ struct AppendArgs {
     int32_t page_shift;  // log2(page_size), or -1
 };
 
-// W consecutive values of a row, and their store.
-template <int W>
-__device__ __forceinline__ void load_row(const float *p, float (&x)[W]) {
-#pragma unroll
-    for (int i = 0; i < W; i += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
-        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-    }
-}
-template <int W, typename H>
-__device__ __forceinline__ void load_row(const H *p, float (&x)[W]) {
-    uint32_t w[W / 2];
-    if (W == 8) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x; w[1] = v.y; w[W / 2 - 2] = v.z; w[W / 2 - 1] = v.w;
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x; w[1] = v.y;
-    }
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) {
-        const float2 f = unpack16<H>(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
-}
-template <int W, typename T>
-__device__ __forceinline__ void store_row(T *p, const float (&y)[W]) {
-    uint32_t w[W / 2];
-#pragma unroll
-    for (int i = 0; i < W / 2; ++i) w[i] = pack16<T>(y[2 * i], y[2 * i + 1]);
-    if (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[W / 2 - 2], w[W / 2 - 1]);
-    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-}
-
 template <typename T, typename S, int D, bool PAIRS, int W>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs A) {
     const trit_kv_append_job &J = A.J;
