@@ -11,7 +11,8 @@ Functions carry the C names:
   trit_pack, trit_unpack, trit_verify, trit_quant_act, trit_quant_act_many,
   trit_gemv, trit_gemm, trit_gemm_many, trit_quant_gemv_many, trit_gemm_noalloc,
   trit_quant_act_folded, trit_intmlp_quant, trit_intmlp_gemv_many, trit_check_div127,
-  trit_read_probe, trit_kv_append, trit_attn_paged, trit_draft_verify
+  trit_read_probe, trit_kv_append, trit_attn_paged, trit_draft_verify,
+  trit_kv4_append, trit_kv4_read, trit_attn_paged4, trit_attn_prompt, trit_logprobs
 """
 from __future__ import annotations
 
@@ -150,13 +151,18 @@ def lib():
         L.trit_attn_workspace_bytes.argtypes = [p]
         L.trit_attn_paged.argtypes = [p, p, p]
         L.trit_draft_verify.argtypes = [p, p, p]
+        L.trit_attn4_workspace_bytes.restype = i64
+        L.trit_attn4_workspace_bytes.argtypes = [p]
+        jobs = ("trit_kv4_append", "trit_kv4_read", "trit_attn_paged4", "trit_attn_prompt", "trit_logprobs")
+        for name in jobs:
+            getattr(L, name).argtypes = [p, p, p]
         for name in ("trit_pack", "trit_unpack", "trit_verify", "trit_quant_act",
                      "trit_quant_act_many", "trit_gemv", "trit_gemm", "trit_gemm_many",
                      "trit_quant_gemv_many", "trit_gemm_noalloc", "trit_quant_act_folded",
                      "trit_intmlp_quant", "trit_check_div127", "trit_read_probe",
                      "trit_intmlp_gemv_many", "trit_bitcos_pack", "trit_bitcos_gemv_many",
                      "trit_issue_probe", "trit_mlp_gate_up", "trit_mlp_down", "trit_kv_append",
-                     "trit_attn_paged", "trit_draft_verify"):
+                     "trit_attn_paged", "trit_draft_verify") + jobs:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -623,5 +629,7 @@ def trit_bitcos_gemv_many(blist: BitcosList, stream=None):
 
 from . import serving  # noqa: E402  (binds the decode step between the products)
 from .serving import *  # noqa: E402,F401,F403
+from . import prompts  # noqa: E402  (binds prompts, the 4-bit cache and scoring)
+from .prompts import *  # noqa: E402,F401,F403
 
-__all__ += serving.__all__
+__all__ += serving.__all__ + prompts.__all__

@@ -1,0 +1,650 @@
+// trit_attn_paged4: out = softmax(scale q K^T) V over a paged cache held in 4 bits.
+//
+// Items, steps, chunks and joins are those of trit_attn_items.cuh: the keys of every
+// (sequence, key head, row tile), and of the shared prefix, in steps of 128, all steps of
+// the call cut into equal chunks, one per CTA.
+//
+// A key and head is D codes of 4 bits and D/64 pairs (s, z) for K and as much for V: 144 bytes
+// where 16 bits have 512.  At a copy's rate an SM gets 23 of them a clock, 47 codes, so
+// turning a code into an operand may cost well under two instructions.  It costs 0.6: with the
+// fp16 bit pattern of c as it stands -- c 2^-24, a subnormal -- a word of eight codes is four
+// operand registers by masking, the codes of the upper halves of bytes 16 times as large:
+//     w & 0x000f000f: c0, c4      w & 0x00f000f0: 16 c1, 16 c5      (w >> 8: c2, c6 and c3, c7).
+// K: S^T = K Q^T with the columns of a 32-column chunk in the order that this gives and
+// q in the same order, q's odd columns divided by 16.  q is scaled by a power of two per row
+// to be large in fp16 (2^14 at its largest column), so that this and fp16's range cost nothing:
+// rounding to within 2^-35 of the largest column.  The pairs come in after the products:
+//     scale q.k = f sum_groups (s (q'.c) + z sum(q')).
+// V: an ldmatrix transposing 16-bit elements, each four columns of a key, gives the same
+// word with two keys' codes, so O^T += V^T P^T has the rows of its m16 tiles in the
+// order 4 g + i.  A value's s goes to the weights: P' = p s in fp16, against a power of two that
+// bounds s in what the warp has seen (2^8 at most; rounding to 2^-11 of each term); its z to
+// sums p z, one per row and group, in fp32.
+//
+// A warp has its own ring of three stages of 32 keys, so that 150 KB an SM are in flight.
+#include <type_traits>
+
+#include "trit_attn_items.cuh"
+
+namespace trit {
+namespace attn {
+namespace {
+
+constexpr int kStages = 3;
+constexpr int KW = 32;                     // keys of a warp's stage
+constexpr int kStep = KW * kWarps;
+constexpr int kGroup = TRIT_KV4_GROUP;
+
+template <int D>
+struct Shape {
+    static constexpr int P = D / kGroup;               // groups of a vector
+    static constexpr int CB = D / 2, SB = 4 * P;       // bytes of its codes and pairs
+    static constexpr int CH = CB / 16;                 // 16-byte chunks of its codes
+    static constexpr int kVAt = KW * CB;               // a stage: K's codes, V's, K's pairs, V's
+    static constexpr int kKsAt = 2 * KW * CB, kVsAt = kKsAt + KW * SB;
+    static constexpr int kStageBytes = kVsAt + KW * SB;
+    static_assert(kStageBytes >= 8 * D * 4, "a stage holds one tile of fp32 sums");
+};
+
+struct Args4 {
+    Args A;                          // its cache: the codes, strides in vectors
+    const uint8_t *k_scale, *v_scale;
+    float scale2;                    // scale log2(e)
+};
+
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok, std::integral_constant<int, 8>) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok, std::integral_constant<int, 4>) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4u : 0u) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r of a tile of codes: eight rows at one c fall on
+// eight different quarters of the banks.
+template <int D>
+__device__ __forceinline__ uint32_t codes_at(int r, int c) {
+    return D == 128 ? uint32_t(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) : uint32_t(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+// A query tile as it is loaded.
+template <int D>
+__device__ __forceinline__ uint32_t query_at(int row, int c) {
+    return uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
+}
+
+// The operand registers of codes 0..3 of each 16 bits.
+__device__ __forceinline__ void operands(const uint32_t (&f)[4], int i, uint32_t (&a)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a[j] = (i < 2 ? f[j] : f[j] >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
+
+template <typename T, int D, int NB>
+__global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __grid_constant__ Args4 A4) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    using Sh = Shape<D>;
+    constexpr int P = Sh::P, RT = 8 * NB, kStageBytes = Sh::kStageBytes;
+    constexpr int kQueries = kStages + 1;     // query tiles: the loads run at most kStages items ahead
+    const Args &A = A4.A;
+    const trit_attn_job &J = A.J;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = smem + warp * kStages * kStageBytes;
+    const uint32_t ring_at = tc::smem_u32(ring);
+    uint8_t *queries = smem + kWarps * kStages * kStageBytes;
+    const uint32_t q_at = tc::smem_u32(queries), q_bytes = RT * D * 2;
+    uint4 *frag = reinterpret_cast<uint4 *>(queries + kQueries * q_bytes);       // [NB][P][2][32]
+    float *facs = reinterpret_cast<float *>(frag + NB * P * 64);                 // [RT] factors f
+    float *qsum = facs + RT;                                                     // [RT][P] 2^-24 sum(q')
+    float *stats = qsum + RT * P;                                                // [kWarps][RT] (m, l)
+    int32_t *scratch = reinterpret_cast<int32_t *>(stats + kWarps * RT * 2);
+    Batch S;
+    S.cum = scratch + kWarps;
+    S.len = S.cum + J.batch.B + 1;
+    S.fresh = S.len + J.batch.B;
+    const int32_t *cum = S.cum;
+
+    pdl_wait();
+    pdl_launch();
+    {   // the page table on its way to L2 while the lengths are: every CTA a few lines of it
+        const int64_t ints = int64_t(J.batch.B - 1) * J.batch.table_stride + J.batch.table_pages;
+        const int64_t at = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 32;
+        if (at < ints) asm volatile("prefetch.global.L2 [%0];" ::"l"(J.batch.table + at));
+    }
+    count_steps<kStep>(A, S, scratch, blockIdx.x == 0);
+    const int B = J.batch.B, Hkv = J.cache.heads, G = A.G;
+    const int64_t pre = int64_t(Hkv) * A.pre_tiles * A.pre_steps;
+    const int64_t W = pre + int64_t(cum[B]) * Hkv * A.own_tiles;
+    // this CTA's chunk
+    const int64_t count = chunk_count(A, W);
+    const int64_t lo = blockIdx.x < count ? chunk_start(blockIdx.x, W, count) : W;
+    const int64_t hi = blockIdx.x < count ? chunk_start(blockIdx.x + 1, W, count) : W;
+
+    // the ring runs ahead of the products, across items: keys and values by stage, and
+    // an item's queries with its first stage (each warp a quarter of the rows)
+    int64_t lu = lo;
+    Place lp = {};
+    Keys lk = {};
+    int lq = 0, page = -1;       // page: of the lane's key of the next stage to load
+    bool lnew = true;
+    auto key_of_lane = [&]() { return lp.step * kStep + warp * KW + lane; };
+    auto fetch_page = [&]() {
+        const int k = key_of_lane();
+        page = k < lk.n ? __ldg(lk.table + (A.page_shift >= 0 ? k >> A.page_shift : k / J.cache.page_size)) : -1;
+    };
+    if (lo < hi) {
+        lp = place_of(A, cum, lo);
+        lk = keys_of(A, S, lp);
+        fetch_page();
+    }
+    Place p = lp;
+    auto load_queries = [&]() {
+        constexpr int CH = D / 8, RI = 32 / CH;
+        const int rows = lp.b < 0 ? B * A.R : A.R, c = lane % CH;
+#pragma unroll
+        for (int j = 0; j < (RT + kWarps * RI - 1) / (kWarps * RI); ++j) {
+            const int rl = (j * kWarps + warp) * RI + lane / CH, row = lp.tile * RT + rl;
+            if (rl >= RT) continue;
+            const int b = lp.b < 0 ? row / A.R : lp.b, r = lp.b < 0 ? row - b * A.R : row;
+            const int t = token_of(A, r);
+            const bool ok = row < rows && t < S.fresh[b];
+            const T *q = static_cast<const T *>(J.q);
+            if (ok) q += (int64_t(b) * J.batch.T + t) * J.q_stride + (int64_t(lp.h) * G + r - t * G) * D + c * 8;
+            cp_async16(q_at + lq * q_bytes + query_at<D>(rl, c), q, ok);
+        }
+        lq = lq + 1 == kQueries ? 0 : lq + 1;
+    };
+    // The copies of the warp's 32 keys of a step; a lane finds one key's place.  Rows past the
+    // end and rows of pages outside the cache are filled with zeros.
+    auto load_stage = [&](uint32_t st) {
+        const int k = key_of_lane();
+        const bool in = k < lk.n, good = in && page >= 0 && page < J.cache.pages;
+        if (in && !good) raise_flag(A.err, TRIT_ERR_INDEX);
+        const int col = A.page_shift >= 0 ? k >> A.page_shift : k / J.cache.page_size;
+        const int64_t vec = good ? page * J.cache.page_stride + int64_t(k - col * J.cache.page_size) * J.cache.slot_stride +
+                                       lp.h * J.cache.head_stride
+                                 : 0;
+        cp_async_small(st + Sh::kKsAt + lane * Sh::SB, A4.k_scale + vec * Sh::SB, good, std::integral_constant<int, Sh::SB>{});
+        cp_async_small(st + Sh::kVsAt + lane * Sh::SB, A4.v_scale + vec * Sh::SB, good, std::integral_constant<int, Sh::SB>{});
+        const uint32_t there = __ballot_sync(~0u, good);
+        constexpr int RI = 32 / Sh::CH;                 // keys of one copy instruction
+        const int c = lane % Sh::CH;
+#pragma unroll
+        for (int j = 0; j < KW / RI; ++j) {
+            const int r = j * RI + lane / Sh::CH;
+            const int64_t at = __shfl_sync(~0u, vec, r) * Sh::CB + c * 16;
+            const bool ok = (there >> r) & 1;
+            const uint32_t dst = st + codes_at<D>(r, c);
+            cp_async16(dst, static_cast<const uint8_t *>(J.cache.k) + at, ok);
+            cp_async16(dst + Sh::kVAt, static_cast<const uint8_t *>(J.cache.v) + at, ok);
+        }
+    };
+    auto load_next = [&](int stage) {
+        if (lu < hi) {
+            if (lnew) {
+                load_queries();
+                lnew = false;
+            }
+            load_stage(ring_at + stage * kStageBytes);
+            if (++lu < hi) {
+                if (++lp.step == lp.steps) {
+                    next_item(A, S, lp);
+                    lk = keys_of(A, S, lp);
+                    lnew = true;
+                }
+                fetch_page();
+            }
+        }
+        tc::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int s = 0; s < kStages; ++s) load_next(s);
+
+    // the join's copy of the sums, and the rows of sequences without a key (in no CTA's share)
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i <= B; i += kThreads) A.cum[i] = cum[i];
+    if (J.batch.prefix_len == 0) {
+        for (int b = blockIdx.x; b < B; b += gridDim.x) {
+            if (cum[b] != cum[b + 1]) continue;
+            const int64_t at = int64_t(b) * J.batch.T * J.q_heads;
+            const int64_t rows = int64_t(J.batch.T) * J.q_heads;
+            for (int64_t i = threadIdx.x; i < rows * (D / 4); i += kThreads)
+                store_out<T>(J, at * D + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+            for (int64_t i = threadIdx.x; J.lse && i < rows; i += kThreads) J.lse[at + i] = -INFINITY;
+        }
+    }
+    if (lo >= hi) return;
+
+    float o[P][4][NB][4];        // columns 64 p + 32 (e / 2) + 4 (lane / 4) + i, row 2 (lane % 4) + e % 2
+    float z[P][NB][2];           // sum of p z over the lane's keys
+    float m[NB][2], l[NB][2];
+    int lim[NB][2];
+    int bound[P];                // exponent field that no s seen so far exceeds
+    uint32_t blind = 0;      // the thread's rows that see none of the item's keys
+    int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no limit lies below `clear`
+    int cq = 0;
+    uint4 held[NB == 1 ? P : 1][2];                        // one tile's queries stay in registers
+
+    // An item's queries as operands: warp n takes tile n.  Lane (g, t) has of row g the
+    // columns 64 p + 32 b + 8 t + 0..7; operand i of chunk b is its columns i and i + 4.
+    auto prepare_queries = [&](const uint8_t *raw) {
+        if (warp >= NB) return;
+        const int row = warp * 8 + (lane >> 2), t = lane & 3;
+        float v[P][2][8], most = 0.0f;
+#pragma unroll
+        for (int pg = 0; pg < P; ++pg)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(raw + query_at<D>(row, 8 * pg + 4 * b + t));
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack16<T>(w[k]);
+                    v[pg][b][2 * k] = f.x;
+                    v[pg][b][2 * k + 1] = f.y;
+                    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 2));
+        // the largest column to [2^14, 2^15), as far as the factor back (2^(24 - e)) stays in range
+        int e = 14 - ((__float_as_int(most) >> 23) - 127);
+        e = e > 100 ? 100 : e < -100 ? -100 : e;
+        const float f[2] = {power2(e), power2(e - 4)};
+#pragma unroll
+        for (int pg = 0; pg < P; ++pg) {
+            uint32_t w[8];
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    w[2 * i + b] = pack16<__half>(v[pg][b][i] * f[i & 1], v[pg][b][i + 4] * f[i & 1]);
+                    const float2 r = unpack16<__half>(w[2 * i + b]);
+                    sum = fmaf(r.x + r.y, i & 1 ? 16.0f : 1.0f, sum);
+                }
+            frag[((warp * P + pg) * 2) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+            frag[((warp * P + pg) * 2 + 1) * 32 + lane] = make_uint4(w[4], w[5], w[6], w[7]);
+            sum += __shfl_xor_sync(~0u, sum, 1);
+            sum += __shfl_xor_sync(~0u, sum, 2);
+            if (t == 0) qsum[row * P + pg] = sum * 0x1p-24f;
+        }
+        if (t == 0) facs[row] = A4.scale2 * power2(24 - e);
+    };
+
+    // The products of one stage with the item's first NM tiles of 8 rows.
+    auto products = [&](auto nm, const uint8_t *st, uint32_t st_at, int key0) {
+        constexpr int NM = decltype(nm)::value, KM = KW / 16;
+        const int g = lane >> 2, t2 = 2 * (lane & 3);
+        float s[KM][NM][4];
+        const int arow = ((lane >> 3) & 1) * 8 + (lane & 7), ach = lane >> 4;
+#pragma unroll
+        for (int km = 0; km < KM; ++km) {
+#pragma unroll
+            for (int n = 0; n < NM; ++n) s[km][n][0] = s[km][n][1] = s[km][n][2] = s[km][n][3] = 0.0f;
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg) {
+                uint32_t f[4], a[4][4];
+                ldsm4(f, st_at + codes_at<D>(km * 16 + arow, 2 * pg + ach));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) operands(f, i, a[i]);
+                const __half2 *ks = reinterpret_cast<const __half2 *>(st + Sh::kKsAt) + pg;
+                const float2 k0 = __half22float2(ks[(km * 16 + g) * P]), k1 = __half22float2(ks[(km * 16 + 8 + g) * P]);
+#pragma unroll
+                for (int n = 0; n < NM; ++n) {
+                    const uint4 q0 = NB == 1 ? held[NB == 1 ? pg : 0][0] : frag[((n * P + pg) * 2) * 32 + lane];
+                    const uint4 q1 = NB == 1 ? held[NB == 1 ? pg : 0][1] : frag[((n * P + pg) * 2 + 1) * 32 + lane];
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816<__half>(acc, a[0], q0.x, q0.y);
+                    mma16816<__half>(acc, a[1], q0.z, q0.w);
+                    mma16816<__half>(acc, a[2], q1.x, q1.y);
+                    mma16816<__half>(acc, a[3], q1.z, q1.w);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float qs = qsum[(n * 8 + t2 + e) * P + pg];
+                        s[km][n][e] = fmaf(k0.x, acc[e], fmaf(k0.y, qs, s[km][n][e]));
+                        s[km][n][2 + e] = fmaf(k1.x, acc[2 + e], fmaf(k1.y, qs, s[km][n][2 + e]));
+                    }
+                }
+            }
+        }
+        const bool masked = key0 + KW > clear;
+        float alpha[NM][2];
+        bool moved = false;
+#pragma unroll
+        for (int n = 0; n < NM; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = facs[n * 8 + t2 + e];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int km = 0; km < KM; ++km)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &v = s[km][n][2 * i + e];
+                        v *= f;
+                        if (masked && key0 + km * 16 + i * 8 + g >= lim[n][e]) v = -INFINITY;
+                        mx = fmaxf(mx, v);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+                const float top = fmaxf(m[n][e], mx), base = base_of(top);
+                alpha[n][e] = ex2(m[n][e] - base);
+                moved |= alpha[n][e] != 1.0f;
+                m[n][e] = top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int km = 0; km < KM; ++km)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float &v = s[km][n][2 * i + e];
+                        v = ex2(v - base);
+                        sum += v;
+                    }
+                l[n][e] = l[n][e] * alpha[n][e] + sum;
+            }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg)
+#pragma unroll
+                for (int n = 0; n < NM; ++n) {
+                    z[pg][n][0] *= alpha[n][0];
+                    z[pg][n][1] *= alpha[n][1];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= alpha[n][e & 1];
+                }
+        }
+        const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;
+#pragma unroll
+        for (int pg = 0; pg < P; ++pg) {
+            const __half2 *vs = reinterpret_cast<const __half2 *>(st + Sh::kVsAt) + pg;
+            // the greatest s of the stage, by its exponent: a lane looks at one key
+            const uint32_t most = __reduce_max_sync(~0u, (*reinterpret_cast<const uint32_t *>(vs + lane * P) >> 10) & 31u);
+            if (int(most) > bound[pg]) {
+                const int to = int(most) + 1;
+                const float f = bound[pg] < 0 ? 0.0f : power2(bound[pg] - to);      // (nothing summed up yet: 0)
+                bound[pg] = to;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NM; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= f;
+            }
+            const float inv = power2(22 - bound[pg]);       // s inv < 2^8
+#pragma unroll
+            for (int km = 0; km < KM; ++km) {
+                const float2 v0 = __half22float2(vs[(km * 16 + g) * P]), v1 = __half22float2(vs[(km * 16 + 8 + g) * P]);
+                const float s0 = v0.x * inv, s1 = v1.x * inv;
+                uint32_t w[NM][2];
+#pragma unroll
+                for (int n = 0; n < NM; ++n) {
+                    const float(&q)[4] = s[km][n];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // a hidden key's z may be NaN
+                        const bool h0 = masked && key0 + km * 16 + g >= lim[n][e], h1 = masked && key0 + km * 16 + 8 + g >= lim[n][e];
+                        z[pg][n][e] = fmaf(q[e], h0 ? 0.0f : v0.y, fmaf(q[2 + e], h1 ? 0.0f : v1.y, z[pg][n][e]));
+                    }
+                    w[n][0] = transposed8(pack16<__half>(q[0] * s0, q[1] * s0));
+                    w[n][1] = transposed8(pack16<__half>(q[2] * s1, q[3] * s1));
+                }
+                uint32_t f[4];
+                ldsm4t(f, st_at + Sh::kVAt + codes_at<D>(km * 16 + vrow, 2 * pg + vch));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a[4];
+                    operands(f, i, a);
+#pragma unroll
+                    for (int n = 0; n < NM; ++n) mma16816<__half>(o[pg][i][n], a, w[n][0], w[n][1]);
+                }
+            }
+        }
+    };
+
+    int64_t u = lo;
+    bool fresh = true;
+    int stage = 0;
+    while (u < hi) {
+        tc::cp_async_wait<kStages - 1>();
+        if (fresh) {
+            fresh = false;
+            if (u != lo) next_item(A, S, p);
+            first_step = p.step;
+            nkeys = keys_of(A, S, p).n;
+            const int rows = p.b < 0 ? B * A.R : A.R;
+            tiles = NB == 1 ? 1 : min(NB, (rows - p.tile * RT + 7) >> 3);
+            clear = nkeys;
+            blind = 0;
+            const int fresh_own = p.b < 0 ? 0 : S.fresh[p.b], len_own = p.b < 0 ? 0 : S.len[p.b];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = p.tile * RT + n * 8 + 2 * (lane & 3) + e;
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.0f;
+                    // rows that see no key (padding, tokens before own key 0) or are not there
+                    // have no limit, so that they ask for no masks: what they sum up is left out
+                    int see = 0;
+                    if (p.b >= 0) {
+                        const int t = token_of(A, row);
+                        if (t < fresh_own) see = len_own - fresh_own + t + 1;
+                    } else if (row < rows) {
+                        const int b = row / A.R;
+                        if (token_of(A, row - b * A.R) < S.fresh[b]) see = nkeys;
+                    }
+                    if (row >= rows || see <= 0) {
+                        blind |= 1u << (2 * n + e);
+                        see = nkeys;
+                    }
+                    lim[n][e] = see;
+                    clear = min(clear, see);
+                }
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg) {
+                bound[pg] = -1;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    z[pg][n][0] = z[pg][n][1] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[pg][i][n][0] = o[pg][i][n][1] = o[pg][i][n][2] = o[pg][i][n][3] = 0.0f;
+                }
+            }
+            clear = min(clear, __shfl_xor_sync(~0u, clear, 1));
+            clear = min(clear, __shfl_xor_sync(~0u, clear, 2));
+            __syncthreads();               // the other warps' rows of the queries
+            prepare_queries(queries + cq * q_bytes);
+            cq = cq + 1 == kQueries ? 0 : cq + 1;
+            __syncthreads();
+            if (NB == 1) {
+#pragma unroll
+                for (int pg = 0; pg < (NB == 1 ? P : 0); ++pg) {
+                    held[pg][0] = frag[(pg * 2) * 32 + lane];
+                    held[pg][1] = frag[(pg * 2 + 1) * 32 + lane];
+                }
+            }
+        }
+        __syncwarp();
+        const int key0 = p.step * kStep + warp * KW;
+        uint8_t *st = ring + stage * kStageBytes;
+        if (key0 < nkeys) {
+            const uint32_t st_at = ring_at + stage * kStageBytes;
+            if (NB == 4 && tiles == 3) products(std::integral_constant<int, NB == 4 ? 3 : 1>{}, st, st_at, key0);
+            else if (NB > 1 && tiles > NB / 2) products(std::integral_constant<int, NB>{}, st, st_at, key0);
+            else products(std::integral_constant<int, NB == 4 ? 2 : 1>{}, st, st_at, key0);
+        }
+        __syncwarp();   // every lane has read the stage
+
+        if (p.step + 1 == p.steps || u + 1 == hi) {
+            // the item's run in this CTA ends: join the four warps through their free stages
+            const bool starts = first_step == 0, ends = p.step + 1 == p.steps;
+            const bool whole = starts && ends;
+            const bool direct = whole && p.b >= 0 && J.batch.prefix_len == 0;
+            const int64_t slot = whole ? (p.b < 0 ? slot_prefix(A, p.h, p.tile) : slot_own(A, p.b, p.h, p.tile))
+                                       : 2 * int64_t(blockIdx.x) + (starts ? 1 : 0);
+            float *part = A.parts + slot * part_floats(RT, D);
+            const int rows = p.b < 0 ? B * A.R : A.R;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {     // 8 rows at a time
+                if (n > 0 && tiles <= n) break;
+                float *mine = reinterpret_cast<float *>(st);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * (lane & 3) + e;
+                    float sum = l[n][e];
+                    sum += __shfl_xor_sync(~0u, sum, 4);
+                    sum += __shfl_xor_sync(~0u, sum, 8);
+                    sum += __shfl_xor_sync(~0u, sum, 16);
+                    if (lane < 4) {
+                        const bool none = (blind >> (2 * n + e)) & 1;
+                        stats[(warp * RT + n * 8 + r) * 2] = none ? -INFINITY : m[n][e];
+                        stats[(warp * RT + n * 8 + r) * 2 + 1] = none ? 0.0f : sum;
+                    }
+#pragma unroll
+                    for (int pg = 0; pg < P; ++pg) {
+                        float zs = z[pg][n][e];
+                        zs += __shfl_xor_sync(~0u, zs, 4);
+                        zs += __shfl_xor_sync(~0u, zs, 8);
+                        zs += __shfl_xor_sync(~0u, zs, 16);
+                        // codes' units: 2^24 and 2^20, over inv = 2^(22 - bound)
+                        const float f0 = power2(2 + bound[pg]), f1 = power2(bound[pg] - 2);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int at = pg * 64 + half * 32 + 4 * (lane >> 2);
+                            *reinterpret_cast<float4 *>(mine + r * D + (at ^ ((lane & 3) << 3))) =
+                                make_float4(fmaf(o[pg][0][n][2 * half + e], f0, zs), fmaf(o[pg][1][n][2 * half + e], f1, zs),
+                                            fmaf(o[pg][2][n][2 * half + e], f0, zs), fmaf(o[pg][3][n][2 * half + e], f1, zs));
+                        }
+                    }
+                }
+                __syncthreads();
+                constexpr int LR = D / 4, RW = 32 / LR;   // lanes of a row, rows of a warp pass
+                const float *all = reinterpret_cast<const float *>(smem + stage * kStageBytes);
+                for (int r = warp * RW + lane / LR; r < 8; r += kWarps * RW) {
+                    const int row = p.tile * RT + n * 8 + r;
+                    if (row >= rows) break;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * RT + n * 8 + r) * 2]);
+                    const float base = base_of(top);
+                    const int c = (lane % LR) * 4, cs = c ^ (((r >> 1) & 3) << 3);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float2 ml = *reinterpret_cast<const float2 *>(stats + (w * RT + n * 8 + r) * 2);
+                        float4 x = *reinterpret_cast<const float4 *>(
+                            all + w * kStages * (kStageBytes / 4) + r * D + cs);
+                        // as add_part, without a branch that the next warp's loads would wait for
+                        const bool none = ml.x == -INFINITY && ml.y == 0.0f;
+                        x.x = none ? 0.0f : x.x; x.y = none ? 0.0f : x.y;
+                        x.z = none ? 0.0f : x.z; x.w = none ? 0.0f : x.w;
+                        const float f = ex2(ml.x - base);
+                        v.x += f * x.x; v.y += f * x.y; v.z += f * x.z; v.w += f * x.w;
+                        sum += f * ml.y;
+                    }
+                    if (direct) {
+                        const int t = token_of(A, row), gq = row - t * G;
+                        const int64_t at = (int64_t(p.b) * J.batch.T + t) * J.q_heads + int64_t(p.h) * G + gq;
+                        const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+                        store_out<T>(J, at * D + c, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                        if (J.lse && lane % LR == 0) J.lse[at] = lse_of(top, sum);
+                    } else {
+                        *reinterpret_cast<float4 *>(part + (n * 8 + r) * D + c) = v;
+                        if (lane % LR == 0)
+                            *reinterpret_cast<float2 *>(part + RT * D + (n * 8 + r) * 2) = make_float2(top, sum);
+                    }
+                }
+                __syncthreads();
+            }
+            if (!direct && J.batch.prefix_len == 0) join_last<T, D, RT>(A, S, p, rows, W, count, scratch);
+            fresh = true;
+        }
+        load_next(stage);
+        if (++stage == kStages) stage = 0;
+        ++p.step;
+        ++u;
+    }
+    tc::cp_async_wait<0>();
+}
+
+// Dynamic shared memory of a CTA: rings, query tiles, their operands and row data, warps'
+// (m, l), the batch.
+size_t smem_of(const Args &A) {
+    const int D = A.J.cache.head_dim, P = D / kGroup, stage = KW * (D + 8 * P);
+    return size_t(kWarps) * kStages * stage + size_t(kStages + 1) * A.RT * D * 2 + size_t(A.RT / 8) * P * 1024 +
+           A.RT * 4 * (1 + P) + kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
+}
+
+Args layout(const trit_attn_job &J) { return layout_of(J, kStep, smem_of, false); }
+
+// The job as the shared layout knows it: a cache of codes, strides in vectors.
+trit_attn_job plain_of(const trit_attn4_job &J) {
+    trit_attn_job p = {};
+    p.cache.k = J.cache.k;
+    p.cache.v = J.cache.v;
+    p.cache.page_stride = J.cache.page_stride;
+    p.cache.head_stride = J.cache.head_stride;
+    p.cache.slot_stride = J.cache.slot_stride;
+    p.cache.pages = J.cache.pages;
+    p.cache.heads = J.cache.heads;
+    p.cache.page_size = J.cache.page_size;
+    p.cache.head_dim = J.cache.head_dim;
+    p.cache.dtype = J.dtype;
+    p.batch = J.batch;
+    p.q = J.q;
+    p.out = J.out;
+    p.lse = J.lse;
+    p.q_stride = J.q_stride;
+    p.scale = J.scale;
+    p.q_heads = J.q_heads;
+    p.out_dtype = J.out_dtype;
+    return p;
+}
+
+template <typename T, int D, int NB>
+cudaError_t launch(const Args4 &A4, cudaStream_t s) {
+    const Args &A = A4.A;
+    const auto kernel = attn4_kernel<T, D, NB>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);
+    if (e == cudaSuccess) e = launch_pdl(kernel, dim3(unsigned(A.grid)), dim3(kThreads), smem_of(A), s, A4);
+    if (e != cudaSuccess || A.J.batch.prefix_len == 0) return e;
+    const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
+    if (joins <= 2 * kSms) return launch_pdl(join_kernel<T, D, 4>, dim3(unsigned(joins)), dim3(4 * D), 0, s, A);
+    return launch_pdl(join_kernel<T, D, 1>, dim3(unsigned(joins)), dim3(D), 0, s, A);
+}
+
+template <typename T>
+cudaError_t launch_t(const Args4 &A4, cudaStream_t s) {
+    const int RT = A4.A.RT;
+    if (A4.A.J.cache.head_dim == 128)
+        return RT == 8 ? launch<T, 128, 1>(A4, s) : RT == 16 ? launch<T, 128, 2>(A4, s) : launch<T, 128, 4>(A4, s);
+    return RT == 8 ? launch<T, 64, 1>(A4, s) : RT == 16 ? launch<T, 64, 2>(A4, s) : launch<T, 64, 4>(A4, s);
+}
+
+}  // namespace
+}  // namespace attn
+
+int64_t attn4_workspace_bytes(const trit_attn4_job &J) {
+    const attn::Args A = attn::layout(attn::plain_of(J));
+    return attn::head_bytes(A) + attn::part_bytes(A);
+}
+
+cudaError_t launch_attn_paged4(const trit_attn4_job &J, uint32_t *err, cudaStream_t s) {
+    attn::Args4 A4;
+    attn::Args &A = A4.A;
+    A = attn::layout(attn::plain_of(J));
+    A.err = err;
+    A4.k_scale = static_cast<const uint8_t *>(J.cache.k_scale);
+    A4.v_scale = static_cast<const uint8_t *>(J.cache.v_scale);
+    A4.scale2 = J.scale * 1.4426950408889634f;
+    uint8_t *ws = static_cast<uint8_t *>(J.workspace);
+    A.count = reinterpret_cast<uint32_t *>(ws);
+    A.cum = reinterpret_cast<int32_t *>(ws + attn::kCountBytes);
+    A.parts = reinterpret_cast<float *>(ws + attn::head_bytes(A));
+    return J.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A4, s) : attn::launch_t<__half>(A4, s);
+}
+
+}  // namespace trit

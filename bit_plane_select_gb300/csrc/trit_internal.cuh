@@ -476,6 +476,14 @@ int64_t attn_workspace_bytes(const trit_attn_job &J);
 cudaError_t launch_attn_paged(const trit_attn_job &J, uint32_t *err, cudaStream_t s);
 cudaError_t launch_draft_verify(const trit_verify_job &J, uint32_t *err, cudaStream_t s);
 
+// Prompts, the cache held in 4 bits, and scoring.
+cudaError_t launch_kv4_append(const trit_kv4_append_job &J, uint32_t *err, cudaStream_t s);
+cudaError_t launch_kv4_read(const trit_kv4_read_job &J, uint32_t *err, cudaStream_t s);
+int64_t attn4_workspace_bytes(const trit_attn4_job &J);
+cudaError_t launch_attn_paged4(const trit_attn4_job &J, uint32_t *err, cudaStream_t s);
+cudaError_t launch_attn_prompt(const trit_prompt_job &J, uint32_t *err, cudaStream_t s);
+cudaError_t launch_logprobs(const trit_logprob_job &J, uint32_t *err, cudaStream_t s);
+
 int device_sm_count();
 
 // Shared by the extern "C" files: the device check (TRIT_OK on sm_103) and the

@@ -84,6 +84,22 @@ __device__ __forceinline__ void store_row(T *p, const float (&y)[W]) {
     else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
+// The sequence that packed row `row` may belong to: the last b < B with starts[b] <= row, or -1.
+// 32 starts at a time; a whole warp asks for one row.  (Starts that fall give some b
+// in range: the caller checks the row against that sequence's own starts.)
+__device__ __forceinline__ int sequence_of(const int32_t *starts, int B, int64_t row, int lane) {
+    int lo = 0, n = B;
+    for (;;) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const uint32_t before = __ballot_sync(~0u, at < n && starts[lo + (at < n ? at : 0)] <= row);
+        if (!before) return -1;
+        const int k = 31 - __clz(int(before));
+        lo += k * step;
+        n = n - k * step < step ? n - k * step : step;
+        if (step == 1) return lo;
+    }
+}
+
 // Launches kernel with programmatic stream serialisation: its CTAs may start
 // while the preceding grid drains; the kernel waits (griddepcontrol.wait)
 // before it touches memory that grid may write or read.

@@ -728,6 +728,194 @@ typedef struct trit_verify_job {
 TRIT_API trit_status trit_draft_verify(const trit_verify_job *job, uint32_t *err_flag,
                                        trit_stream_t stream);
 
+/*
+ * ---- a cache held in 4 bits ------------------------------------------------------
+ * A vector of D columns (a key's or a value's, of one head) is D/2 bytes of codes,
+ * columns 2i and 2i + 1 in the low and the high four bits of byte i, and D/64 pairs
+ * (s, z) of fp16, one per TRIT_KV4_GROUP = 64 columns: a column of code c stands for
+ *     s c + z.
+ * Of a group's 64 fp32 values x, clamped to +-65504,
+ *     z = fp16(min x),  s = fp16((max x - min x) / 15),
+ *     c = (x - z) (1/s) to the nearest whole number in 0..15, ties to even (0 where s is 0),
+ * each operation rounded to fp32, s and z once more to fp16.  A group that holds a
+ * NaN or an infinity stands for NaN throughout (s = 0, z = NaN): what it lost shows.
+ * 4.5 bits a column: 144 bytes a key and head for D = 128 instead of 512.
+ */
+#define TRIT_KV4_GROUP 64
+
+/* One layer's paged cache.  Vector (page, head, slot) is vector page * page_stride +
+ * head * head_stride + slot * slot_stride of all four arrays, strides in vectors:
+ * its codes begin D/2 times that many bytes into k or v, its pairs D/16 times that many
+ * into k_scale or v_scale.  Pointers 16-byte aligned. */
+typedef struct trit_kv4_cache {
+    uint8_t *k, *v;
+    void *k_scale, *v_scale;
+    int64_t page_stride, head_stride, slot_stride;
+    int32_t pages, heads, page_size;
+    int32_t head_dim;            /* D: 64 or 128 */
+    int64_t reserved;            /* must be 0 */
+} trit_kv4_cache;
+
+/*
+ * trit_kv4_append -- as trit_kv_append, into a 4-bit cache: norm and rotation of q
+ * and k in fp32 (a rotation rounds both products and their sum, so that a key's codes
+ * are fixed by its fp32 values), q rounded once into q_out, the keys and values
+ * quantised from fp32.  Token (b, t) is row b*T + t; with `starts` the rows are packed
+ * instead: token t of sequence b is row starts[b] + t, n = starts[b+1] - starts[b] of
+ * them, at most T, and new_lens must be NULL.  Rows in front of starts[0] and from
+ * starts[B] on are left alone.  Starts that fall, or leave [0, rows], and an n above T set
+ * TRIT_ERR_INDEX; tokens past the T-th are then padding.
+ *   q, k, v   a row every `stride` elements: Hq, heads, heads vectors of D; src_dtype
+ *             TRIT_F32 or `dtype`.  q may be NULL (then q_out too)
+ *   q_out     [rows][Hq][D] of `dtype`, TRIT_BF16 or TRIT_F16
+ *   rows      B*T, or with starts the rows that there are
+ * All else (cos, sin, gains, limits, what is flagged) as for trit_kv_append.
+ */
+typedef struct trit_kv4_append_job {
+    trit_kv4_cache cache;
+    trit_kv_batch batch;
+    const void *q, *k, *v;
+    void *q_out;
+    const int32_t *starts;              /* [B+1], or NULL */
+    const float *cos, *sin;
+    const float *q_gain, *k_gain;       /* [D] fp32, or NULL: no norm */
+    int64_t q_stride, k_stride, v_stride;
+    int64_t rows;
+    int64_t max_pos;
+    float eps;
+    int32_t q_heads, rot, src_dtype, dtype;
+    uint32_t flags;                     /* 0 or TRIT_ROPE_PAIRS */
+} trit_kv4_append_job;
+TRIT_API trit_status trit_kv4_append(const trit_kv4_append_job *job, uint32_t *err_flag,
+                                     trit_stream_t stream);
+
+/*
+ * trit_kv4_read -- the keys and values that the sequences see, as rows: key i of
+ * sequence b's prefix_len + lens[b] (the shared prefix first) goes to row
+ * starts[b] + i of k and v, its value s c + z formed in fp32 and rounded once.  That
+ * is what trit_attn_prompt takes for prompts behind cached tokens.  Rows that no key
+ * goes to are left as they were.  A sequence with room (starts[b+1] - starts[b]) for
+ * fewer keys sets TRIT_ERR_INDEX and gets its first ones, as do starts that fall or leave
+ * [0, rows], a length outside its range, and a page outside the cache (zeros).
+ * new_lens and T of the batch are not used.
+ *   k, v   [rows][heads][D] of `dtype`, TRIT_BF16 or TRIT_F16; 16-byte aligned;
+ *          rows <= 2^27, rows * heads <= 2^31
+ */
+typedef struct trit_kv4_read_job {
+    trit_kv4_cache cache;
+    trit_kv_batch batch;
+    void *k, *v;
+    const int32_t *starts;              /* [B+1] */
+    int64_t rows;
+    int32_t dtype;
+    uint32_t flags;                     /* must be 0 */
+} trit_kv4_read_job;
+TRIT_API trit_status trit_kv4_read(const trit_kv4_read_job *job, uint32_t *err_flag,
+                                   trit_stream_t stream);
+
+/*
+ * trit_attn_paged4 -- trit_attn_paged over a 4-bit cache: the same sums, limits,
+ * flags, layouts and workspace rules.  Codes enter the products as they are
+ * (exactly), q as fp16 after a power of two per row has brought its largest column to
+ * [2^14, 2^15) (exact but for columns below 2^-24 of it, those to within 2^-35 of
+ * it), and the pairs (s, z) are applied to the products' fp32 sums; exp(..) s, which
+ * weighs the codes of a value, is rounded to fp16, up to 2^-11 of each term.
+ *   q      `dtype`, TRIT_BF16 or TRIT_F16
+ *   workspace  trit_attn4_workspace_bytes(job) bytes
+ */
+typedef struct trit_attn4_job {
+    trit_kv4_cache cache;
+    trit_kv_batch batch;
+    const void *q;
+    void *out;
+    float *lse;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t q_stride;
+    float scale;                        /* finite */
+    int32_t q_heads, dtype, out_dtype;
+    uint32_t flags;                     /* must be 0 */
+    int32_t reserved;                   /* must be 0 */
+} trit_attn4_job;
+/* Bytes of the workspace, or -1 where the sizes are not supported. */
+TRIT_API int64_t trit_attn4_workspace_bytes(const trit_attn4_job *job);
+TRIT_API trit_status trit_attn_paged4(const trit_attn4_job *job, uint32_t *err_flag,
+                                      trit_stream_t stream);
+
+/*
+ * ---- whole prompts ---------------------------------------------------------------
+ * trit_attn_prompt -- causal attention of packed prompts.  Sequence b has the nq
+ * query rows q_starts[b] .. q_starts[b+1] - 1 and the nk key rows k_starts[b] ..
+ * k_starts[b+1] - 1; its queries are its last tokens, so that query t sees the keys
+ * 0 .. t + nk - nq (none where that is negative):
+ *     out = sum_j softmax_j(scale * q.k_j) v_j,   lse = ln sum_j exp(scale * q.k_j),
+ * query head h reading key head h / (Hq / heads).  Products, sums and roundings as
+ * for trit_attn_paged.  A row that sees no key gives out = 0 and lse = -inf; rows of
+ * q in no sequence are left as they were in out and lse.  Keys that a row does not
+ * see change nothing of it, whatever they hold.  Starts that fall or leave
+ * [0, q_rows] or [0, k_rows] set TRIT_ERR_INDEX; such a sequence's rows are then
+ * not computed.
+ *   q      row r at r * q_stride elements: Hq vectors of D; k, v: `heads` vectors
+ *          at r * k_stride and r * v_stride.  `dtype`, TRIT_BF16 or TRIT_F16; 16-byte
+ *          aligned, strides multiples of 8 and at least a row.  k and v may be NULL
+ *          when k_rows is 0
+ *   out    [q_rows][Hq][D], out_dtype TRIT_F32 or `dtype`; 16-byte aligned
+ *   lse    [q_rows][Hq] fp32, or NULL
+ *   q_starts, k_starts   [B+1] int32; k_starts may be NULL: q_starts
+ * D 64 or 128, B <= TRIT_MAX_SEQUENCES, rows <= 2^27, q_rows * Hq <= 2^31.  Asynchronous on
+ * `stream`; no workspace.
+ */
+typedef struct trit_prompt_job {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    const int32_t *q_starts, *k_starts;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t q_rows, k_rows;
+    int32_t B, q_heads, heads, head_dim;
+    int32_t dtype, out_dtype;
+    float scale;                        /* finite, > 0 */
+    uint32_t flags;                     /* must be 0 */
+} trit_prompt_job;
+TRIT_API trit_status trit_attn_prompt(const trit_prompt_job *job, uint32_t *err_flag,
+                                      trit_stream_t stream);
+
+/*
+ * trit_logprobs -- of every row of logits x over V tokens, with m = max x and
+ * l = sum_i exp(x_i - m):
+ *     logprob      = x[tokens[r]] - m - ln l   (0 where tokens[r] is -1: padding)
+ *     entropy      = ln l - (sum_i exp(x_i - m) (x_i - m)) / l
+ *     top_tokens   the top_n tokens of the largest x, the lowest first where x ties
+ *     top_logprobs their x - m - ln l
+ * in fp32.  A logit of -inf is a token that cannot come: it adds nothing to either
+ * sum.  Where fewer than top_n tokens can come the rest of top_tokens is -1 and of
+ * top_logprobs -inf.  A row of which none can come gives logprob -inf (0 for
+ * padding) and entropy 0, with TRIT_ERR_EMPTY; a row that holds a NaN or +inf gives NaN in
+ * all of its fp32 results (0 for padding's logprob) and -1 in top_tokens.
+ * A token outside [-1, V) sets TRIT_ERR_INDEX and gives logprob -inf.
+ *   logits   row r at r * stride elements; dtype TRIT_F32, TRIT_BF16 or TRIT_F16,
+ *            aligned for one element
+ *   tokens   [rows] int32, or NULL with logprob NULL
+ *   logprob, entropy [rows] fp32, each may be NULL
+ *   top_tokens [rows][top_n] int32, top_logprobs [rows][top_n] fp32; both NULL and top_n = 0, or neither
+ * top_n <= TRIT_MAX_TOP, V < 2^31, rows <= 2^24.  Asynchronous on `stream`; no workspace.
+ */
+#define TRIT_MAX_TOP 64
+typedef struct trit_logprob_job {
+    const void *logits;
+    const int32_t *tokens;
+    float *logprob, *entropy;
+    int32_t *top_tokens;
+    float *top_logprobs;
+    int64_t stride;
+    int64_t rows, V;
+    int32_t top_n, dtype;
+    uint32_t flags;                     /* must be 0 */
+    int32_t reserved;                   /* must be 0 */
+} trit_logprob_job;
+TRIT_API trit_status trit_logprobs(const trit_logprob_job *job, uint32_t *err_flag,
+                                   trit_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
