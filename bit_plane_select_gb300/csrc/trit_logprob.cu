@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 1; e < E; ++e) cm = max_nan(cm, v[e]);
         if (!(cm <= a.m)) {
-            a = moved(a, cm);
+            a = moved(a, max_nan(a.m, cm));      // once NaN, always
             top_chunk = c;
         }
         if (a.m == -INFINITY) return;
