@@ -225,7 +225,8 @@ def prepare(case, seed):
             total = sum(_lens(case))
             s["k_out"], s["v_out"] = (torch.empty((total, hkv, d), dtype=dt, device=dev) for _ in range(2))
             rope = trit.Rope(s["cos"], s["sin"], pairs=case["pairs"], q_gain=s["q_gain"], eps=1e-5)
-            s["job"] = trit.Append4Job(cache, batch, rope, s["q"], s["k"], s["v"], s["q_out"], starts=s["starts"])
+            q_out = s["q_out"] if case["packed"] else s["q_out"].view(b, t, hq, d)
+            s["job"] = trit.Append4Job(cache, batch, rope, s["q"], s["k"], s["v"], q_out, starts=s["starts"])
             s["read"] = trit.Read4Job(cache, batch, s["k_out"], s["v_out"], s["k_starts"])
     else:
         s["q"] = rand(b, t, hq, d).mul_(1.5).to(dt)
