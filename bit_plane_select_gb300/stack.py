@@ -287,15 +287,24 @@ class ServedStack:
     prepared lists of one KvBatch, so the prefix's prompt and the decode steps
     are two plans over the same caches.
 
+    With cache_bits=4 the caches hold 4 bits (Kv4Cache) and 2. and 3. are
+    trit_kv4_append and trit_attn_paged4; whole prompts of different lengths then go in
+    as packed rows (see `prompt_plan`): trit_kv4_append, trit_kv4_read and trit_attn_prompt,
+    so that prompts and single tokens attend to the same cached values.
+
     weights: per layer, name -> (int8 [N, K] tensor, w_scale) for q, k, v, o, gate,
     up, down, plus "attn_gain" and "mlp_gain" (fp32 [K] norm gains).  rope: a
-    Rope; pages and page_size: of every layer's cache."""
+    Rope; pages and page_size: of every layer's cache; dtype: of the queries and of
+    16-bit keys and values."""
 
     NAMES = LayerChain.NAMES
 
     def __init__(self, weights, head_dim: int, rope, pages: int, page_size: int,
-                 dtype=torch.bfloat16, eps: float = 1e-5, device="cuda"):
-        from . import KvCache
+                 dtype=torch.bfloat16, eps: float = 1e-5, device="cuda", cache_bits: int = 16):
+        from . import Kv4Cache, KvCache
+        if cache_bits not in (4, 16):
+            raise ValueError("cache_bits must be 4 or 16")
+        self.cache_bits, self.dtype = cache_bits, dtype
         self.device, self.head_dim, self.rope, self.eps = torch.device(device), head_dim, rope, float(eps)
         self.layers = []
         sizes = self._sizes(weights, head_dim)
@@ -307,10 +316,13 @@ class ServedStack:
                 if int(err.item()) != 0:
                     raise ValueError(f"{name}: non-ternary weights")
                 P[name], S[name] = planes, float(ws)
-            cache = [torch.zeros((pages, heads["k"], page_size, head_dim), dtype=dtype, device=self.device)
-                     for _ in range(2)]
+            if cache_bits == 4:
+                cache = Kv4Cache.empty(pages, heads["k"], page_size, head_dim, self.device)
+            else:
+                cache = KvCache(*(torch.zeros((pages, heads["k"], page_size, head_dim), dtype=dtype, device=self.device)
+                                  for _ in range(2)))
             gains = [lw[g].to(device=self.device, dtype=torch.float32) for g in ("attn_gain", "mlp_gain")]
-            self.layers.append({"P": P, "S": S, "K": K, "F": F, "heads": heads, "cache": KvCache(*cache),
+            self.layers.append({"P": P, "S": S, "K": K, "F": F, "heads": heads, "cache": cache,
                                 "attn_gain": gains[0], "mlp_gain": gains[1]})
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
 
@@ -335,40 +347,74 @@ class ServedStack:
 
     def plan(self, batch):
         """Buffers and prepared calls for the T new tokens of every sequence of `batch`."""
-        from . import AppendJob, AttnJob
-        M, D, dev = batch.B * batch.T, self.head_dim, self.device
-
-        def buf(*shape, dtype=torch.float32):
-            return torch.empty(shape, dtype=dtype, device=dev)
+        from . import Append4Job, AppendJob, Attn4Job, AttnJob, trit_attn_paged, trit_attn_paged4, trit_kv4_append, trit_kv_append
+        four = self.cache_bits == 4
         plan = []
         for L in self.layers:
-            K, F, hq, hk, P, S = L["K"], L["F"], L["heads"]["q"], L["heads"]["k"], L["P"], L["S"]
-            B = {"x_i8": buf(M, k_pad(K), dtype=torch.int8), "s": buf(M), "a_i8": buf(M, k_pad(hq * D), dtype=torch.int8),
-                 "sa": buf(M), "h_i8": buf(M, k_pad(F), dtype=torch.int8), "sh": buf(M),
-                 "q": buf(M, hq * D), "k": buf(M, hk * D), "v": buf(M, hk * D), "o": buf(M, K), "down": buf(M, K),
-                 "gate": buf(M, F, dtype=torch.int32), "up": buf(M, F, dtype=torch.int32),
-                 "q_rot": buf(batch.B, batch.T, hq, D, dtype=L["cache"].k.dtype), "attn": buf(batch.B, batch.T, hq, D)}
-            B["qkv_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, None, B[n]) for n in "qkv"])
-            B["o_list"] = ProjList([(P["o"], S["o"], B["a_i8"], B["sa"], hq * D, None, B["o"])])
-            B["gu_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, B[n], None) for n in ("gate", "up")])
-            B["down_list"] = ProjList([(P["down"], S["down"], B["h_i8"], B["sh"], F, None, B["down"])])
-            B["append"] = AppendJob(L["cache"], batch, self.rope, B["q"], B["k"], B["v"], B["q_rot"])
-            B["attend"] = AttnJob(L["cache"], batch, B["q_rot"], B["attn"])
+            hq, D = L["heads"]["q"], self.head_dim
+            B = self._buffers(L, batch.B * batch.T, (batch.B, batch.T, hq, D))
+            B["append"] = (Append4Job if four else AppendJob)(L["cache"], batch, self.rope, B["q"], B["k"], B["v"], B["q_rot"])
+            B["attend"] = (Attn4Job if four else AttnJob)(L["cache"], batch, B["q_rot"], B["attn"])
+            B["calls"] = [(trit_kv4_append if four else trit_kv_append, B["append"]),
+                          (trit_attn_paged4 if four else trit_attn_paged, B["attend"])]
             plan.append(B)
         return plan
 
+    def prompt_plan(self, batch, rows: int, starts, keys: int, key_starts):
+        """Buffers and prepared calls for whole prompts as packed rows (4-bit caches): of x's
+        `rows` rows, sequence b's new tokens are starts[b] .. starts[b+1] - 1 (starts [B + 1]
+        int32; at most batch.T each), and its prefix_len + lens[b] keys, the new ones
+        last, take key_starts[b] .. key_starts[b+1] - 1 of `keys` (key_starts
+        [B + 1] int32).  Both are read when a step runs, as the batch's tables are."""
+        from . import Append4Job, PromptJob, Read4Job, trit_attn_prompt, trit_kv4_append, trit_kv4_read
+        if self.cache_bits != 4:
+            raise ValueError("packed prompts need caches of 4 bits")
+        plan, packed = [], {}
+        for L in self.layers:
+            hq, hk, D = L["heads"]["q"], L["heads"]["k"], self.head_dim
+            B = self._buffers(L, rows, (rows, hq, D))
+            for name in ("q_rot", "attn"):          # rows of no sequence stay 0
+                B[name].zero_()
+            if hk not in packed:                    # the layers take turns
+                packed[hk] = [torch.zeros((keys, hk, D), dtype=self.dtype, device=self.device) for _ in range(2)]
+            k, v = packed[hk]
+            B["append"] = Append4Job(L["cache"], batch, self.rope, B["q"], B["k"], B["v"], B["q_rot"], starts=starts)
+            B["read"] = Read4Job(L["cache"], batch, k, v, key_starts)
+            B["attend"] = PromptJob(B["q_rot"], k, v, B["attn"], starts, key_starts)
+            B["calls"] = [(trit_kv4_append, B["append"]), (trit_kv4_read, B["read"]), (trit_attn_prompt, B["attend"])]
+            plan.append(B)
+        return plan
+
+    def _buffers(self, L, M: int, q_shape):
+        """A layer's buffers and products for M rows."""
+        D, dev = self.head_dim, self.device
+
+        def buf(*shape, dtype=torch.float32):
+            return torch.empty(shape, dtype=dtype, device=dev)
+        K, F, hq, hk, P, S = L["K"], L["F"], L["heads"]["q"], L["heads"]["k"], L["P"], L["S"]
+        B = {"x_i8": buf(M, k_pad(K), dtype=torch.int8), "s": buf(M), "a_i8": buf(M, k_pad(hq * D), dtype=torch.int8),
+             "sa": buf(M), "h_i8": buf(M, k_pad(F), dtype=torch.int8), "sh": buf(M),
+             "q": buf(M, hq * D), "k": buf(M, hk * D), "v": buf(M, hk * D), "o": buf(M, K), "down": buf(M, K),
+             "gate": buf(M, F, dtype=torch.int32), "up": buf(M, F, dtype=torch.int32),
+             "q_rot": buf(*q_shape, dtype=self.dtype), "attn": buf(*q_shape)}
+        B["qkv_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, None, B[n]) for n in "qkv"])
+        B["o_list"] = ProjList([(P["o"], S["o"], B["a_i8"], B["sa"], hq * D, None, B["o"])])
+        B["gu_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, B[n], None) for n in ("gate", "up")])
+        B["down_list"] = ProjList([(P["down"], S["down"], B["h_i8"], B["sh"], F, None, B["down"])])
+        return B
+
     def step(self, plan, x, stream=None):
-        """x [B*T, K] fp32, the new tokens' rows, through every layer in place."""
-        from . import (trit_attn_paged, trit_intmlp_quant, trit_kv_append, trit_quant_act,
-                       trit_quant_act_folded)
+        """x [rows, K] fp32, the new tokens' rows (B*T of them, or a prompt plan's), through every
+        layer in place."""
+        from . import trit_intmlp_quant, trit_quant_act, trit_quant_act_folded
         if len(plan) != len(self.layers) or tuple(x.shape) != tuple(plan[0]["o"].shape):
             raise ValueError("x must be [B*T, K] of the plan's batch")
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
             for L, B in zip(self.layers, plan):
                 trit_quant_act_folded(x, L["attn_gain"], self.eps, B["x_i8"], B["s"], self.err)
                 trit_gemm_many(B["qkv_list"], self.err)
-                trit_kv_append(B["append"], self.err)
-                trit_attn_paged(B["attend"], self.err)
+                for call, job in B["calls"]:
+                    call(job, self.err)
                 trit_quant_act(B["attn"].view(x.shape[0], -1), B["a_i8"], B["sa"], self.err)
                 trit_gemm_many(B["o_list"], self.err)
                 x += B["o"]
