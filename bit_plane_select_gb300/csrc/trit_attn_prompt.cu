@@ -7,11 +7,13 @@
 // fp32 in tensor memory) is overwritten in place by P (16-bit, the operand of the second
 // product), O accumulates beside it and is rescaled only when a row's maximum grew by more
 // than 2^8 since its base was fixed.  These steps wait for one another, so an SM runs two of them
-// at a time, one's products under the other's softmax: two CTAs, a tile each (kSolo), which
+// at a time, one's products under the other's softmax: two CTAs, a tile each, which
 // also covers the beginning and end of a tile by the other's work; or, where there are
 // fewer tiles than SMs, one CTA whose two streams take a tile's blocks of keys by turns
 // (TURNS) and are joined at the end.  (Measured, us: one prompt of 16384 tokens, 20 query heads over 5 of
-// 128: 876; two tiles of one CTA sharing the loads of K and V 965.  700 tokens: 12.4 by turns, 13.9 solo.)
+// 128: 849; two tiles of one CTA sharing the loads of K and V 965.  700 tokens: 12.4 by turns, 13.9 a
+// tile per CTA.)  P goes to the products in halves of 64 keys (in quarters 855 to 890 us, whole 928):
+// every store to tensor memory is waited for, and takes its turn behind the products under way.
 //
 // A row is a token and one of the G query heads that share a key head: 128 / G tokens'
 // rows fill a tile, so one K and V tile serves them all, a prompt's diagonal cuts off little
@@ -196,12 +198,12 @@ __global__ void __launch_bounds__(Shape<D, TURNS>::kThreads, TURNS ? 1 : 2)
     uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kTile);
     uint64_t *empty = full + kRing;
     uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
-    uint64_t *p_full = s_full + 2;       // [stream][quarter]: P of 32 keys each is
-    uint64_t *o_full = p_full + 8;       // stream's O is finished
+    uint64_t *p_full = s_full + 2;       // [stream][half]: P of 64 keys each is
+    uint64_t *o_full = p_full + 4;       // stream's O is finished
     uint64_t *pv_done = o_full + 2;      // stream's product into O has completed
     uint64_t *q_full = pv_done + 2;
     uint64_t *tail = q_full + 1;         // the copies of a V block that is looked through
-    constexpr int kBars = 2 * kRing + 16;
+    constexpr int kBars = 2 * kRing + 12;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail + 1);
     uint32_t *timed_out = tmem_slot + 1;
     uint32_t *odd = tmem_slot + 2;       // V held an infinity or NaN in a block that is masked
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(Shape<D, TURNS>::kThreads, TURNS ? 1 : 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == kMmaWarp && lane < kBars) {       // a barrier per lane, in the order above
         const int i = lane;
-        const bool by_warps = i >= 2 * kRing + 2 && i < 2 * kRing + 10;      // p_full
+        const bool by_warps = i >= 2 * kRing + 2 && i < 2 * kRing + 6;       // p_full
         mbar_init(full + i, by_warps ? 4u : 1u);
         if (i == 0) *timed_out = *odd = 0;
         fence_barrier_init();
@@ -347,13 +349,13 @@ __global__ void __launch_bounds__(Shape<D, TURNS>::kThreads, TURNS ? 1 : 2)
             ok = tile_there(at);
             const uint32_t b = rv + st * (kTile >> 4);
 #pragma unroll
-            for (int part4 = 0; part4 < 4; ++part4) {
-                ok = ok && warp_wait(&p_full[4 * s + part4], i & 1, timed_out);
+            for (int part2 = 0; part2 < 2; ++part2) {
+                ok = ok && warp_wait(&p_full[2 * s + part2], i & 1, timed_out);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
-                    for (int kk = 2 * part4; kk < 2 * part4 + 2; ++kk)
+                    for (int kk = 4 * part2; kk < 4 * part2 + 4; ++kk)
                         mma_ts(o, sp + kk * 8, b + kk * (2048 >> 4), idesc_o<T, D>(), i > 0 || kk > 0);
                 }
                 __syncwarp();
@@ -437,21 +439,22 @@ __global__ void __launch_bounds__(Shape<D, TURNS>::kThreads, TURNS ? 1 : 2)
             const uint64_t k2 = pack2(scale2, scale2), b2 = pack2(-base, -base);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[16];
+            for (int q = 0; q < 2; ++q) {
+                uint32_t w[32];
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const int at = q * 32 + 2 * c;
+                for (int c = 0; c < 32; ++c) {
+                    const int at = q * 64 + 2 * c;
                     const float2 x = unpack2(fma2(pack2(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), k2, b2));
                     const float e0 = ex2(x.x), e1 = ex2(x.y);
                     sum[c & 1] = add2(sum[c & 1], pack2(e0, e1));
                     w[c] = pack16<T>(e0, e1);
                 }
-                tmem_st16(sa + q * 16, w);
+                tmem_st16(sa + q * 32, w);
+                tmem_st16(sa + q * 32 + 16, w + 16);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[4 * s + q]);
+                if (lane == 0) mbar_arrive(&p_full[2 * s + q]);
             }
             const float2 x = unpack2(add2(sum[0], sum[1]));
             l += x.x + x.y;

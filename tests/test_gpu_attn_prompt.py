@@ -83,6 +83,12 @@ CASES = [
     ([1] * 90, None, 4, 1, 64, BF),
     ([(i * 37) % 200 for i in range(75)], None, 4, 2, 64, HF),
     ([1500], None, 6, 2, 128, HF),
+    # more tiles than SMs: two CTAs an SM
+    ([1500], None, 20, 5, 128, BF),
+    ([700, 1, 0, 333], [1100, 900, 7, 333], 24, 8, 64, HF),        # a few an SM: by length
+    ([300 + i for i in range(33)], None, 8, 4, 64, BF),            # many sequences: in their order
+    ([(i * 53) % 260 for i in range(70)], [(i * 53) % 260 + i for i in range(70)], 20, 5, 128, HF),
+    ([3, 200], [2, 90], 600, 100, 64, BF),                         # and fewer keys than queries
     ([1030, 517], [2050, 517], 4, 1, 64, BF),
 ]
 
