@@ -34,6 +34,7 @@ constexpr int kStages = 3;
 constexpr int KW = 32;                     // keys of a warp's stage
 constexpr int kStep = KW * kWarps;
 constexpr int kGroup = TRIT_KV4_GROUP;
+constexpr float kLift = 8.0f;              // weights are up to 2^8, so that fp16 holds small ones too
 
 template <int D>
 struct Shape {
@@ -75,6 +76,25 @@ __device__ __forceinline__ uint32_t query_at(int row, int c) {
 __device__ __forceinline__ void operands(const uint32_t (&f)[4], int i, uint32_t (&a)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) a[j] = (i < 2 ? f[j] : f[j] >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+// The same product with nothing before it.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ uint32_t mul16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t half_power2(int e) {       // a pair of 2^e, e in -24..15
+    const uint32_t h = e >= -14 ? uint32_t(e + 15) << 10 : 1u << (e + 24);
+    return h | h << 16;
+}
+__device__ __forceinline__ bool odd16(uint32_t pair) {         // an infinity or NaN among two fp16 values
+    return (pair & 0x7c00u) == 0x7c00u || (pair & 0x7c000000u) == 0x7c000000u;
 }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
 
@@ -214,14 +234,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
     if (lo >= hi) return;
 
     float o[P][4][NB][4];        // columns 64 p + 32 (e / 2) + 4 (lane / 4) + i, row 2 (lane % 4) + e % 2
-    float z[P][NB][2];           // sum of p z over the lane's keys
+    float z[NB][2];              // of lanes 4 pg + t: sum of p z of group pg, row 2 t + e
     float m[NB][2], l[NB][2];
     int lim[NB][2];
     int bound[P];                // exponent field that no s seen so far exceeds
     uint32_t blind = 0;      // the thread's rows that see none of the item's keys
     int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no limit lies below `clear`
     int cq = 0;
-    uint4 held[NB == 1 ? P : 1][2];                        // one tile's queries stay in registers
+    // one tile's queries stay in registers
+    uint4 held[NB == 1 ? P : 1][2];
+    float held_sum[NB == 1 ? P : 1][2], held_fac[2];
 
     // An item's queries as operands: warp n takes tile n.  Lane (g, t) has of row g the
     // columns 64 p + 32 b + 8 t + 0..7; operand i of chunk b is its columns i and i + 4.
@@ -270,65 +292,79 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
         if (t == 0) facs[row] = A4.scale2 * power2(24 - e);
     };
 
-    // The products of one stage with the item's first NM tiles of 8 rows.
-    auto products = [&](auto nm, const uint8_t *st, uint32_t st_at, int key0) {
+    // The products of one stage with the item's first NM tiles of 8 rows.  MASKED: some row does
+    // not see all of its keys.
+    auto products = [&](auto nm, auto masked, uint8_t *st, uint32_t st_at, int key0) {
         constexpr int NM = decltype(nm)::value, KM = KW / 16;
+        constexpr bool MASKED = decltype(masked)::value;
         const int g = lane >> 2, t2 = 2 * (lane & 3);
         float s[KM][NM][4];
         const int arow = ((lane >> 3) & 1) * 8 + (lane & 7), ach = lane >> 4;
 #pragma unroll
         for (int km = 0; km < KM; ++km) {
+            // the pairs of keys g and g + 8
+            uint32_t ks[2][P];
 #pragma unroll
-            for (int n = 0; n < NM; ++n) s[km][n][0] = s[km][n][1] = s[km][n][2] = s[km][n][3] = 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *at = st + Sh::kKsAt + (km * 16 + 8 * i + g) * Sh::SB;
+                if (P == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                    ks[i][0] = v.x;
+                    ks[i][P - 1] = v.y;
+                } else {
+                    ks[i][0] = *reinterpret_cast<const uint32_t *>(at);
+                }
+            }
 #pragma unroll
             for (int pg = 0; pg < P; ++pg) {
                 uint32_t f[4], a[4][4];
                 ldsm4(f, st_at + codes_at<D>(km * 16 + arow, 2 * pg + ach));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) operands(f, i, a[i]);
-                const __half2 *ks = reinterpret_cast<const __half2 *>(st + Sh::kKsAt) + pg;
-                const float2 k0 = __half22float2(ks[(km * 16 + g) * P]), k1 = __half22float2(ks[(km * 16 + 8 + g) * P]);
+                const float2 k0 = unpack16<__half>(ks[0][pg]), k1 = unpack16<__half>(ks[1][pg]);
 #pragma unroll
                 for (int n = 0; n < NM; ++n) {
                     const uint4 q0 = NB == 1 ? held[NB == 1 ? pg : 0][0] : frag[((n * P + pg) * 2) * 32 + lane];
                     const uint4 q1 = NB == 1 ? held[NB == 1 ? pg : 0][1] : frag[((n * P + pg) * 2 + 1) * 32 + lane];
-                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma16816<__half>(acc, a[0], q0.x, q0.y);
+                    float acc[4];
+                    mma16816_first(acc, a[0], q0.x, q0.y);
                     mma16816<__half>(acc, a[1], q0.z, q0.w);
                     mma16816<__half>(acc, a[2], q1.x, q1.y);
                     mma16816<__half>(acc, a[3], q1.z, q1.w);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float qs = qsum[(n * 8 + t2 + e) * P + pg];
-                        s[km][n][e] = fmaf(k0.x, acc[e], fmaf(k0.y, qs, s[km][n][e]));
-                        s[km][n][2 + e] = fmaf(k1.x, acc[2 + e], fmaf(k1.y, qs, s[km][n][2 + e]));
+                        const float qs = NB == 1 ? held_sum[NB == 1 ? pg : 0][e] : qsum[(n * 8 + t2 + e) * P + pg];
+                        const float z0 = k0.y * qs, z1 = k1.y * qs;
+                        s[km][n][e] = fmaf(k0.x, acc[e], pg ? s[km][n][e] + z0 : z0);
+                        s[km][n][2 + e] = fmaf(k1.x, acc[2 + e], pg ? s[km][n][2 + e] + z1 : z1);
                     }
                 }
             }
         }
-        const bool masked = key0 + KW > clear;
         float alpha[NM][2];
         bool moved = false;
 #pragma unroll
         for (int n = 0; n < NM; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float f = facs[n * 8 + t2 + e];
+                const float f = NB == 1 ? held_fac[e] : facs[n * 8 + t2 + e];
                 float mx = -INFINITY;
 #pragma unroll
-                for (int km = 0; km < KM; ++km)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float &v = s[km][n][2 * i + e];
-                        v *= f;
-                        if (masked && key0 + km * 16 + i * 8 + g >= lim[n][e]) v = -INFINITY;
-                        mx = fmaxf(mx, v);
+                for (int km = 0; km < KM; ++km) {
+                    float &v0 = s[km][n][e], &v1 = s[km][n][2 + e];
+                    v0 *= f;
+                    v1 *= f;
+                    if (MASKED) {
+                        if (key0 + km * 16 + g >= lim[n][e]) v0 = -INFINITY;
+                        if (key0 + km * 16 + 8 + g >= lim[n][e]) v1 = -INFINITY;
                     }
+                    mx = max3(mx, v0, v1);
+                }
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                const float top = fmaxf(m[n][e], mx), base = base_of(top);
-                alpha[n][e] = ex2(m[n][e] - base);
+                const float top = fmaxf(m[n][e], mx), base = base_of(top) - kLift;
+                alpha[n][e] = ex2(m[n][e] - base - kLift);
                 moved |= alpha[n][e] != 1.0f;
                 m[n][e] = top;
                 float sum = 0.0f;
@@ -344,52 +380,103 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
             }
         if (__any_sync(~0u, moved)) {
 #pragma unroll
-            for (int pg = 0; pg < P; ++pg)
+            for (int n = 0; n < NM; ++n) {
+                z[n][0] *= alpha[n][0];
+                z[n][1] *= alpha[n][1];
 #pragma unroll
-                for (int n = 0; n < NM; ++n) {
-                    z[pg][n][0] *= alpha[n][0];
-                    z[pg][n][1] *= alpha[n][1];
+                for (int pg = 0; pg < P; ++pg)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= alpha[n][e & 1];
+            }
+        }
+        // the pairs of V: a lane looks at one key's.  In units of a power of two that bounds s in
+        // what the warp has seen.
+        uint32_t inv[P];
+        {
+            uint32_t *own = reinterpret_cast<uint32_t *>(st + Sh::kVsAt + lane * Sh::SB);
+            uint32_t pair[P];
+            bool bad = false;
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg) {
+                pair[pg] = own[pg];
+                bad |= MASKED && odd16(pair[pg]);
+            }
+            if (MASKED) {
+                // A NaN that some row does not see must not meet its P = 0: it goes to the rows that do, one by
+                // one, and out of the stage.
+                uint32_t which = __ballot_sync(~0u, bad);
+                for (uint32_t left = which; left; left &= left - 1) {
+                    const int k = __ffs(int(left)) - 1;
+#pragma unroll
+                    for (int pg = 0; pg < P; ++pg) {
+                        const uint32_t v = __shfl_sync(~0u, pair[pg], k);
+                        if (!odd16(v) || g != pg) continue;
+#pragma unroll
+                        for (int n = 0; n < NM; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (key0 + k < lim[n][e]) z[n][e] += unpack16<__half>(v).x - unpack16<__half>(v).x + unpack16<__half>(v).y;
+                    }
                 }
+                if (which) {
+#pragma unroll
+                    for (int pg = 0; pg < P; ++pg)
+                        if (bad) own[pg] = pair[pg] = odd16(pair[pg]) ? 0u : pair[pg];
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg) {
+                const uint32_t most = __reduce_max_sync(~0u, (pair[pg] >> 10) & 31u);
+                if (int(most) > bound[pg]) {
+                    const int to = int(most) + 1;
+                    const float f = bound[pg] < 0 ? 0.0f : power2(bound[pg] - to);      // (nothing summed up yet: 0)
+                    bound[pg] = to;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int n = 0; n < NM; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= f;
+                }
+                inv[pg] = half_power2(14 - bound[pg]);       // s inv < 1
+            }
         }
         const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;
 #pragma unroll
-        for (int pg = 0; pg < P; ++pg) {
-            const __half2 *vs = reinterpret_cast<const __half2 *>(st + Sh::kVsAt) + pg;
-            // the greatest s of the stage, by its exponent: a lane looks at one key
-            const uint32_t most = __reduce_max_sync(~0u, (*reinterpret_cast<const uint32_t *>(vs + lane * P) >> 10) & 31u);
-            if (int(most) > bound[pg]) {
-                const int to = int(most) + 1;
-                const float f = bound[pg] < 0 ? 0.0f : power2(bound[pg] - to);      // (nothing summed up yet: 0)
-                bound[pg] = to;
+        for (int km = 0; km < KM; ++km) {
+            // the pairs of keys 2t, 2t + 1 and 8 further: s by keys, in units; z as a product's operand whose
+            // row pg is the group's
+            uint32_t sp[P][2], za[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NM; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= f;
-            }
-            const float inv = power2(22 - bound[pg]);       // s inv < 2^8
-#pragma unroll
-            for (int km = 0; km < KM; ++km) {
-                const float2 v0 = __half22float2(vs[(km * 16 + g) * P]), v1 = __half22float2(vs[(km * 16 + 8 + g) * P]);
-                const float s0 = v0.x * inv, s1 = v1.x * inv;
-                uint32_t w[NM][2];
-#pragma unroll
-                for (int n = 0; n < NM; ++n) {
-                    const float(&q)[4] = s[km][n];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // a hidden key's z may be NaN
-                        const bool h0 = masked && key0 + km * 16 + g >= lim[n][e], h1 = masked && key0 + km * 16 + 8 + g >= lim[n][e];
-                        z[pg][n][e] = fmaf(q[e], h0 ? 0.0f : v0.y, fmaf(q[2 + e], h1 ? 0.0f : v1.y, z[pg][n][e]));
-                    }
-                    w[n][0] = transposed8(pack16<__half>(q[0] * s0, q[1] * s0));
-                    w[n][1] = transposed8(pack16<__half>(q[2] * s1, q[3] * s1));
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *at = st + Sh::kVsAt + (km * 16 + 8 * i + t2) * Sh::SB;
+                if (P == 2) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                    sp[0][i] = mul16(prmt(v.x, v.z, 0x5410u), inv[0]);
+                    sp[P - 1][i] = mul16(prmt(v.y, v.w, 0x5410u), inv[P - 1]);
+                    za[2 * i] = prmt(g == 0 ? v.x : v.y, g == 0 ? v.z : v.w, 0x7632u);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                    sp[0][i] = mul16(prmt(v.x, v.y, 0x5410u), inv[0]);
+                    za[2 * i] = prmt(v.x, v.y, 0x7632u);
                 }
+                if (g >= P) za[2 * i] = 0;
+            }
+            uint32_t w[NM][2];
+#pragma unroll
+            for (int n = 0; n < NM; ++n) {
+                w[n][0] = transposed8(pack16<__half>(s[km][n][0], s[km][n][1]));
+                w[n][1] = transposed8(pack16<__half>(s[km][n][2], s[km][n][3]));
+                float zc[4] = {z[n][0], z[n][1], 0.0f, 0.0f};
+                mma16816<__half>(zc, za, w[n][0], w[n][1]);
+                z[n][0] = zc[0];
+                z[n][1] = zc[1];
+            }
+#pragma unroll
+            for (int pg = 0; pg < P; ++pg) {
                 uint32_t f[4];
                 ldsm4t(f, st_at + Sh::kVAt + codes_at<D>(km * 16 + vrow, 2 * pg + vch));
 #pragma unroll
@@ -397,10 +484,16 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                     uint32_t a[4];
                     operands(f, i, a);
 #pragma unroll
-                    for (int n = 0; n < NM; ++n) mma16816<__half>(o[pg][i][n], a, w[n][0], w[n][1]);
+                    for (int n = 0; n < NM; ++n)
+                        mma16816<__half>(o[pg][i][n], a, mul16(w[n][0], sp[pg][0]), mul16(w[n][1], sp[pg][1]));
                 }
             }
         }
+    };
+    auto stage_products = [&](auto masked, uint8_t *st, uint32_t st_at, int key0) {
+        if (NB == 4 && tiles == 3) products(std::integral_constant<int, NB == 4 ? 3 : 1>{}, masked, st, st_at, key0);
+        else if (NB > 1 && tiles > NB / 2) products(std::integral_constant<int, NB>{}, masked, st, st_at, key0);
+        else products(std::integral_constant<int, NB == 4 ? 2 : 1>{}, masked, st, st_at, key0);
     };
 
     int64_t u = lo;
@@ -447,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                 bound[pg] = -1;
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
-                    z[pg][n][0] = z[pg][n][1] = 0.0f;
+                    z[n][0] = z[n][1] = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[pg][i][n][0] = o[pg][i][n][1] = o[pg][i][n][2] = o[pg][i][n][3] = 0.0f;
                 }
@@ -464,6 +557,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                     held[pg][0] = frag[(pg * 2) * 32 + lane];
                     held[pg][1] = frag[(pg * 2 + 1) * 32 + lane];
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    held_fac[e] = facs[2 * (lane & 3) + e];
+#pragma unroll
+                    for (int pg = 0; pg < (NB == 1 ? P : 0); ++pg) held_sum[pg][e] = qsum[(2 * (lane & 3) + e) * P + pg];
+                }
             }
         }
         __syncwarp();
@@ -471,9 +570,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
         uint8_t *st = ring + stage * kStageBytes;
         if (key0 < nkeys) {
             const uint32_t st_at = ring_at + stage * kStageBytes;
-            if (NB == 4 && tiles == 3) products(std::integral_constant<int, NB == 4 ? 3 : 1>{}, st, st_at, key0);
-            else if (NB > 1 && tiles > NB / 2) products(std::integral_constant<int, NB>{}, st, st_at, key0);
-            else products(std::integral_constant<int, NB == 4 ? 2 : 1>{}, st, st_at, key0);
+            if (key0 + KW > clear) stage_products(std::true_type{}, st, st_at, key0);
+            else stage_products(std::false_type{}, st, st_at, key0);
         }
         __syncwarp();   // every lane has read the stage
 
@@ -499,17 +597,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                     sum += __shfl_xor_sync(~0u, sum, 16);
                     if (lane < 4) {
                         const bool none = (blind >> (2 * n + e)) & 1;
-                        stats[(warp * RT + n * 8 + r) * 2] = none ? -INFINITY : m[n][e];
+                        stats[(warp * RT + n * 8 + r) * 2] = none ? -INFINITY : m[n][e] - kLift;
                         stats[(warp * RT + n * 8 + r) * 2 + 1] = none ? 0.0f : sum;
                     }
 #pragma unroll
                     for (int pg = 0; pg < P; ++pg) {
-                        float zs = z[pg][n][e];
-                        zs += __shfl_xor_sync(~0u, zs, 4);
-                        zs += __shfl_xor_sync(~0u, zs, 8);
-                        zs += __shfl_xor_sync(~0u, zs, 16);
-                        // codes' units: 2^24 and 2^20, over inv = 2^(22 - bound)
-                        const float f0 = power2(2 + bound[pg]), f1 = power2(bound[pg] - 2);
+                        const float zs = __shfl_sync(~0u, z[n][e], 4 * pg + (lane & 3));
+                        // codes' units: 2^24 and 2^20, over inv = 2^(14 - bound)
+                        const float f0 = power2(10 + bound[pg]), f1 = power2(6 + bound[pg]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int at = pg * 64 + half * 32 + 4 * (lane >> 2);

@@ -9,9 +9,9 @@
 // The top entries need no second pass over the row.  Order entries by (value, lower
 // index) and, coarser, by (value, lower chunk of 16 bytes).  A thread knows its greatest
 // entry in the coarse order from the running maximum for nothing; the top_n-th of the
-// 64 groups' greatest (eight threads each) is a bound that at least top_n
+// 64 groups' greatest (a few threads each) is a bound that at least top_n
 // entries reach, so an entry below it is none of the answer.  Only the threads that reach it --
-// little more than top_n of 512 -- have their chunks read again, and the few dozen entries
+// little more than top_n of 256 -- have their chunks read again, and the few dozen entries
 // found are ranked by counting.  (Where more than kRoom are found, which takes values
 // that lie by stride, top_n passes find one entry each.)
 //
@@ -23,12 +23,17 @@
 namespace trit {
 namespace {
 
-constexpr int kThreads = 512;
+#ifndef LT
+#define LT 256
+#define LF 4
+#define LC 4
+#endif
+constexpr int kThreads = LT;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 8;      // at least TRIT_MAX_TOP
+constexpr int kGroups = 64;                // at least TRIT_MAX_TOP
 constexpr int kMaxCluster = 8;
 constexpr int kRoom = 2048;                // entries that may reach the bound
-constexpr int kFlight = 4;                 // chunks of a thread in flight
+constexpr int kFlight = LF;                 // chunks of a thread in flight
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kGroups >= TRIT_MAX_TOP, "a bound needs a group for each entry");
 
@@ -45,6 +50,58 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
+
+// Two fp32 lanes in one 64-bit register: one instruction for both.
+__device__ __forceinline__ u64 pack2(float x, float y) {
+    u64 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(u64 v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// The greatest of 16 bytes of logits (NaN if one is), 16-bit ones two at a time.
+template <typename S>
+__device__ __forceinline__ float greatest(uint4 u);
+template <>
+__device__ __forceinline__ float greatest<float>(uint4 u) {
+    float d;
+    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, %2, %3;\n max.NaN.f32 %0, t, %4;\n}"
+        : "=f"(d)
+        : "f"(__uint_as_float(u.x)), "f"(__uint_as_float(u.y)), "f"(__uint_as_float(u.z)), "f"(__uint_as_float(u.w)));
+    return d;
+}
+#define TRIT_GREATEST(S, type)                                                                                       \
+    template <>                                                                                                      \
+    __device__ __forceinline__ float greatest<S>(uint4 u) {                                                          \
+        uint32_t d;                                                                                                  \
+        asm("{\n .reg .b32 s, t;\n max.NaN." type " s, %1, %2;\n max.NaN." type " t, %3, %4;\n max.NaN." type " %0, s, t;\n}" \
+            : "=r"(d)                                                                                                \
+            : "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w));                                                               \
+        const float2 f = unpack16<S>(d);                                                                             \
+        return max_nan(f.x, f.y);                                                                                    \
+    }
+TRIT_GREATEST(__nv_bfloat16, "bf16x2")
+TRIT_GREATEST(__half, "f16x2")
+#undef TRIT_GREATEST
 
 // A float as a whole number of the same order (-0 as +0); -inf and NaN are not asked for.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -122,7 +179,7 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, LC)
     logprob_kernel(const __grid_constant__ trit_logprob_job J, uint32_t *err, int cluster) {
     constexpr int E = Row<S>::E;
     __shared__ u64 keys[kRoom];
@@ -153,30 +210,59 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (token >= 0 && token < J.V) given = to_f32<S>(row.x[token]);
     }
 
-    Sums a = {-INFINITY, 0.0f, 0.0f};
+    float m = -INFINITY;
+    u64 l2[2] = {0, 0}, w2[2] = {0, 0};        // l and w in four parts
     uint32_t top_chunk = 0;
-    auto see = [&](const float (&v)[E], uint32_t c) {
-        float cm = v[0];
+    auto raised = [&](float cm, uint32_t c) {
+        if (!(cm <= m)) {
+            const float to = max_nan(m, cm);      // once NaN, always
+            const float d = fmaxf(m - to, -150.0f), f = ex2(d * kLog2e);
+            const u64 dd = pack2(d, d), ff = pack2(f, f);
 #pragma unroll
-        for (int e = 1; e < E; ++e) cm = max_nan(cm, v[e]);
-        if (!(cm <= a.m)) {
-            a = moved(a, max_nan(a.m, cm));      // once NaN, always
+            for (int k = 0; k < 2; ++k) {
+                w2[k] = mul2(ff, fma2(l2[k], dd, w2[k]));
+                l2[k] = mul2(ff, l2[k]);
+            }
+            m = to;
             top_chunk = c;
         }
-        if (a.m == -INFINITY) return;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float d = fmaxf(v[e] - a.m, -150.0f), x = ex2(d * kLog2e);
-            a.l += x;
-            a.w = fmaf(x, d, a.w);
+        return m != -INFINITY;
+    };
+    auto add = [&](float2 x, int k) {
+        float2 d = unpack2(add2(pack2(x.x, x.y), pack2(-m, -m)));
+        d.x = fmaxf(d.x, -150.0f);            // -inf: e^d is 0, and 0 d must not be NaN
+        d.y = fmaxf(d.y, -150.0f);
+        const u64 dd = pack2(d.x, d.y);
+        const float2 t = unpack2(mul2(dd, pack2(kLog2e, kLog2e)));
+        const u64 e = pack2(ex2(t.x), ex2(t.y));
+        l2[k] = add2(l2[k], e);
+        w2[k] = fma2(e, dd, w2[k]);
+    };
+    auto see_whole = [&](uint4 u, uint32_t c) {
+        if (!raised(greatest<S>(u), c)) return;
+        if constexpr (sizeof(S) == 4) {
+            add(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), 0);
+            add(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), 1);
+        } else {
+            add(unpack16<S>(u.x), 0);
+            add(unpack16<S>(u.y), 1);
+            add(unpack16<S>(u.z), 0);
+            add(unpack16<S>(u.w), 1);
         }
+    };
+    auto see = [&](uint32_t c) {              // a chunk that may reach out of the row
+        float v[E], cm = -INFINITY;
+        row.load(c, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) cm = max_nan(cm, v[e]);
+        if (!raised(cm, c)) return;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) add(make_float2(v[e], v[e + 1]), (e >> 1) & 1);
     };
     uint32_t c = from + tid;
     // the row's first chunk if it is not whole; whole chunks, kFlight at a time; what is left one by one
     if (c < to && !row.is_whole(c)) {
-        float v[E];
-        row.load(c, v);
-        see(v, c);
+        see(c);
         c += kThreads;
     }
     const uint32_t whole = from < to && !row.is_whole(to - 1) ? to - 1 : to;
@@ -185,17 +271,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) u[k] = row.whole(c + k * kThreads);
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-            float v[E];
-            Row<S>::unpack(u[k], v);
-            see(v, c + k * kThreads);
-        }
+        for (int k = 0; k < kFlight; ++k) see_whole(u[k], c + k * kThreads);
     }
-    for (; c < to; c += kThreads) {
-        float v[E];
-        row.load(c, v);
-        see(v, c);
-    }
+    for (; c < to; c += kThreads) see(c);
+    const float2 la = unpack2(add2(l2[0], l2[1])), wa = unpack2(add2(w2[0], w2[1]));
+    Sums a = {m, la.x + la.y, wa.x + wa.y};
 
     const u64 best = N && a.m > -INFINITY ? key_of(a.m, top_chunk) : 0;      // (a NaN row's keys are not used)
     // the sums of the CTA
@@ -208,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (N) {
         u64 g = best;
 #pragma unroll
-        for (int o = 4; o; o >>= 1) {
+        for (int o = kThreads / kGroups / 2; o; o >>= 1) {
             const u64 x = __shfl_xor_sync(~0u, g, o);
             g = x > g ? x : g;
         }
-        if ((lane & 7) == 0) groups[tid >> 3] = g;
+        if (tid % (kThreads / kGroups) == 0) groups[tid / (kThreads / kGroups)] = g;
     }
     __syncthreads();
     a = lane < kWarps ? warp_sums[lane] : Sums{-INFINITY, 0.0f, 0.0f};
