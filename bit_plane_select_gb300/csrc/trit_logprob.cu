@@ -23,17 +23,13 @@
 namespace trit {
 namespace {
 
-#ifndef LT
-#define LT 256
-#define LF 4
-#define LC 4
-#endif
-constexpr int kThreads = LT;
+constexpr int kThreads = 256;
+constexpr int kCtas = 4;                   // an SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = 64;                // at least TRIT_MAX_TOP
 constexpr int kMaxCluster = 8;
 constexpr int kRoom = 2048;                // entries that may reach the bound
-constexpr int kFlight = LF;                 // chunks of a thread in flight
+constexpr int kFlight = 4;                 // chunks of a thread in flight
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kGroups >= TRIT_MAX_TOP, "a bound needs a group for each entry");
 
@@ -179,7 +175,7 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, LC)
+__global__ void __launch_bounds__(kThreads, kCtas)
     logprob_kernel(const __grid_constant__ trit_logprob_job J, uint32_t *err, int cluster) {
     constexpr int E = Row<S>::E;
     __shared__ u64 keys[kRoom];
@@ -266,12 +262,26 @@ __global__ void __launch_bounds__(kThreads, LC)
         c += kThreads;
     }
     const uint32_t whole = from < to && !row.is_whole(to - 1) ? to - 1 : to;
-    for (; c + (kFlight - 1) * kThreads < whole; c += kFlight * kThreads) {
-        uint4 u[kFlight];
+    // (the next kFlight are asked for before these are looked at)
+    uint4 u[kFlight];
+    bool more = c + (kFlight - 1) * kThreads < whole;
+    if (more) {
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) u[k] = row.whole(c + k * kThreads);
+    }
+    while (more) {
+        uint4 now[kFlight];
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k) see_whole(u[k], c + k * kThreads);
+        for (int k = 0; k < kFlight; ++k) now[k] = u[k];
+        const uint32_t next = c + kFlight * kThreads;
+        more = next + (kFlight - 1) * kThreads < whole;
+        if (more) {
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) u[k] = row.whole(next + k * kThreads);
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) see_whole(now[k], c + k * kThreads);
+        c = next;
     }
     for (; c < to; c += kThreads) see(c);
     const float2 la = unpack2(add2(l2[0], l2[1])), wa = unpack2(add2(w2[0], w2[1]));
