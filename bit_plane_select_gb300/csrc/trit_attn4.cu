@@ -51,6 +51,7 @@ struct Args4 {
     Args A;                          // its cache: the codes, strides in vectors
     const uint8_t *k_scale, *v_scale;
     float scale2;                    // scale log2(e)
+    int32_t runs;                    // whether 32 keys from a multiple of 32 on always lie side by side
 };
 
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool ok, std::integral_constant<int, 8>) {
@@ -97,6 +98,77 @@ __device__ __forceinline__ bool odd16(uint32_t pair) {         // an infinity or
     return (pair & 0x7c00u) == 0x7c00u || (pair & 0x7c000000u) == 0x7c000000u;
 }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
+
+// The same as join_last, every part of a row on its way at once into a warp's `room` slots of 512 bytes (a
+// thread's own 16, so that no other thread waits for them).
+template <typename T, int D, int RT>
+__device__ __forceinline__ void join_apart(const Args &A, const Batch &S, const Place &q, int rows, int64_t W,
+                                           int64_t count, int32_t *scratch, const uint8_t *slots, int room) {
+    const int64_t s0 = int64_t(S.cum[q.b]) * A.J.cache.heads * A.own_tiles + (int64_t(q.h) * A.own_tiles + q.tile) * q.steps;
+    const int64_t c0 = chunk_of(s0, W, count);
+    const int parts = int(chunk_of(s0 + q.steps - 1, W, count) - c0) + 1;
+    uint32_t *arrived = A.count + c0;
+    if (threadIdx.x == 0) {
+        __threadfence();
+        const bool last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
+        if (last) *arrived = 0;
+        __threadfence();
+        scratch[0] = last;
+    }
+    __syncthreads();
+    if (scratch[0]) {
+        constexpr int LR = D / 4;                  // lanes of a row
+        const int lane = threadIdx.x & 31, j = lane % LR;
+        const uint8_t *mine = slots + lane * 16;
+        const uint32_t mine_at = tc::smem_u32(mine);
+        if (room > LR) room = LR;
+        for (int r = threadIdx.x / LR; r - lane / LR < RT; r += kThreads / LR) {      // (a warp's rows together)
+            const int row = q.tile * RT + r;
+            if (row - lane / LR >= rows) break;
+            const bool there = row < rows;
+            float m = -INFINITY, l = 0.0f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < parts; k0 += room) {
+                const int n = min(room, parts - k0);
+                // chunk c's part: at 2 c, or 2 c + 1 where the item begins in it
+                const float *first = A.parts + 2 * (c0 + k0) * part_floats(RT, D);
+                for (int k = 0; k < n; ++k)
+                    cp_async16(mine_at + k * 512, first + (2 * k + (k0 + k == 0 ? 1 : 0)) * part_floats(RT, D) + r * D + j * 4, there);
+                tc::cp_async_commit();
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                if (there && j < n)
+                    ml = __ldcg(reinterpret_cast<const float2 *>(
+                        first + (2 * j + (k0 + j == 0 ? 1 : 0)) * part_floats(RT, D) + RT * D + 2 * r));
+                float top = fmaxf(m, ml.x);
+#pragma unroll
+                for (int o = LR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                const float base = base_of(top), f0 = ex2(m - base);
+                m = top;
+                // -1: a part without keys, which holds no sums
+                const float f = ml.x == -INFINITY && ml.y == 0.0f ? -1.0f : ex2(ml.x - base);
+                float sum = f == -1.0f ? 0.0f : f * ml.y;
+#pragma unroll
+                for (int o = LR / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                l = l * f0 + sum;
+                v.x *= f0; v.y *= f0; v.z *= f0; v.w *= f0;
+                tc::cp_async_wait<0>();
+                for (int k = 0; k < n; ++k) {
+                    const float fk = __shfl_sync(~0u, f, k, LR);
+                    const float4 x = *reinterpret_cast<const float4 *>(mine + k * 512);
+                    if (fk == -1.0f) continue;
+                    v.x += fk * x.x; v.y += fk * x.y; v.z += fk * x.z; v.w += fk * x.w;
+                }
+            }
+            if (!there) continue;
+            const float inv = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+            const int t = token_of(A, row), g = row - t * A.G;
+            const int64_t at = (int64_t(q.b) * A.J.batch.T + t) * A.J.q_heads + int64_t(q.h) * A.G + g;
+            store_out<T>(A.J, at * D + j * 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            if (A.J.lse && j == 0) A.J.lse[at] = lse_of(m, l);
+        }
+    }
+    __syncthreads();   // scratch[0] is free again
+}
 
 template <typename T, int D, int NB>
 __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __grid_constant__ Args4 A4) {
@@ -175,6 +247,23 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
     // The copies of the warp's 32 keys of a step; a lane finds one key's place.  Rows past the
     // end and rows of pages outside the cache are filled with zeros.
     auto load_stage = [&](uint32_t st) {
+        if (A4.runs && lp.step * kStep + (warp + 1) * KW <= lk.n && page >= 0 && page < J.cache.pages) {
+            // all 32 there, in a row: one place for the warp (every lane's page is the same)
+            const int k = lp.step * kStep + warp * KW;
+            const int64_t vec = page * J.cache.page_stride + (k & (J.cache.page_size - 1)) + lp.h * J.cache.head_stride;
+            const uint8_t *kc = static_cast<const uint8_t *>(J.cache.k) + vec * Sh::CB + lane * 16;
+            const uint8_t *vc = static_cast<const uint8_t *>(J.cache.v) + vec * Sh::CB + lane * 16;
+            cp_async_small(st + Sh::kKsAt + lane * Sh::SB, A4.k_scale + (vec + lane) * Sh::SB, true, std::integral_constant<int, Sh::SB>{});
+            cp_async_small(st + Sh::kVsAt + lane * Sh::SB, A4.v_scale + (vec + lane) * Sh::SB, true, std::integral_constant<int, Sh::SB>{});
+            // row lane / CH + j 32 / CH: its swizzle depends on j by a constant
+            const uint32_t dst = st + codes_at<D>(lane / Sh::CH, lane % Sh::CH);
+#pragma unroll
+            for (int j = 0; j < Sh::CH; ++j) {
+                cp_async16(dst + j * 512, kc + j * 512, true);
+                cp_async16(dst + j * 512 + Sh::kVAt, vc + j * 512, true);
+            }
+            return;
+        }
         const int k = key_of_lane();
         const bool in = k < lk.n, good = in && page >= 0 && page < J.cache.pages;
         if (in && !good) raise_flag(A.err, TRIT_ERR_INDEX);
@@ -654,7 +743,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                 }
                 __syncthreads();
             }
-            if (!direct && J.batch.prefix_len == 0) join_last<T, D, RT>(A, S, p, rows, W, count, scratch);
+            if (!direct && J.batch.prefix_len == 0) {
+                // (the warp's other stages are free where nothing is left to load)
+                const bool all = u + 1 == hi;
+                join_apart<T, D, RT>(A, S, p, rows, W, count, scratch, all ? ring : st,
+                                     (all ? kStages : 1) * kStageBytes / 512);
+            }
             fresh = true;
         }
         load_next(stage);
@@ -735,6 +829,7 @@ cudaError_t launch_attn_paged4(const trit_attn4_job &J, uint32_t *err, cudaStrea
     A4.k_scale = static_cast<const uint8_t *>(J.cache.k_scale);
     A4.v_scale = static_cast<const uint8_t *>(J.cache.v_scale);
     A4.scale2 = J.scale * 1.4426950408889634f;
+    A4.runs = J.cache.slot_stride == 1 && A.page_shift >= 5;
     uint8_t *ws = static_cast<uint8_t *>(J.workspace);
     A.count = reinterpret_cast<uint32_t *>(ws);
     A.cum = reinterpret_cast<int32_t *>(ws + attn::kCountBytes);
