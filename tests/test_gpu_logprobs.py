@@ -124,6 +124,32 @@ def test_matches_the_definition(t, case):  # noqa: F811
         assert bool(((got[0][k:].double() - w).abs()[fine] <= 2e-4).all()) and bool((got[0][k:][~fine] == -math.inf).all())
 
 
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+@pytest.mark.parametrize("V,offset", [(40003, 0), (9001, 3), (130, 1)])
+def test_masks_of_the_lowest_value_and_far_rows(t, dt, V, offset):  # noqa: F811
+    """Rows masked by the type's lowest value, in part or whole and beside -inf; rows about the
+    distance from 0 where differences are taken another way, and across it."""
+    g = torch.Generator().manual_seed(V)
+    low = torch.finfo(dt).min
+    x = 2.5 * torch.randn(9, V, generator=g)
+    x[0, : V // 2] = low
+    x[1, V // 2:] = low
+    x[2] = low
+    x[3] = low
+    x[3, torch.rand(V, generator=g) < 0.5] = -math.inf
+    x[4] = low * 0.999 + x[4]
+    far = 60000.0 if dt is HF else 2.0 ** 20
+    x[5] += far
+    x[6] -= far
+    x[7] = far + torch.linspace(-40.0, 40.0, V)
+    x[8, ::3] = -far
+    x = x.to(dt)
+    tokens = torch.randint(V, (9,), generator=g, dtype=torch.int32)
+    got, err = run(t, x, tokens, 7, 5, offset)
+    check(got, pr.scored(x, tokens, 7), V)
+    assert err == 0
+
+
 def test_rows_that_are_not_numbers(t):  # noqa: F811
     g = torch.Generator().manual_seed(1)
     x = torch.randn(6, 40000, generator=g)
