@@ -17,11 +17,23 @@
 //     scale q.k = f sum_groups (s (q'.c) + z sum(q')).
 // V: an ldmatrix transposing 16-bit elements, each four columns of a key, gives the same
 // word with two keys' codes, so O^T += V^T P^T has the rows of its m16 tiles in the
-// order 4 g + i.  A value's s goes to the weights: P' = p s in fp16, against a power of two that
-// bounds s in what the warp has seen (2^8 at most; rounding to 2^-11 of each term); its z to
-// sums p z, one per row and group, in fp32.
+// order 4 g + i.  p is rounded to fp16 once for all groups (2^8 times as large, so that small ones keep
+// their bits); a group's s goes to a copy of it, as s in units of a power of two that bounds s in
+// what the warp has seen, and that product is rounded once more: 2 2^-11 of a term s c.  The z are
+// the A operand of one product more, whose row g is group g: sums p z in fp32, 2^-11 of a term.
 //
-// A warp has its own ring of three stages of 32 keys, so that 150 KB an SM are in flight.
+// A warp has its own ring of three stages of 32 keys, so that 165 KB an SM are in flight.  Where pages hold
+// runs of 32 keys a stage is copied from one place, else key by key (the address work of that
+// was 7% of the time of 64 sequences).  Of two dozen parts and more of a long item the last CTA
+// to come has as many on their way as its free stages hold.
+//
+// Measured, 20 query heads over 5 of 128: 64 sequences of 6000 to 16000 keys 111 us, 4.6 TB/s; two of
+// 90000 and 131001 keys 48 us; one of 700 keys 8.6 us.  24 x 5 drafts of 24 heads over 8 of
+// 64 behind 8005 keys: 72 us.  What bounds it is not memory but the issue of instructions (0.55 a clock
+// and scheduler; masks and shifts keep the ALU at 53%), and among drafts 8 warps an SM with
+// little to issue while one waits.  Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
+// of two stages (registers spill), chunks of uneven length for CTAs of uneven speed (125 us: calls that
+// follow one another overlap worse), tiles of 16 rows for the drafts (71 us: no gain).
 #include <type_traits>
 
 #include "trit_attn_items.cuh"
@@ -99,8 +111,9 @@ __device__ __forceinline__ bool odd16(uint32_t pair) {         // an infinity or
 }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
 
-// The same as join_last, every part of a row on its way at once into a warp's `room` slots of 512 bytes (a
-// thread's own 16, so that no other thread waits for them).
+// The same as join_last, but up to `room` parts of a row on their way at once, into a warp's slots of 512 bytes
+// (a thread's own 16, so that no other thread waits for them).  Two sequences of 90000 and
+// 131001 keys, 46 parts an item: 52.4 us with eight in registers, 48.3 so.
 template <typename T, int D, int RT>
 __device__ __forceinline__ void join_apart(const Args &A, const Batch &S, const Place &q, int rows, int64_t W,
                                            int64_t count, int32_t *scratch, const uint8_t *slots, int room) {

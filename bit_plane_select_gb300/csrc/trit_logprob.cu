@@ -386,6 +386,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const float2 la = unpack2(add2(l2[0], l2[1])), wa = unpack2(add2(w2[0], w2[1]));
     const float to_m = ex2(-off), l_seen = la.x + la.y;
     Sums a = {m, l_seen * to_m, to_m * kLn2 * fmaf(-off, l_seen, wa.x + wa.y)};
+    if (mode != kNothing) {        // the term of m is 1 and none of w is positive: no rounding makes an entropy negative
+        a.l = fmaxf(a.l, 1.0f);
+        a.w = fminf(a.w, 0.0f);
+    }
 
     const u64 best = N && m > -INFINITY ? key_of(m, top_group) : 0;      // (a NaN row's keys are not used)
     // the sums of the CTA

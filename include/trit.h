@@ -818,8 +818,9 @@ TRIT_API trit_status trit_kv4_read(const trit_kv4_read_job *job, uint32_t *err_f
  * flags, layouts and workspace rules.  Codes enter the products as they are
  * (exactly), q as fp16 after a power of two per row has brought its largest column to
  * [2^14, 2^15) (exact but for columns below 2^-24 of it, those to within 2^-35 of
- * it), and the pairs (s, z) are applied to the products' fp32 sums; exp(..) s, which
- * weighs the codes of a value, is rounded to fp16, up to 2^-11 of each term.
+ * it), and the pairs (s, z) are applied to the products' fp32 sums; the weights
+ * exp(..) of a value are rounded to fp16 (2^-11), and once more after a product with s: up to
+ * 2 2^-11 of each term s c and 2^-11 of each term z.
  *   q      `dtype`, TRIT_BF16 or TRIT_F16
  *   workspace  trit_attn4_workspace_bytes(job) bytes
  */

@@ -3,10 +3,10 @@ codes stand for, row by row.
 
 Tolerances.  A score is a sum of D exact products q' c per 64 columns, times s, plus z times
 a sum of q', in fp32: off by at most e = (D + 8) 2^-24 scale sum |q_i| (15 s + |z|), taken
-for the case's largest (about 2^-10), a factor of 1 +- e on a probability.  P s is
-rounded to fp16, 2^-11 of each term s c, and to 2^-25 absolutely against a bound of s times
-2^-8 to 2^-11 of it: below 2^-16 for the lengths here.  fp32 sums over at most 2^12 keys a part
-add 2^-12.  So |out - exact| <= (2^-11 + 2 e + 2^-12) sum_j p_j (s c + |z|)_j + 2^-16 +
+for the case's largest (about 2^-10), a factor of 1 +- e on a probability.  P is
+rounded to fp16 and P s once more, each by up to 2^-11 of a term s c (of a term z only the
+first), and to 2^-25 absolutely against a bound of s times 2^-8 to 2^-11 of it: below 2^-16
+for the lengths here.  fp32 sums over at most 2^12 keys a part add 2^-12.  So |out - exact| <= (2 2^-11 + 2 e + 2^-12) sum_j p_j (s c + |z|)_j + 2^-16 +
 w |exact| where the output is 16-bit, and |lse - exact| <= e + 2^-12 + 2^-22 |exact|."""
 import math
 
@@ -71,7 +71,7 @@ def check(c, out, lse, out_dt, scale=None):
             q = c["q"][b, i].double()
             want, wl = ref.attend(q, keys[:see], vals[:see], scale)
             mag, _ = ref.attend(q, keys[:see], sizes[:see], scale)
-            tol = (2.0 ** -11 + 2 * e + 2.0 ** -12) * mag + 2.0 ** -16 + wo * want.abs()
+            tol = (2 * 2.0 ** -11 + 2 * e + 2.0 ** -12) * mag + 2.0 ** -16 + wo * want.abs()
             assert bool(((out[b, i] - want).abs() <= tol).all()), (b, i)
             if see == 0:
                 assert bool((lse[b, i] == -math.inf).all()) and not bool(out[b, i].any())

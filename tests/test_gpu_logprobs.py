@@ -150,6 +150,19 @@ def test_masks_of_the_lowest_value_and_far_rows(t, dt, V, offset):  # noqa: F811
     assert err == 0
 
 
+@pytest.mark.parametrize("dt", [F32, BF, HF])
+def test_no_positive_logprob_and_no_negative_entropy(t, dt):  # noqa: F811
+    """Rows of one great logit each, of sizes whose products with log2 e round either way."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(64, 3001, generator=g)
+    x[torch.arange(64), torch.arange(64) * 40] = 30.0 + 61.0 * torch.rand(64, generator=g)
+    x = x.to(dt)
+    tokens = (torch.arange(64) * 40).int()
+    got, err = run(t, x, tokens, 2)
+    check(got, pr.scored(x, tokens, 2), 3001)
+    assert err == 0 and bool((got[0] <= 0).all()) and bool((got[1] >= 0).all()) and bool((got[3] <= 0).all())
+
+
 def test_rows_that_are_not_numbers(t):  # noqa: F811
     g = torch.Generator().manual_seed(1)
     x = torch.randn(6, 40000, generator=g)
