@@ -593,9 +593,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
         }
     };
     auto stage_products = [&](auto masked, uint8_t *st, uint32_t st_at, int key0) {
-        if (NB == 4 && tiles == 3) products(std::integral_constant<int, NB == 4 ? 3 : 1>{}, masked, st, st_at, key0);
-        else if (NB > 1 && tiles > NB / 2) products(std::integral_constant<int, NB>{}, masked, st, st_at, key0);
-        else products(std::integral_constant<int, NB == 4 ? 2 : 1>{}, masked, st, st_at, key0);
+        if (NB > 1 && tiles > 1) products(std::integral_constant<int, NB>{}, masked, st, st_at, key0);
+        else products(std::integral_constant<int, 1>{}, masked, st, st_at, key0);
     };
 
     int64_t u = lo;
@@ -780,7 +779,7 @@ size_t smem_of(const Args &A) {
            A.RT * 4 * (1 + P) + kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
 }
 
-Args layout(const trit_attn_job &J) { return layout_of(J, kStep, smem_of, false); }
+Args layout(const trit_attn_job &J) { return layout_of(J, kStep, smem_of, false, 16); }
 
 // The job as the shared layout knows it: a cache of codes, strides in vectors.
 trit_attn_job plain_of(const trit_attn4_job &J) {
@@ -822,8 +821,8 @@ template <typename T>
 cudaError_t launch_t(const Args4 &A4, cudaStream_t s) {
     const int RT = A4.A.RT;
     if (A4.A.J.cache.head_dim == 128)
-        return RT == 8 ? launch<T, 128, 1>(A4, s) : RT == 16 ? launch<T, 128, 2>(A4, s) : launch<T, 128, 4>(A4, s);
-    return RT == 8 ? launch<T, 64, 1>(A4, s) : RT == 16 ? launch<T, 64, 2>(A4, s) : launch<T, 64, 4>(A4, s);
+        return RT == 8 ? launch<T, 128, 1>(A4, s) : launch<T, 128, 2>(A4, s);
+    return RT == 8 ? launch<T, 64, 1>(A4, s) : launch<T, 64, 2>(A4, s);
 }
 
 }  // namespace

@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 
 // The work's layout from the job's sizes; the grid that a call would use.  kStep: keys of
 // an own step; smem_of: a CTA's dynamic shared memory; on_tc: the prefix is not among the items.
-inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const Args &), bool on_tc) {
+inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const Args &), bool on_tc, int most_tile = 32) {
     Args A = {};
     A.J = J;
     A.G = J.q_heads / J.cache.heads;
@@ -370,7 +370,7 @@ inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const
     const int64_t most_rows = pre_rows > A.R ? pre_rows : A.R;
     A.g_inv = A.R < 65536 ? uint32_t(((int64_t(1) << 32) + A.G - 1) / A.G) : 0;
     if (A.G == 1) A.g_inv = 0;
-    A.RT = most_rows > 16 ? 32 : most_rows > 8 ? 16 : 8;
+    A.RT = most_rows > 16 ? most_tile : most_rows > 8 ? 16 : 8;
     A.own_tiles = (A.R + A.RT - 1) / A.RT;
     A.pre_tiles = int((pre_rows + A.RT - 1) / A.RT);
     A.own_step = kStep;
