@@ -47,6 +47,8 @@ struct Args {
     int64_t tc_from[kPlans];
     int32_t own_step;        // keys of an own step
     float *tc_parts;         // workspace: their partial results, [item][tc_splits][stream]
+    int32_t split;           // its keys come as two 16-bit parts, 2 D columns a key, its queries in units of their own:
+    const float *q_units;    // [B T Hq]
 };
 
 // Row r's token r / G: a high product with ceil(2^32 / G) is exact for r G < 2^32.

@@ -27,13 +27,16 @@
 // was 7% of the time of 64 sequences).  Of two dozen parts and more of a long item the last CTA
 // to come has as many on their way as its free stages hold.
 //
+// A shared prefix that some hundred rows read is written out in 16 bits instead and goes through the
+// tensor cores' kernel (prefix_written_out).
+//
 // Measured, 20 query heads over 5 of 128: 64 sequences of 6000 to 16000 keys 111 us, 4.6 TB/s; two of
 // 90000 and 131001 keys 48 us; one of 700 keys 8.6 us.  24 x 5 drafts of 24 heads over 8 of
-// 64 behind 8005 keys: 72 us.  What bounds it is not memory but the issue of instructions (0.55 a clock
-// and scheduler; masks and shifts keep the ALU at 53%), and among drafts 8 warps an SM with
-// little to issue while one waits.  Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
+// 64 behind 8005 keys: 54 us (71 without the tensor cores).  What bounds it is not memory but the issue of
+// instructions (0.55 a clock and scheduler; masks and shifts keep the ALU at 53%).  Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
 // of two stages (registers spill), chunks of uneven length for CTAs of uneven speed (125 us: calls that
-// follow one another overlap worse), tiles of 16 rows for the drafts (71 us: no gain).
+// follow one another overlap worse), tiles of 32 rows (2 x 8 drafts over
+// 3443 keys 37 us where tiles of 16 take 29: registers spill and the join has more to do alone).
 #include <type_traits>
 
 #include "trit_attn_items.cuh"
@@ -207,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
     S.fresh = S.len + J.batch.B;
     const int32_t *cum = S.cum;
 
-    pdl_wait();
+    // (beside the prefix kernel, which started after all that this one reads was written)
+    if (!A.tc_items) pdl_wait();
     pdl_launch();
     {   // the page table on its way to L2 while the lengths are: every CTA a few lines of it
         const int64_t ints = int64_t(J.batch.B - 1) * J.batch.table_stride + J.batch.table_pages;
@@ -333,7 +337,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
             for (int64_t i = threadIdx.x; J.lse && i < rows; i += kThreads) J.lse[at + i] = -INFINITY;
         }
     }
-    if (lo >= hi) return;
+    if (lo >= hi) {
+        if (A.tc_items && blockIdx.x == 0) pdl_wait();     // see the end
+        return;
+    }
 
     float o[P][4][NB][4];        // columns 64 p + 32 (e / 2) + 4 (lane / 4) + i, row 2 (lane % 4) + e % 2
     float z[NB][2];              // of lanes 4 pg + t: sum of p z of group pg, row 2 t + e
@@ -768,6 +775,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
         ++p.step;
         ++u;
     }
+    // the join waits for this grid alone and reads the prefix kernel's results too: one CTA
+    // ends after that kernel
+    if (A.tc_items && blockIdx.x == 0) pdl_wait();
     tc::cp_async_wait<0>();
 }
 
@@ -779,7 +789,182 @@ size_t smem_of(const Args &A) {
            A.RT * 4 * (1 + P) + kWarps * A.RT * 8 + kWarps * 4 + (size_t(A.J.batch.B) * 3 + 1) * 4;
 }
 
-Args layout(const trit_attn_job &J) { return layout_of(J, kStep, smem_of, false, 16); }
+// A prefix that many rows read goes through the tensor cores' kernel, which wants 16 bits: written out once a
+// call, each value as two fp16 (s c + z to 22 bits), and the queries beside it as fp16 in units of
+// their own.  Weights are rounded once there, to fp16.
+constexpr int kPage = 128;         // keys of a page of that copy
+// Measured, here and on tiles of 16 rows (us in all, own keys of 50 to 200): 5 heads of 128, 300 rows, prefix
+// of 1000 and 16000: 29 and 78, 36 and 161; 128 rows, 1000 and 4000: 24 and 30, 23 and 36; 8 heads of 64, 300 rows, 300
+// and 4000: 22 and 34, 22 and 48; 126 rows, 4000: 29, 26; one head of 128, 296 rows, 1000 and 4000: 19 and 21, 17
+// and 27.  (A tile of 128 rows is filled in pairs; the copy is held to 1 GB.)
+bool prefix_written_out(const trit_attn_job &J) {
+    const int64_t rows = int64_t(J.batch.B) * J.batch.T * (J.q_heads / J.cache.heads);
+    const int64_t columns = J.batch.prefix_len * J.cache.heads * J.cache.head_dim;
+    return rows > 96 && columns <= int64_t(1) << 27 && double(rows) * double(columns) >= (rows > 128 ? 1e8 : 3.2e8);
+}
+
+Args layout(const trit_attn_job &J) { return layout_of(J, kStep, smem_of, prefix_written_out(J), 16, true); }
+
+// What the copy takes of the workspace, behind the partial results: K, V, the queries, their units, pages' numbers.
+struct Copy {
+    int64_t pages, vectors, k, v, q, units, table, end;      // offsets in bytes
+};
+Copy copy_of(const Args &A) {
+    const trit_attn_job &J = A.J;
+    Copy c = {};
+    c.k = head_bytes(A) + part_bytes(A) + (A.tc_items ? prefix_part_bytes(A) : 0);
+    c.end = c.k;
+    if (!A.tc_items) return c;
+    c.k = (c.k + 255) / 256 * 256;
+    c.pages = (J.batch.prefix_len + kPage - 1) / kPage;
+    c.vectors = c.pages * kPage * J.cache.heads;
+    c.v = c.k + c.vectors * J.cache.head_dim * 4;
+    c.q = c.v + c.vectors * J.cache.head_dim * 4;
+    const int64_t rows = int64_t(J.batch.B) * J.batch.T * J.q_heads;
+    c.units = c.q + rows * J.cache.head_dim * 2;
+    c.table = c.units + rows * 4;
+    c.end = (c.table + c.pages * 4 + 255) / 256 * 256;
+    return c;
+}
+
+struct WriteArgs {
+    trit_attn_job J;                 // its cache: the codes, strides in vectors
+    const uint8_t *k_scale, *v_scale;
+    uint32_t *err;
+    __half *k, *v, *q;               // [heads][pages * kPage][2 D] (hi, lo), [B T][Hq][D]
+    float *units;
+    int32_t *table;
+    uint32_t flip, keep;             // the sign of scale, and 0 where it is 0, on pairs of q
+    int32_t keys;                    // pages * kPage
+    int32_t q_blocks;                // blocks of the queries, the first ones
+    int32_t page_shift;
+};
+
+// What is finite in fp16's range, the rest as it is.
+__device__ __forceinline__ float held(float x) { return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x; }
+
+// Eight columns a lane, vectors of K and then of V, each by head and key.  Bound by latency and by its stores: 4
+// bytes a code.
+constexpr int kWriteThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kWriteThreads) write_out_kernel(const __grid_constant__ WriteArgs A) {
+    const trit_attn_job &J = A.J;
+    constexpr int L = D / 8;
+    pdl_wait();
+    pdl_launch();
+    if (int(blockIdx.x) < A.q_blocks) {       // a lane D / 32 columns of a row
+        const int lane = threadIdx.x & 31;
+        const int64_t row = int64_t(blockIdx.x) * (kWriteThreads / 32) + (threadIdx.x >> 5);
+        if (row >= int64_t(J.batch.B) * J.batch.T * J.q_heads) return;
+        const int64_t token = row / J.q_heads;
+        constexpr int C = D / 64;             // pairs of columns
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(static_cast<const T *>(J.q) + token * J.q_stride + (row - token * J.q_heads) * D) + lane * C;
+        float2 x[C];
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            x[i] = unpack16<T>((__ldg(src + i) & A.keep) ^ A.flip);
+            most = fmaxf(most, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        // the largest column to [2^14, 2^15)
+        int e = 14 - ((__float_as_int(most) >> 23) - 127);
+        e = e > 100 ? 100 : e < -100 ? -100 : e;
+        const float f = power2(e);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(A.q + row * D) + lane * C;
+#pragma unroll
+        for (int i = 0; i < C; ++i) dst[i] = pack16<__half>(x[i].x * f, x[i].y * f);
+        if (lane == 0) A.units[row] = power2(-e);
+        return;
+    }
+    const int block = int(blockIdx.x) - A.q_blocks;
+    if (block == 0)
+        for (int i = threadIdx.x; i < A.keys / kPage; i += kWriteThreads) A.table[i] = i;
+    const int64_t at = (int64_t(block) * kWriteThreads + threadIdx.x) / L, half = int64_t(A.keys) * J.cache.heads;
+    if (at >= 2 * half) return;
+    const bool is_v = at >= half;
+    const int64_t vec = is_v ? at - half : at;
+    const int h = int(vec / A.keys), key = int(vec - int64_t(h) * A.keys), sub = threadIdx.x % L;
+    uint32_t word = 0;
+    __half2 sz = {};
+    if (key < J.batch.prefix_len) {
+        const int col = A.page_shift >= 0 ? key >> A.page_shift : key / J.cache.page_size;
+        const int page = __ldg(J.batch.prefix_table + col);
+        if (page >= 0 && page < J.cache.pages) {
+            const int64_t from = page * J.cache.page_stride + int64_t(key - col * J.cache.page_size) * J.cache.slot_stride + h * J.cache.head_stride;
+            word = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(is_v ? J.cache.v : J.cache.k) + from * (D / 2)) + sub);
+            sz = __ldg(reinterpret_cast<const __half2 *>((is_v ? A.v_scale : A.k_scale) + from * (D / 16)) + sub / 8);
+        } else if (sub == 0) {
+            raise_flag(A.err, TRIT_ERR_INDEX);
+        }
+    }
+    const float2 f = __half22float2(sz);
+    const float s[4] = {f.x, f.x * 0.0625f, f.x * 0.00390625f, f.x * 0.000244140625f};
+    uint32_t w[4], rest[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float y[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            // 2^23 + c 16^n, exactly, by its bits; what is finite stays so
+            const int n = 2 * i + j;
+            const float c = __uint_as_float(0x4b000000u | ((n < 4 ? word : word >> 16) & (15u << (4 * (n & 3))))) - 8388608.0f;
+            y[j] = fmaf(c, s[n & 3], f.y);
+        }
+        const float2 most = {held(y[0]), held(y[1])};
+        w[i] = pack16<__half>(most.x, most.y);
+        const float2 hi = unpack16<__half>(w[i]);
+        rest[i] = pack16<__half>(fabsf(y[0]) < INFINITY ? held(y[0] - hi.x) : 0.0f, fabsf(y[1]) < INFINITY ? held(y[1] - hi.y) : 0.0f);
+    }
+    __half *const to = (is_v ? A.v : A.k) + vec * 2 * D + sub * 8;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(to + D) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+}
+
+// The copy, and the tensor cores' kernel over it.
+template <typename T, int D>
+cudaError_t launch_written(const Args4 &A4, cudaStream_t s) {
+    Args A = A4.A;
+    const Copy c = copy_of(A);
+    uint8_t *ws = reinterpret_cast<uint8_t *>(A.count);
+    WriteArgs W = {};
+    W.J = A.J;
+    W.k_scale = A4.k_scale;
+    W.v_scale = A4.v_scale;
+    W.err = A.err;
+    W.k = reinterpret_cast<__half *>(ws + c.k);
+    W.v = reinterpret_cast<__half *>(ws + c.v);
+    W.q = reinterpret_cast<__half *>(ws + c.q);
+    W.units = reinterpret_cast<float *>(ws + c.units);
+    W.table = reinterpret_cast<int32_t *>(ws + c.table);
+    W.flip = A.J.scale < 0.0f ? 0x80008000u : 0u;
+    W.keep = A.J.scale == 0.0f ? 0u : 0xffffffffu;
+    W.keys = int32_t(c.pages * kPage);
+    W.page_shift = A.page_shift;
+    const int64_t rows = int64_t(A.J.batch.B) * A.J.batch.T * A.J.q_heads;
+    W.q_blocks = int32_t((rows + kWriteThreads / 32 - 1) / (kWriteThreads / 32));
+    const int64_t lanes = 2 * c.vectors * (D / 8);
+    const cudaError_t e = launch_pdl(write_out_kernel<T, D>, dim3(unsigned(W.q_blocks + (lanes + kWriteThreads - 1) / kWriteThreads)),
+                                     dim3(kWriteThreads), 0, s, W);
+    if (e != cudaSuccess) return e;
+    A.scale2 = A.J.scale == 0.0f ? 1.0f : fabsf(A4.scale2);
+    A.flip = 0;
+    A.keep = 0xffffffffu;
+    A.q_units = W.units;
+    A.J.q = W.q;
+    A.J.q_stride = int64_t(A.J.q_heads) * D;
+    A.J.cache.k = W.k;
+    A.J.cache.v = W.v;
+    A.J.cache.slot_stride = D;
+    A.J.cache.page_stride = kPage * D;
+    A.J.cache.head_stride = int64_t(W.keys) * D;
+    A.J.cache.pages = int32_t(c.pages);
+    A.J.cache.page_size = kPage;
+    A.J.cache.dtype = TRIT_F16;
+    A.J.batch.prefix_table = W.table;
+    return launch_prefix(A, s);
+}
 
 // The job as the shared layout knows it: a cache of codes, strides in vectors.
 trit_attn_job plain_of(const trit_attn4_job &J) {
@@ -810,6 +995,8 @@ cudaError_t launch(const Args4 &A4, cudaStream_t s) {
     const Args &A = A4.A;
     const auto kernel = attn4_kernel<T, D, NB>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 180 * 1024);
+    // (the own keys' kernel depends on nothing of the prefix's and may run beside it)
+    if (e == cudaSuccess && A.tc_items) e = launch_written<T, D>(A4, s);
     if (e == cudaSuccess) e = launch_pdl(kernel, dim3(unsigned(A.grid)), dim3(kThreads), smem_of(A), s, A4);
     if (e != cudaSuccess || A.J.batch.prefix_len == 0) return e;
     const int64_t joins = int64_t(A.J.batch.B) * A.J.cache.heads * ((A.R + 3) / 4);
@@ -829,8 +1016,7 @@ cudaError_t launch_t(const Args4 &A4, cudaStream_t s) {
 }  // namespace attn
 
 int64_t attn4_workspace_bytes(const trit_attn4_job &J) {
-    const attn::Args A = attn::layout(attn::plain_of(J));
-    return attn::head_bytes(A) + attn::part_bytes(A);
+    return attn::copy_of(attn::layout(attn::plain_of(J))).end;
 }
 
 cudaError_t launch_attn_paged4(const trit_attn4_job &J, uint32_t *err, cudaStream_t s) {
@@ -846,6 +1032,7 @@ cudaError_t launch_attn_paged4(const trit_attn4_job &J, uint32_t *err, cudaStrea
     A.count = reinterpret_cast<uint32_t *>(ws);
     A.cum = reinterpret_cast<int32_t *>(ws + attn::kCountBytes);
     A.parts = reinterpret_cast<float *>(ws + attn::head_bytes(A));
+    A.tc_parts = A.parts + attn::part_bytes(A) / 4;
     return J.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A4, s) : attn::launch_t<__half>(A4, s);
 }
 

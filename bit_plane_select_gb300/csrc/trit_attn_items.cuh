@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kJoin *D) join_kernel(const __grid_constant__ 
 
 // The work's layout from the job's sizes; the grid that a call would use.  kStep: keys of
 // an own step; smem_of: a CTA's dynamic shared memory; on_tc: the prefix is not among the items.
-inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const Args &), bool on_tc, int most_tile = 32) {
+inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const Args &), bool on_tc, int most_tile = 32,
+                      bool split = false) {
     Args A = {};
     A.J = J;
     A.G = J.q_heads / J.cache.heads;
@@ -388,6 +389,7 @@ inline Args layout_of(const trit_attn_job &J, int kStep, size_t (*smem_of)(const
     const int64_t grid = int64_t(kSms) * per_sm;
     A.grid = int(most < grid ? most : grid);
     A.resident = resident;
+    A.split = split;
     if (on_tc) prefix_layout(A, most);     // and the grid, beside it
     return A;
 }

@@ -35,7 +35,6 @@ namespace attn {
 namespace {
 
 constexpr int kRows = 128;
-constexpr int kRing = 4;
 constexpr int kMmaWarp = 8;       // 8 and 9: an issuing warp per stream
 constexpr int kLoadWarp = 10;     // 10 and 11: K's copies and V's
 constexpr int kThreads = 384;      // 8 softmax warps and the four above
@@ -47,8 +46,14 @@ constexpr float kGrow = 8.0f;      // log2 of the growth of a maximum that O tol
 
 template <int D>
 __host__ __device__ constexpr int tile_bytes() { return kBlockKeys * D * 2; }
-template <int D>
-constexpr size_t smem_bytes() { return 1024 + size_t(2 + kRing) * tile_bytes<D>() + 256; }
+// SPLIT: keys and values as two 16-bit parts whose sum is meant (hi, then lo: 2 D columns); where D = 128 that leaves
+// room for one tile of each.  S and O sum both parts' products.  (Their copies end with zeros.)
+template <int D, bool SPLIT>
+__host__ __device__ constexpr int ring_of() { return SPLIT && D == 128 ? 2 : 4; }
+template <int D, bool SPLIT>
+__host__ __device__ constexpr int stage_bytes() { return tile_bytes<D>() * (SPLIT ? 2 : 1); }
+template <int D, bool SPLIT>
+constexpr size_t smem_bytes() { return 1024 + size_t(2) * tile_bytes<D>() + size_t(ring_of<D, SPLIT>()) * stage_bytes<D, SPLIT>() + 256; }
 
 __device__ __forceinline__ void tma_page(void *dst, const CUtensorMap *map, int x, int slot, int head, int page,
                                          uint64_t *bar) {
@@ -63,15 +68,15 @@ __device__ __forceinline__ void tma_page(void *dst, const CUtensorMap *map, int 
 // issuing warps.
 __device__ __forceinline__ void tmem_ready() { asm volatile("bar.sync 1, 320;" ::: "memory"); }
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ Args A, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    constexpr int kTile = tile_bytes<D>();
+    constexpr int kTile = tile_bytes<D>(), kRing = ring_of<D, SPLIT>(), kStage = stage_bytes<D, SPLIT>();
     uint8_t *qs = smem, *ring = smem + 2 * kTile;
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kTile);
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kRing * kStage);
     uint64_t *empty = full + kRing;
     uint64_t *s_full = empty + kRing;    // stream's S is in tensor memory
     uint64_t *p_full = s_full + 2;       // [stream][quarter]: P of 32 keys each is
@@ -107,7 +112,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int j0 = int(int64_t(nb) * split / splits), j1 = int(int64_t(nb) * (split + 1) / splits);
     const int n = j1 - j0;
-    const bool pair = 2 * group + 1 < A.tc_tiles;     // two row tiles, or one over two streams
+    // two row tiles, or one over two streams (split: always two, the last perhaps empty, since with a ring of two both
+    // streams must see every tile)
+    const bool pair = SPLIT || 2 * group + 1 < A.tc_tiles;
 
     if (warp == kMmaWarp && lane < kBars) {       // a barrier per lane, in the order above
         const int i = lane;
@@ -154,16 +161,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int have = 0, ids = fetch(lane), ids_next = fetch(32 + lane);
         const bool is_v = warp > kLoadWarp;
         const CUtensorMap *map = is_v ? &vmap : &kmap;
-        const int c = lane / (D / 64), half = lane % (D / 64);     // the lane's copy of a block
+        constexpr int halves = (SPLIT ? 2 : 1) * (D / 64);
+        const int c = lane / halves, half = lane % halves;         // the lane's copy of a block
         for (int j = 0; j < n; ++j) {
             const int at = is_v ? v_at(j) : k_at(j), s = at % kRing;
             const int key0 = (j0 + j) * kBlockKeys;
             const int first = key0 / ps;
             const int copies = per_block < npages - first ? per_block : npages - first;
             const int keys = P - key0 < kBlockKeys ? P - key0 : kBlockKeys;
-            const bool clear = is_v && keys < kBlockKeys;
+            const bool clear = !SPLIT && is_v && keys < kBlockKeys;
             uint64_t *bar = clear ? tail : &full[s];
-            uint8_t *st = ring + s * kTile;
+            uint8_t *st = ring + s * kStage;
             if (j * per_block >= have + 32) {
                 have += 32;
                 ids = ids_next;
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int page = __shfl_sync(~0u, ids, (j * per_block + c - have) & 31);
             if (c < copies && (page < 0 || page >= J.cache.pages)) raise_flag(A.err, TRIT_ERR_INDEX);   // reads as zeros
             if (!warp_wait(&empty[s], ((at / kRing) & 1) ^ 1, timed_out)) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * D * 2);
+            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(copies) * rows * halves * 128);
             __syncwarp();
             if (c < copies)
                 tma_page(st + half * (kBlockKeys * 128) + c * rows * 128, map, half * 64, key0 - first * ps, h, page, bar);
@@ -215,12 +223,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto issue_s = [&](int i) {
             const int st = k_at(pair ? i : 2 * i + s) % kRing;
             tc_fence_after();
-            const uint32_t b = rk + st * (kTile >> 4);
+            const uint32_t b = rk + st * (kStage >> 4);
             if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
+                for (int kk = 0; kk < (SPLIT ? 2 : 1) * D / 16; ++kk) {
                     const uint32_t off = (kk / 4) * (kBlockKeys * 128 >> 4) + (kk % 4) * 2;
-                    mma_ss(sp, qlo + off, b + off, idesc_s<T>(), kk > 0);
+                    const int qk = kk % (D / 16);
+                    mma_ss(sp, qlo + (qk / 4) * (kBlockKeys * 128 >> 4) + (qk % 4) * 2, b + off, idesc_s<T>(), kk > 0);
                 }
                 mma_commit(&s_full[s]);
                 mma_commit(&empty[st]);
@@ -232,7 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pipe together and then the exponentials together (measured: 4100 SM-clocks a
         // block pair in step): with the first stream's second block, or behind its first where
         // there are few
-        const int go_block = n >= 8 ? 1 : 0, go_part = n >= 8 ? 0 : 3;
+        // (with a ring of two the second block needs the second stream's look at the first)
+        const bool late = kRing == 4 && n >= 8;
+        const int go_block = late ? 1 : 0, go_part = late ? 0 : 3;
         if (s == 1) ok = ok && warp_wait(go, 0, timed_out);
         if (ok && mine > 0) {
             ok = k_there(0);
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < mine; ++i) {
             const int at = v_at(pair ? i : 2 * i + s), st = at % kRing;
             ok = warp_wait(&full[st], (at / kRing) & 1, timed_out);
-            const uint32_t b = rv + st * (kTile >> 4);
+            const uint32_t b = rv + st * (kStage >> 4);
 #pragma unroll
             for (int part = 0; part < 4; ++part) {
                 ok = ok && warp_wait(&p_full[4 * s + part], i & 1, timed_out);
@@ -252,6 +263,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
                         mma_ts(o, sp + kk * 8, b + kk * (2048 >> 4), idesc_o<T, D>(), i > 0 || kk > 0);
+                    if (SPLIT) {
+#pragma unroll
+                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                            mma_ts(o, sp + kk * 8, b + (kTile >> 4) + kk * (2048 >> 4), idesc_o<T, D>(), true);
+                    }
                 }
                 __syncwarp();
             }
@@ -303,7 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ready();     // after the queries: the allocation takes as long
         tc_fence_after();
         const uint32_t tmem = *tmem_slot;
-        const float scale2 = A.scale2;
+        float scale2 = A.scale2;
+        if (SPLIT) {
+            const int fr = (2 * group + (pair ? s : 0)) * kRows + r, b = fr / A.R, rr = fr - b * A.R, t = rr / A.G;
+            if (fr < J.batch.B * A.R)
+                scale2 *= A.q_units[(int64_t(b) * J.batch.T + t) * J.q_heads + int64_t(h) * A.G + rr - t * A.G];
+        }
         const int mine = pair ? n : (n + 1 - s) / 2;       // this stream's blocks
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
@@ -409,15 +430,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The cache as (column, slot, head, page); a copy is 64 columns of min(page_size,
 // 128) keys of one head's page.
-bool make_map(CUtensorMap *map, const trit_kv_cache &C, void *base) {
+bool make_map(CUtensorMap *map, const trit_kv_cache &C, void *base, int width) {      // width: parts of a key
     const EncodeFn fn = encoder();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {cuuint64_t(C.head_dim), cuuint64_t(C.page_size), cuuint64_t(C.heads),
+    const cuuint64_t dims[4] = {cuuint64_t(C.head_dim) * width, cuuint64_t(C.page_size), cuuint64_t(C.heads),
                                 cuuint64_t(C.pages)};
-    const cuuint64_t one = cuuint64_t(C.head_dim) * 2;   // a dimension of one entry needs no stride
-    const cuuint64_t strides[3] = {C.page_size > 1 ? cuuint64_t(C.slot_stride) * 2 : one,
-                                   C.heads > 1 ? cuuint64_t(C.head_stride) * 2 : one,
-                                   C.pages > 1 ? cuuint64_t(C.page_stride) * 2 : one};
+    const cuuint64_t one = cuuint64_t(C.head_dim) * 2 * width;   // a dimension of one entry needs no stride
+    const cuuint64_t strides[3] = {C.page_size > 1 ? cuuint64_t(C.slot_stride) * 2 * width : one,
+                                   C.heads > 1 ? cuuint64_t(C.head_stride) * 2 * width : one,
+                                   C.pages > 1 ? cuuint64_t(C.page_stride) * 2 * width : one};
     const cuuint32_t box[4] = {64, cuuint32_t(C.page_size < kBlockKeys ? C.page_size : kBlockKeys), 1, 1};
     const cuuint32_t unit[4] = {1, 1, 1, 1};
     return fn(map, C.dtype == TRIT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
@@ -425,20 +446,20 @@ bool make_map(CUtensorMap *map, const trit_kv_cache &C, void *base) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT = false>
 cudaError_t launch(const Args &A, cudaStream_t s) {
     CUtensorMap kmap, vmap;
-    if (!make_map(&kmap, A.J.cache, A.J.cache.k) || !make_map(&vmap, A.J.cache, A.J.cache.v))
+    if (!make_map(&kmap, A.J.cache, A.J.cache.k, SPLIT ? 2 : 1) || !make_map(&vmap, A.J.cache, A.J.cache.v, SPLIT ? 2 : 1))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem_bytes<D>()));
+    cudaError_t e = cudaFuncSetAttribute(prefix_kernel<T, D, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(smem_bytes<D, SPLIT>()));
     if (e != cudaSuccess) return e;
     // the register split draws on what the launch allocates: never start it with less
     cudaFuncAttributes f;
-    e = cudaFuncGetAttributes(&f, prefix_kernel<T, D>);
+    e = cudaFuncGetAttributes(&f, prefix_kernel<T, D, SPLIT>);
     if (e != cudaSuccess) return e;
     if (f.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
-    return launch_pdl(prefix_kernel<T, D>, dim3(unsigned(A.tc_items * A.tc_splits)), dim3(kThreads), smem_bytes<D>(), s, A,
+    return launch_pdl(prefix_kernel<T, D, SPLIT>, dim3(unsigned(A.tc_items * A.tc_splits)), dim3(kThreads), smem_bytes<D, SPLIT>(), s, A,
                       kmap, vmap);
 }
 
@@ -464,6 +485,7 @@ void prefix_layout(Args &A, int64_t most) {
     const int64_t rows = int64_t(J.batch.B) * A.R;
     const int nb = int((J.batch.prefix_len + kBlockKeys - 1) / kBlockKeys);
     A.tc_tiles = int((rows + kRows - 1) / kRows);
+    A.tc_tiles += A.split ? A.tc_tiles & 1 : 0;
     A.tc_groups = (A.tc_tiles + 1) / 2;
     A.tc_items = A.tc_groups * J.cache.heads;
     // The parts s each item is cut into, by a model in us fitted to sweeps.  The prefix
@@ -524,6 +546,7 @@ void prefix_layout(Args &A, int64_t most) {
 }
 
 cudaError_t launch_prefix(const Args &A, cudaStream_t s) {
+    if (A.split) return A.J.cache.head_dim == 128 ? launch<__half, 128, true>(A, s) : launch<__half, 64, true>(A, s);
     if (A.J.cache.dtype == TRIT_BF16)
         return A.J.cache.head_dim == 128 ? launch<__nv_bfloat16, 128>(A, s) : launch<__nv_bfloat16, 64>(A, s);
     return A.J.cache.head_dim == 128 ? launch<__half, 128>(A, s) : launch<__half, 64>(A, s);

@@ -820,7 +820,9 @@ TRIT_API trit_status trit_kv4_read(const trit_kv4_read_job *job, uint32_t *err_f
  * [2^14, 2^15) (exact but for columns below 2^-24 of it, those to within 2^-35 of
  * it), and the pairs (s, z) are applied to the products' fp32 sums; the weights
  * exp(..) of a value are rounded to fp16 (2^-11), and once more after a product with s: up to
- * 2 2^-11 of each term s c and 2^-11 of each term z.
+ * 2 2^-11 of each term s c and 2^-11 of each term z.  A long shared prefix of many rows is
+ * first written into the workspace as pairs of fp16 whose sum is the value to 2^-22
+ * of it (2^-25 absolutely; values past fp16's range up to twice that range); the workspace's size counts it in.
  *   q      `dtype`, TRIT_BF16 or TRIT_F16
  *   workspace  trit_attn4_workspace_bytes(job) bytes
  */

@@ -6,7 +6,8 @@ a sum of q', in fp32: off by at most e = (D + 8) 2^-24 scale sum |q_i| (15 s + |
 for the case's largest (about 2^-10), a factor of 1 +- e on a probability.  P is
 rounded to fp16 and P s once more, each by up to 2^-11 of a term s c (of a term z only the
 first), and to 2^-25 absolutely against a bound of s times 2^-8 to 2^-11 of it: below 2^-16
-for the lengths here.  fp32 sums over at most 2^12 keys a part add 2^-12.  So |out - exact| <= (2 2^-11 + 2 e + 2^-12) sum_j p_j (s c + |z|)_j + 2^-16 +
+for the lengths here.  fp32 sums over at most 2^12 keys a part add 2^-12.  (A prefix that is written out has its values to 2^-22 of them and 2^-25 -- of scores, less than
+the room of 8 roundings in e -- and its weights rounded once.)  So |out - exact| <= (2 2^-11 + 2 e + 2^-12) sum_j p_j (s c + |z|)_j + 2^-16 +
 w |exact| where the output is 16-bit, and |lse - exact| <= e + 2^-12 + 2^-22 |exact|."""
 import math
 
@@ -96,6 +97,43 @@ def test_matches_64_bits(t, case, wide):  # noqa: F811
     c = build_case(lens, T, new, hq, hkv, D, page, dt, prefix, nhd, seed=len(lens) + prefix)
     err, _ = run(t, c, F32 if wide else dt)
     assert err == 0
+
+
+MANY = [
+    # lens, T, new, heads, key heads, D, page, type, prefix, order: all behind a prefix that is written out
+    ([5, 300, 0, 70] * 10, 1, None, 20, 5, 128, 64, BF, 4101, False),
+    ([60 + 7 * i for i in range(24)], 5, [i % 6 for i in range(24)], 24, 8, 64, 16, HF, 1501, True),
+    ([9, 40] * 20, 4, None, 8, 1, 128, 48, HF, 2049, False),
+    ([3] * 52, 5, [5, 0, 1, 3] * 13, 7, 7, 64, 5, BF, 999, False),
+    ([64] * 100, 1, None, 32, 8, 128, 128, HF, 1024, True),
+    ([17] * 33, 1, None, 24, 6, 64, 16, BF, 8200, False),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_rows_behind_a_prefix(t, case, wide):  # noqa: F811
+    lens, T, new, hq, hkv, D, page, dt, prefix, nhd = case
+    c = build_case(lens, T, new, hq, hkv, D, page, dt, prefix, nhd, seed=prefix)
+    rows, columns = len(lens) * T * (hq // hkv), prefix * hkv * D
+    assert rows * columns >= (1e8 if rows > 128 else 3.2e8)      # (or this would be another kernel's test)
+    err, job = run(t, c, F32 if wide else dt)
+    assert err == 0 and job.workspace.numel() > 8 * columns
+
+
+@pytest.mark.parametrize("scale", [-0.03, 0.0])
+def test_many_rows_scales_and_bad_pages(t, scale):  # noqa: F811
+    c = build_case([30] * 60, 1, None, 20, 5, 128, 16, BF, 3000)
+    for x in c["four"][2:]:
+        x.nan_to_num_(0.0)
+    err, _ = run(t, c, F32, scale)
+    assert err == 0
+    d = dict(c, pre=c["pre"].clone())
+    d["pre"][7], d["pre"][100] = -1, 10 ** 6
+    flag, job = torch.zeros(1, dtype=torch.int32, device="cuda"), make_job(t, d, F32, scale)
+    t.trit_attn_paged4(job, flag)
+    torch.cuda.synchronize()
+    assert int(flag.item()) == t.ERR_INDEX and bool(job.out.isfinite().all())
 
 
 @pytest.mark.parametrize("scale", [0.02, -0.03, 0.0])
