@@ -35,6 +35,7 @@ namespace attn {
 namespace {
 
 constexpr int kRows = 128;
+constexpr int kRing = 4;
 constexpr int kMmaWarp = 8;       // 8 and 9: an issuing warp per stream
 constexpr int kLoadWarp = 10;     // 10 and 11: K's copies and V's
 constexpr int kThreads = 384;      // 8 softmax warps and the four above
@@ -49,7 +50,7 @@ __host__ __device__ constexpr int tile_bytes() { return kBlockKeys * D * 2; }
 // SPLIT: keys and values as two 16-bit parts whose sum is meant (hi, then lo: 2 D columns); where D = 128 that leaves
 // room for one tile of each.  S and O sum both parts' products.  (Their copies end with zeros.)
 template <int D, bool SPLIT>
-__host__ __device__ constexpr int ring_of() { return SPLIT && D == 128 ? 2 : 4; }
+__host__ __device__ constexpr int ring_of() { return SPLIT && D == 128 ? 2 : kRing; }
 template <int D, bool SPLIT>
 __host__ __device__ constexpr int stage_bytes() { return tile_bytes<D>() * (SPLIT ? 2 : 1); }
 template <int D, bool SPLIT>
