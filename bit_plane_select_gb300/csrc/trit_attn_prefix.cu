@@ -23,6 +23,9 @@
 // sequences' own by the join kernel.  They are stored four columns by row,
 // [D/4][128] float4, so that a warp's 32 rows store 512 contiguous bytes.
 //
+// Keys and values that come as two parts (SPLIT: trit_attn4.cu's copies of a 4-bit prefix) take both
+// products twice: 992 rows of D = 128 on each of 5 heads against 16000 keys 150 us in all.
+//
 // Measured: 1024 rows of D = 128 on each of 5 heads against 32768 keys, on 80 of 152 SMs,
 // beside the sequences' own keys: 137 us in all, 645 TFLOP/s, most of it here; what bounds
 // it is the chain of a stream's block (S, softmax, P V, S).  P goes to the products in

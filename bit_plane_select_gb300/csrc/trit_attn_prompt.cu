@@ -11,7 +11,7 @@
 // also covers the beginning and end of a tile by the other's work; or, where there are
 // fewer tiles than SMs, one CTA whose two streams take a tile's blocks of keys by turns
 // (TURNS) and are joined at the end.  (Measured, us: one prompt of 16384 tokens, 20 query heads over 5 of
-// 128: 849; two tiles of one CTA sharing the loads of K and V 965.  700 tokens: 12.4 by turns, 13.9 a
+// 128: 849 in short bursts, 910 call after call under the power limit; in bursts two tiles of one CTA sharing the loads of K and V 965.  700 tokens: 12.4 by turns, 13.9 a
 // tile per CTA.)  P goes to the products in halves of 64 keys (in quarters 855 to 890 us, whole 928):
 // every store to tensor memory is waited for, and takes its turn behind the products under way.
 //

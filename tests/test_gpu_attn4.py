@@ -121,6 +121,46 @@ def test_many_rows_behind_a_prefix(t, case, wide):  # noqa: F811
     assert err == 0 and job.workspace.numel() > 8 * columns
 
 
+def test_written_out_prefix_captured_shared_and_beside_another(t):  # noqa: F811
+    """A call that writes its prefix out and one of other sizes share a workspace in turn, captured and replayed
+    with other queries; on two streams, each with a workspace, both as alone."""
+    cases = [build_case([40] * 70, 1, None, 20, 5, 128, 64, BF, 2500, seed=1),
+             build_case([500, 30, 0], 2, None, 8, 2, 64, 16, HF, 100, seed=2)]
+    jobs = [make_job(t, c, c["dt"]) for c in cases]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for j in jobs:
+        t.trit_attn_paged4(j, err)
+    torch.cuda.synchronize()
+    alone = [(j.out.clone(), j.lse.clone()) for j in jobs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, j in zip(streams, jobs):
+            t.trit_attn_paged4(j, err, stream=s)
+    torch.cuda.synchronize()
+    for j, (out, lse) in zip(jobs, alone):
+        assert torch.equal(j.out, out) and torch.equal(j.lse, lse)
+    ws = torch.zeros(max(j.workspace.numel() for j in jobs), dtype=torch.uint8, device="cuda")
+    queries = [c["q"].cuda() for c in cases]
+    shared = [make_job(t, c, c["dt"], workspace=ws, q=q) for c, q in zip(cases, queries)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for j in shared + shared[:1]:
+            t.trit_attn_paged4(j, err)
+    graph.replay()
+    torch.cuda.synchronize()
+    for j, (out, lse) in zip(shared, alone):
+        assert torch.equal(j.out, out) and torch.equal(j.lse, lse)
+    for c, q in zip(cases, queries):
+        c["q"] = c["q"].flip(0)
+        q.copy_(c["q"])
+    graph.replay()
+    torch.cuda.synchronize()
+    for c, j in zip(cases, shared):
+        check(c, j.out, j.lse, c["dt"])
+    assert int(err.item()) == 0
+
+
 @pytest.mark.parametrize("scale", [-0.03, 0.0])
 def test_many_rows_scales_and_bad_pages(t, scale):  # noqa: F811
     c = build_case([30] * 60, 1, None, 20, 5, 128, 16, BF, 3000)
