@@ -132,8 +132,10 @@ __device__ __forceinline__ int find_by_length(const PromptArgs &A, int k, int la
     if (lane < A.J.B) s = span_of(A, lane, &bad);
     if (bad && report) raise_flag(A.err, TRIT_ERR_INDEX);
     const int units = (s.nq + A.unit - 1) / A.unit;
-    // the lane's first unit with at least x blocks (those behind it have them too)
+    // the lane's first unit with at least x blocks (those behind it have them too); units whose last token sees no
+    // key have none
     auto first_with = [&](int x) {
+        if (x <= 0) return 0;
         const int need = (x - 1) * kBlockKeys + 1 - (s.nk - s.nq);      // tokens up to its last
         if (need > s.nq) return units;
         return need <= A.unit ? 0 : (need + A.unit - 1) / A.unit - 1;
