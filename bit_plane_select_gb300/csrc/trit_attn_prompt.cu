@@ -104,14 +104,29 @@ __device__ __forceinline__ Span from_lane(const Span &s, int who) {
     return Span{__shfl_sync(~0u, s.q0, who), __shfl_sync(~0u, s.nq, who), __shfl_sync(~0u, s.k0, who),
                 __shfl_sync(~0u, s.nk, who)};
 }
+// Of 32 sequences, one a lane, in their order: where starts fall, some may have rows in common and more tiles than the
+// grid.  One that has rows of a sequence before it is left out too; `taken` ends the rows of those that are not.
+__device__ __forceinline__ void keep_apart(Span &s, int lane, int32_t &taken) {
+    for (int i = 0; i < 32; ++i) {
+        const int32_t q0 = __shfl_sync(~0u, s.q0, i), n = __shfl_sync(~0u, s.nq, i);
+        if (n == 0) continue;
+        if (q0 >= taken) taken = q0 + n;
+        else if (lane == i) s.nq = 0;
+    }
+}
 // In the order of the sequences, 32 at a time, a sequence's last units first.
 __device__ __forceinline__ int find_in_order(const PromptArgs &A, int k, int lane, bool report, Span &me) {
     int unit = -1;
+    int32_t taken = -1;                           // (-1: all starts so far are in order)
     for (int b0 = 0; b0 < A.J.B; b0 += 32) {
         bool bad = false;
         Span s{0, 0, 0, 0};
         if (b0 + lane < A.J.B) s = span_of(A, b0 + lane, &bad);
         if (bad && report) raise_flag(A.err, TRIT_ERR_INDEX);
+        if (taken >= 0 || __any_sync(~0u, bad)) {
+            if (taken < 0) taken = b0 ? A.J.q_starts[b0] : 0;
+            keep_apart(s, lane, taken);
+        }
         const int n = (s.nq + A.unit - 1) / A.unit, inc = lane_scan(n, lane), all = __shfl_sync(~0u, inc, 31);
         if (unit < 0 && k < all) {
             const int who = __ffs(int(__ballot_sync(~0u, k < inc))) - 1;
@@ -131,6 +146,10 @@ __device__ __forceinline__ int find_by_length(const PromptArgs &A, int k, int la
     Span s{0, 0, 0, 0};
     if (lane < A.J.B) s = span_of(A, lane, &bad);
     if (bad && report) raise_flag(A.err, TRIT_ERR_INDEX);
+    if (__any_sync(~0u, bad)) {
+        int32_t taken = 0;
+        keep_apart(s, lane, taken);
+    }
     const int units = (s.nq + A.unit - 1) / A.unit;
     // the lane's first unit with at least x blocks (those behind it have them too); units whose last token sees no
     // key have none
@@ -646,7 +665,7 @@ cudaError_t launch_attn_prompt(const trit_prompt_job &J, uint32_t *err, cudaStre
     A.unit = attn::kRows / A.heads;
     A.parts = (A.G + attn::kRows - 1) / attn::kRows;
     A.page = A.parts * J.heads;
-    // tiles: at most one begun for each sequence
+    // tiles: at most one begun for each sequence (whose rows are apart: keep_apart)
     const int64_t sms = device_sm_count(), grid = (J.q_rows / A.unit + J.B) * A.page;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
     const bool turns = grid <= sms;

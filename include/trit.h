@@ -856,8 +856,9 @@ TRIT_API trit_status trit_attn_paged4(const trit_attn4_job *job, uint32_t *err_f
  * for trit_attn_paged.  A row that sees no key gives out = 0 and lse = -inf; rows of
  * q in no sequence are left as they were in out and lse.  Keys that a row does not
  * see change nothing of it, whatever they hold.  Starts that fall or leave
- * [0, q_rows] or [0, k_rows] set TRIT_ERR_INDEX; such a sequence's rows are then
- * not computed.
+ * [0, q_rows] or [0, k_rows] set TRIT_ERR_INDEX; such a sequence is then not
+ * computed, and, where starts fall, no sequence that has query rows of a computed one
+ * before it.
  *   q      row r at r * q_stride elements: Hq vectors of D; k, v: `heads` vectors
  *          at r * k_stride and r * v_stride.  `dtype`, TRIT_BF16 or TRIT_F16; 16-byte
  *          aligned, strides multiples of 8 and at least a row.  k and v may be NULL

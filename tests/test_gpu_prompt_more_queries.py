@@ -8,7 +8,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_attn_prompt import BF, F32, HF, build, run, t  # noqa: E402,F401
+from test_gpu_attn_prompt import BF, F32, HF, build, check, make, run, t  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,18 @@ def test_rows_without_keys_are_zero(t, case, wide):  # noqa: F811
     nq, nk, hq, h, D, dt = case
     err, _ = run(t, build(nq, nk, hq, h, D, dt, seed=D + len(nq)), F32 if wide else dt)
     assert err == 0
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_starts_that_fall(t, many):  # noqa: F811
+    """The sequences before the fall are whole, the ones behind it that have rows of theirs are left out (`many`:
+    found in their order)."""
+    c = build([20, 480], [20, 480], 8, 2, 64, BF)
+    at = torch.tensor([2, 22, 502, 102, 482] + [482] * (30 if many else 0))
+    job = make(t, dict(c, qs=at, ks=at), BF)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        t.trit_attn_prompt(job, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == t.ERR_INDEX
+    check(c, job)

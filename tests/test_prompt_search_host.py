@@ -192,3 +192,47 @@ def test_many_sequences_in_their_order(search):
     want = units_of(q, k, 4, range(150))
     room, got, err = search(q, k, 4, False, q[-1], k[-1], len(want) + 2)
     assert len(want) <= room and err == 0 and sorted(x for x in got if x[0] >= 0) == want
+
+
+def apart(q, k, q_rows, k_rows):
+    """The sequences that are computed: starts in order and in range, and, once some are not, no rows of one
+    before."""
+    good, taken, fell = [], 0, False
+    for b in range(len(q) - 1):
+        ok = 0 <= q[b] <= q[b + 1] <= q_rows and 0 <= k[b] <= k[b + 1] <= k_rows
+        fell = fell or not ok
+        if ok and q[b + 1] > q[b]:
+            assert fell or q[b] >= taken
+            if q[b] >= taken:
+                good.append(b)
+                taken = q[b + 1]
+    return good, fell
+
+
+@pytest.mark.parametrize("by_length", [False, True])
+def test_starts_that_fall_leave_the_others_their_tiles(search, by_length):
+    """A sequence before the fall keeps its tiles however many the sequences behind it would have."""
+    q, k = [0, 20, 500, 100, 480], [0, 20, 500, 100, 480]
+    room, got, err = search(q, k, 4, by_length, 500, 500, 40)
+    assert [x for x in got if x[0] >= 0 and x[1:] == (0, 20, 0, 20)] == [(0, 0, 20, 0, 20)]
+    assert sorted(x for x in got if x[0] >= 0) == units_of(q, k, 4, [0, 1]) and err != 0
+    assert all(x[0] < 0 for x in got[room:])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_any_starts(search, seed):
+    """Starts out of order and out of range: computed sequences are found once, and fit the grid."""
+    import random
+    rng = random.Random(seed)
+    B, G = rng.choice([1, 5, 20, 32, 33, 90]), rng.choice([1, 3, 4, 128])
+    q, k = (starts([rng.randrange(300 // G + 2) for _ in range(B)]) for _ in range(2))
+    q_rows, k_rows = q[-1] + 1, k[-1] + 1
+    for _ in range(seed % 4):
+        x = rng.choice([q, q, k])
+        x[rng.randrange(B + 1)] = rng.choice([-1, 0, 3, q_rows // 2, q_rows - 1, 2 ** 31 - 1, -2 ** 31])
+    good, fell = apart(q, k, q_rows, k_rows)
+    want = units_of(q, k, G, good)
+    for by_length in (False, True) if B <= 32 else (False,):
+        room, got, err = search(q, k, G, by_length, q_rows, k_rows, len(want) + 4)
+        assert len(want) <= room and bool(err) == fell
+        assert sorted(x for x in got if x[0] >= 0) == want
