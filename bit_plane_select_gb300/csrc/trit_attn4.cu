@@ -112,6 +112,9 @@ __device__ __forceinline__ uint32_t half_power2(int e) {       // a pair of 2^e,
 __device__ __forceinline__ bool odd16(uint32_t pair) {         // an infinity or NaN among two fp16 values
     return (pair & 0x7c00u) == 0x7c00u || (pair & 0x7c000000u) == 0x7c000000u;
 }
+// What the weights of a row with greatest score x are taken against: they are up to 2^kLift.  From 2^24 on x less kLift
+// is no fp32 number of its own: there up to 1.
+__device__ __forceinline__ float lifted(float x) { return fabsf(x) < 16777216.0f ? x - kLift : x; }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
 
 // The same as join_last, but up to `room` parts of a row on their way at once, into a warp's slots of 512 bytes
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
 
     float o[P][4][NB][4];        // columns 64 p + 32 (e / 2) + 4 (lane / 4) + i, row 2 (lane % 4) + e % 2
     float z[NB][2];              // of lanes 4 pg + t: sum of p z of group pg, row 2 t + e
-    float m[NB][2], l[NB][2];
+    float m[NB][2], l[NB][2];    // what the row's weights are against, and their sum
     int lim[NB][2];
     int bound[P];                // exponent field that no s seen so far exceeds
     uint32_t blind = 0;      // the thread's rows that see none of the item's keys
@@ -472,10 +475,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                const float top = fmaxf(m[n][e], mx), base = base_of(top) - kLift;
-                alpha[n][e] = ex2(m[n][e] - base - kLift);
+                const float to = fmaxf(m[n][e], lifted(mx)), base = base_of(to);
+                alpha[n][e] = ex2(m[n][e] - base);
                 moved |= alpha[n][e] != 1.0f;
-                m[n][e] = top;
+                m[n][e] = to;
                 float sum = 0.0f;
 #pragma unroll
                 for (int km = 0; km < KM; ++km)
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                     sum += __shfl_xor_sync(~0u, sum, 16);
                     if (lane < 4) {
                         const bool none = (blind >> (2 * n + e)) & 1;
-                        stats[(warp * RT + n * 8 + r) * 2] = none ? -INFINITY : m[n][e] - kLift;
+                        stats[(warp * RT + n * 8 + r) * 2] = none ? -INFINITY : m[n][e];
                         stats[(warp * RT + n * 8 + r) * 2 + 1] = none ? 0.0f : sum;
                     }
 #pragma unroll
