@@ -17,7 +17,7 @@
 //     scale q.k = f sum_groups (s (q'.c) + z sum(q')).
 // V: an ldmatrix transposing 16-bit elements, each four columns of a key, gives the same
 // word with two keys' codes, so O^T += V^T P^T has the rows of its m16 tiles in the
-// order 4 g + i.  p is rounded to fp16 once for all groups (2^8 times as large, so that small ones keep
+// order 4 g + i.  p is rounded to fp16 once for all groups (2^15 times as large, so that small ones keep
 // their bits); a group's s goes to a copy of it, as s in units of a power of two that bounds s in
 // what the warp has seen, and that product is rounded once more: 2 2^-11 of a term s c.  The z are
 // the A operand of one product more, whose row g is group g: sums p z in fp32, 2^-11 of a term.
@@ -49,7 +49,7 @@ constexpr int kStages = 3;
 constexpr int KW = 32;                     // keys of a warp's stage
 constexpr int kStep = KW * kWarps;
 constexpr int kGroup = TRIT_KV4_GROUP;
-constexpr float kLift = 8.0f;              // weights are up to 2^8, so that fp16 holds small ones too
+constexpr float kLift = 15.0f;             // weights are up to 2^15, so that fp16 holds small ones too
 
 template <int D>
 struct Shape {
@@ -112,9 +112,9 @@ __device__ __forceinline__ uint32_t half_power2(int e) {       // a pair of 2^e,
 __device__ __forceinline__ bool odd16(uint32_t pair) {         // an infinity or NaN among two fp16 values
     return (pair & 0x7c00u) == 0x7c00u || (pair & 0x7c000000u) == 0x7c000000u;
 }
-// What the weights of a row with greatest score x are taken against: they are up to 2^kLift.  From 2^24 on x less kLift
-// is no fp32 number of its own: there up to 1.
-__device__ __forceinline__ float lifted(float x) { return fabsf(x) < 16777216.0f ? x - kLift : x; }
+// What the weights of a row with greatest score x are taken against, so that they are up to 2^kLift.  From 2^24 on
+// x less kLift may be no fp32 number: rounded upwards, since a weight of 2^16 is past fp16's range.
+__device__ __forceinline__ float lifted(float x) { return __fsub_ru(x, kLift); }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // e in -126..127
 
 // The same as join_last, but up to `room` parts of a row on their way at once, into a warp's slots of 512 bytes
