@@ -18,8 +18,11 @@
 // V: an ldmatrix transposing 16-bit elements, each four columns of a key, gives the same
 // word with two keys' codes, so O^T += V^T P^T has the rows of its m16 tiles in the
 // order 4 g + i.  p is rounded to fp16 once for all groups (2^15 times as large, so that small ones keep
-// their bits); a group's s goes to a copy of it, as s in units of a power of two that bounds s in
-// what the warp has seen, and that product is rounded once more: 2 2^-11 of a term s c.  The z are
+// their bits); a group's s goes to a copy of it, as s in a unit that fits it, and that
+// product is rounded once more: 2 2^-11 of a term s c, or 2^-32 of s c where the weight is small.  One unit, a power of
+// two, does for keys whose s lie within 2^8 of one another; others are gone through apart, so that what
+// one key's values are off by does not depend on another's (64 sequences of 6000 to 16000 keys of a usual
+// spread: 109 us, 110 with one unit for all: a vote a stage).  The z are
 // the A operand of one product more, whose row g is group g: sums p z in fp32, 2^-11 of a term.
 //
 // A warp has its own ring of three stages of 32 keys, so that 165 KB an SM are in flight.  Where pages hold
@@ -30,7 +33,7 @@
 // A shared prefix that some hundred rows read is written out in 16 bits instead and goes through the
 // tensor cores' kernel (prefix_written_out).
 //
-// Measured, 20 query heads over 5 of 128: 64 sequences of 6000 to 16000 keys 111 us, 4.6 TB/s; two of
+// Measured, 20 query heads over 5 of 128: 64 sequences of 6000 to 16000 keys 109 us, 4.7 TB/s; two of
 // 90000 and 131001 keys 48 us; one of 700 keys 8.6 us.  24 x 5 drafts of 24 heads over 8 of
 // 64 behind 8005 keys: 54 us (71 without the tensor cores).  What bounds it is not memory but the issue of
 // instructions (0.55 a clock and scheduler; masks and shifts keep the ALU at 53%).  Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
     float z[NB][2];              // of lanes 4 pg + t: sum of p z of group pg, row 2 t + e
     float m[NB][2], l[NB][2];    // what the row's weights are against, and their sum
     int lim[NB][2];
-    int bound[P];                // exponent field that no s seen so far exceeds
+    int unit[P];                 // sums of s c are in units of 2^(unit - 14)
     uint32_t blind = 0;      // the thread's rows that see none of the item's keys
     int nkeys = 0, tiles = 1, first_step = 0, clear = 0;   // no limit lies below `clear`
     int cq = 0;
@@ -503,11 +506,25 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                         for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= alpha[n][e & 1];
             }
         }
-        // the pairs of V: a lane looks at one key's.  In units of a power of two that bounds s in
-        // what the warp has seen.
-        uint32_t inv[P];
+        // The pairs of V: a lane looks at one key's.  s counts in a unit, 2^(unit - 14), that keeps s over it in
+        // [2^-8, 1) (exactly; an s of 0 and a subnormal one may be less), so that a product p s is as
+        // exact as p, whatever other keys hold.  Keys that the unit does not fit move it; where a stage's lie
+        // too far apart for one it is gone through in parts, a range of eight exponents each.  In a stage that some
+        // rows see in part the ranges are fixed ones: a key hidden from a row then has no part in its roundings.
+        uint32_t *own = reinterpret_cast<uint32_t *>(st + Sh::kVsAt + lane * Sh::SB);
+        uint32_t left = 0;           // ranges still to come
+        auto move_unit = [&](int pg, int to) {
+            if (to == unit[pg]) return;
+            const float f = power2(unit[pg] - to);
+            unit[pg] = to;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NM; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= f;
+        };
         {
-            uint32_t *own = reinterpret_cast<uint32_t *>(st + Sh::kVsAt + lane * Sh::SB);
             uint32_t pair[P];
             bool bad = false;
 #pragma unroll
@@ -519,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                 // A NaN that some row does not see must not meet its P = 0: it goes to the rows that do, one by
                 // one, and out of the stage.
                 uint32_t which = __ballot_sync(~0u, bad);
-                for (uint32_t left = which; left; left &= left - 1) {
-                    const int k = __ffs(int(left)) - 1;
+                for (uint32_t more = which; more; more &= more - 1) {
+                    const int k = __ffs(int(more)) - 1;
 #pragma unroll
                     for (int pg = 0; pg < P; ++pg) {
                         const uint32_t v = __shfl_sync(~0u, pair[pg], k);
@@ -539,67 +556,109 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                     __syncwarp();
                 }
             }
+            bool fits = !MASKED;
 #pragma unroll
-            for (int pg = 0; pg < P; ++pg) {
-                const uint32_t most = __reduce_max_sync(~0u, (pair[pg] >> 10) & 31u);
-                if (int(most) > bound[pg]) {
-                    const int to = int(most) + 1;
-                    const float f = bound[pg] < 0 ? 0.0f : power2(bound[pg] - to);      // (nothing summed up yet: 0)
-                    bound[pg] = to;
+            for (int pg = 0; pg < P; ++pg) fits = fits && (pair[pg] & 0x7fffu) - (uint32_t(unit[pg] - 7) << 10) < (8u << 10);
+            if (MASKED || !__all_sync(~0u, fits)) {
+                uint32_t there[P];           // exponents of the stage's s that are not 0
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                for (int pg = 0; pg < P; ++pg)
+                    there[pg] = __reduce_or_sync(~0u, pair[pg] & 0x7fffu ? 1u << ((pair[pg] >> 10) & 31u) : 0u);
+                bool far = MASKED;
 #pragma unroll
-                        for (int n = 0; n < NM; ++n)
+                for (int pg = 0; pg < P; ++pg) far |= __clz(int(there[pg])) + __ffs(int(there[pg])) <= 24;     // more than 8
+                if (!far) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) o[pg][i][n][e] *= f;
+                    for (int pg = 0; pg < P; ++pg)
+                        if (there[pg] & ~(0xffu << (unit[pg] - 7)))
+                            move_unit(pg, max(7, min(31, (31 - __clz(int(there[pg])) + __ffs(int(there[pg])) + 7) / 2)));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int pg = 0; pg < P; ++pg) left |= (there[pg] >> (8 * c)) & 0xffu ? 1u << c : 0u;
+                    const int c = __ffs(int(left | 16u)) - 1;
+                    left &= left - 1;
+                    if (c < 4)
+#pragma unroll
+                        for (int pg = 0; pg < P; ++pg) move_unit(pg, 8 * c + 7);
+                    if (left) {      // K's pairs are no longer needed: V's go there, and to their own place part by part
+                        __syncwarp();
+#pragma unroll
+                        for (int pg = 0; pg < P; ++pg) {
+                            own[pg - Sh::kVsAt / 4 + Sh::kKsAt / 4] = pair[pg];
+                            own[pg] = int(pair[pg] >> 13 & 3u) == c ? pair[pg] : pair[pg] & 0xffff0000u;
+                        }
+                        __syncwarp();
+                    }
                 }
-                inv[pg] = half_power2(14 - bound[pg]);       // s inv < 1
             }
         }
+        // the weights as an operand, for all groups
+        uint32_t w[KM][NM][2];
+#pragma unroll
+        for (int km = 0; km < KM; ++km)
+#pragma unroll
+            for (int n = 0; n < NM; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) w[km][n][i] = transposed8(pack16<__half>(s[km][n][2 * i], s[km][n][2 * i + 1]));
         const int vrow = (lane >> 4) * 8 + (lane & 7), vch = (lane >> 3) & 1;
+        for (;;) {
+            uint32_t inv[P];
 #pragma unroll
-        for (int km = 0; km < KM; ++km) {
-            // the pairs of keys 2t, 2t + 1 and 8 further: s by keys, in units; z as a product's operand whose
-            // row pg is the group's
-            uint32_t sp[P][2], za[4] = {0, 0, 0, 0};
+            for (int pg = 0; pg < P; ++pg) inv[pg] = half_power2(14 - unit[pg]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t *at = st + Sh::kVsAt + (km * 16 + 8 * i + t2) * Sh::SB;
-                if (P == 2) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(at);
-                    sp[0][i] = mul16(prmt(v.x, v.z, 0x5410u), inv[0]);
-                    sp[P - 1][i] = mul16(prmt(v.y, v.w, 0x5410u), inv[P - 1]);
-                    za[2 * i] = prmt(g == 0 ? v.x : v.y, g == 0 ? v.z : v.w, 0x7632u);
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                    sp[0][i] = mul16(prmt(v.x, v.y, 0x5410u), inv[0]);
-                    za[2 * i] = prmt(v.x, v.y, 0x7632u);
+            for (int km = 0; km < KM; ++km) {
+                // the pairs of keys 2t, 2t + 1 and 8 further: s by keys, in units; z as a product's operand whose
+                // row pg is the group's
+                uint32_t sp[P][2], za[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t *at = st + Sh::kVsAt + (km * 16 + 8 * i + t2) * Sh::SB;
+                    if (P == 2) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                        sp[0][i] = mul16(prmt(v.x, v.z, 0x5410u), inv[0]);
+                        sp[P - 1][i] = mul16(prmt(v.y, v.w, 0x5410u), inv[P - 1]);
+                        za[2 * i] = prmt(g == 0 ? v.x : v.y, g == 0 ? v.z : v.w, 0x7632u);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                        sp[0][i] = mul16(prmt(v.x, v.y, 0x5410u), inv[0]);
+                        za[2 * i] = prmt(v.x, v.y, 0x7632u);
+                    }
+                    if (g >= P) za[2 * i] = 0;
                 }
-                if (g >= P) za[2 * i] = 0;
-            }
-            uint32_t w[NM][2];
 #pragma unroll
-            for (int n = 0; n < NM; ++n) {
-                w[n][0] = transposed8(pack16<__half>(s[km][n][0], s[km][n][1]));
-                w[n][1] = transposed8(pack16<__half>(s[km][n][2], s[km][n][3]));
-                float zc[4] = {z[n][0], z[n][1], 0.0f, 0.0f};
-                mma16816<__half>(zc, za, w[n][0], w[n][1]);
-                z[n][0] = zc[0];
-                z[n][1] = zc[1];
+                for (int n = 0; n < NM; ++n) {
+                    float zc[4] = {z[n][0], z[n][1], 0.0f, 0.0f};
+                    mma16816<__half>(zc, za, w[km][n][0], w[km][n][1]);
+                    z[n][0] = zc[0];
+                    z[n][1] = zc[1];
+                }
+#pragma unroll
+                for (int pg = 0; pg < P; ++pg) {
+                    uint32_t f[4];
+                    ldsm4t(f, st_at + Sh::kVAt + codes_at<D>(km * 16 + vrow, 2 * pg + vch));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t a[4];
+                        operands(f, i, a);
+#pragma unroll
+                        for (int n = 0; n < NM; ++n)
+                            mma16816<__half>(o[pg][i][n], a, mul16(w[km][n][0], sp[pg][0]), mul16(w[km][n][1], sp[pg][1]));
+                    }
+                }
             }
+            if (!left) break;
+            const int c = __ffs(int(left)) - 1;
+            left &= left - 1;
+            __syncwarp();
 #pragma unroll
             for (int pg = 0; pg < P; ++pg) {
-                uint32_t f[4];
-                ldsm4t(f, st_at + Sh::kVAt + codes_at<D>(km * 16 + vrow, 2 * pg + vch));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t a[4];
-                    operands(f, i, a);
-#pragma unroll
-                    for (int n = 0; n < NM; ++n)
-                        mma16816<__half>(o[pg][i][n], a, mul16(w[n][0], sp[pg][0]), mul16(w[n][1], sp[pg][1]));
-                }
+                const uint32_t v = own[pg - Sh::kVsAt / 4 + Sh::kKsAt / 4];
+                own[pg] = int(v >> 13 & 3u) == c ? v & 0xffffu : 0u;      // (z has been added)
+                move_unit(pg, 8 * c + 7);
             }
+            __syncwarp();
         }
     };
     auto stage_products = [&](auto masked, uint8_t *st, uint32_t st_at, int key0) {
@@ -648,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
                 }
 #pragma unroll
             for (int pg = 0; pg < P; ++pg) {
-                bound[pg] = -1;
+                unit[pg] = 15;                 // s from 2^-7 to 2, as values of a usual spread have
 #pragma unroll
                 for (int n = 0; n < NB; ++n) {
                     z[n][0] = z[n][1] = 0.0f;
@@ -714,8 +773,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn4_kernel(const __gr
 #pragma unroll
                     for (int pg = 0; pg < P; ++pg) {
                         const float zs = __shfl_sync(~0u, z[n][e], 4 * pg + (lane & 3));
-                        // codes' units: 2^24 and 2^20, over inv = 2^(14 - bound)
-                        const float f0 = power2(10 + bound[pg]), f1 = power2(6 + bound[pg]);
+                        // codes' units: 2^24 and 2^20, over inv = 2^(14 - unit)
+                        const float f0 = power2(10 + unit[pg]), f1 = power2(6 + unit[pg]);
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const int at = pg * 64 + half * 32 + 4 * (lane >> 2);

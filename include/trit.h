@@ -655,8 +655,8 @@ TRIT_API trit_status trit_kv_append(const trit_kv_append_job *job, uint32_t *err
  * tensor-core instructions with fp32 sums; maxima, sums and partial outputs are
  * fp32.  For the second product exp(..) is rounded to the cache's type, whatever
  * out's type (the sum it is divided by is not): up to 2^-8 (bf16) or 2^-11 (fp16) of each
- * term.  A row that sees no key (padding, or nothing cached) gives out = 0 and
- * lse = -inf.  Keys past a sequence's length are never read: their slots may
+ * term (in fp16 of a weight below 2^-14 of the row's largest, 2^-25 of that).  A row
+ * that sees no key (padding, or nothing cached) gives out = 0 and lse = -inf.  Keys past a sequence's length are never read: their slots may
  * hold anything, and a later token's keys and values change nothing of an earlier
  * one.  lens[b] outside [0, table_pages * page_size] or a page id
  * outside the cache sets TRIT_ERR_INDEX (the length is clamped, the page's keys
@@ -818,11 +818,15 @@ TRIT_API trit_status trit_kv4_read(const trit_kv4_read_job *job, uint32_t *err_f
  * flags, layouts and workspace rules.  Codes enter the products as they are
  * (exactly), q as fp16 after a power of two per row has brought its largest column to
  * [2^14, 2^15) (exact but for columns below 2^-24 of it, those to within 2^-35 of
- * it), and the pairs (s, z) are applied to the products' fp32 sums; the weights
- * exp(..) of a value are rounded to fp16 (2^-11), and once more after a product with s: up to
- * 2 2^-11 of each term s c and 2^-11 of each term z.  A long shared prefix of many rows is
- * first written into the workspace as pairs of fp16 whose sum is the value to 2^-22
- * of it (2^-25 absolutely; values past fp16's range up to twice that range); the workspace's size counts it in.
+ * it; for a largest column in [2^-86, 2^115)), and the pairs (s, z) are applied to the
+ * products' fp32 sums.  A weight p = exp(..) of a value, 1 at the row's greatest score,
+ * is rounded to fp16, and once more after a product with s: of a term z it is off by
+ * up to 2^-11 p or 2^-40, of a term s c by up to 2 2^-11 p or 2^-32 (2^-47 / s where s is
+ * subnormal), whatever s and z other keys have.  (For scores below 2^23; beyond,
+ * 2^-25 and 2^-17 take the places of 2^-40 and 2^-32.)  A long shared prefix of many
+ * rows is first written into the workspace as pairs of fp16 whose sum is the value to
+ * 2^-22 of it (2^-25 absolutely; values past fp16's range up to twice that range), its
+ * weights off by up to 2^-11 p or 2^-25; the workspace's size counts it in.
  *   q      `dtype`, TRIT_BF16 or TRIT_F16
  *   workspace  trit_attn4_workspace_bytes(job) bytes
  */
