@@ -349,12 +349,14 @@ class ServedStack:
         """Buffers and prepared calls for the T new tokens of every sequence of `batch`."""
         from . import Append4Job, AppendJob, Attn4Job, AttnJob, trit_attn_paged, trit_attn_paged4, trit_kv4_append, trit_kv_append
         four = self.cache_bits == 4
-        plan = []
+        plan, workspaces = [], {}
         for L in self.layers:
-            hq, D = L["heads"]["q"], self.head_dim
+            hq, hk, D = L["heads"]["q"], L["heads"]["k"], self.head_dim
             B = self._buffers(L, batch.B * batch.T, (batch.B, batch.T, hq, D))
             B["append"] = (Append4Job if four else AppendJob)(L["cache"], batch, self.rope, B["q"], B["k"], B["v"], B["q_rot"])
-            B["attend"] = (Attn4Job if four else AttnJob)(L["cache"], batch, B["q_rot"], B["attn"])
+            # (layers of one size take turns with a workspace, which may hold a whole prefix)
+            B["attend"] = (Attn4Job if four else AttnJob)(L["cache"], batch, B["q_rot"], B["attn"], workspace=workspaces.get((hq, hk)))
+            workspaces[hq, hk] = B["attend"].workspace
             B["calls"] = [(trit_kv4_append if four else trit_kv_append, B["append"]),
                           (trit_attn_paged4 if four else trit_attn_paged, B["attend"])]
             plan.append(B)
