@@ -371,11 +371,11 @@ class ServedStack:
         from . import Append4Job, PromptJob, Read4Job, trit_attn_prompt, trit_kv4_append, trit_kv4_read
         if self.cache_bits != 4:
             raise ValueError("packed prompts need caches of 4 bits")
-        plan, packed = [], {}
+        plan, packed, shared = [], {}, {}
         for L in self.layers:
             hq, hk, D = L["heads"]["q"], L["heads"]["k"], self.head_dim
-            B = self._buffers(L, rows, (rows, hq, D))
-            for name in ("q_rot", "attn"):          # rows of no sequence stay 0
+            B = self._buffers(L, rows, (rows, hq, D), shared)
+            for name in ("q_rot", "attn"):          # rows of no sequence start as 0
                 B[name].zero_()
             if hk not in packed:                    # the layers take turns
                 packed[hk] = [torch.zeros((keys, hk, D), dtype=self.dtype, device=self.device) for _ in range(2)]
@@ -387,18 +387,26 @@ class ServedStack:
             plan.append(B)
         return plan
 
-    def _buffers(self, L, M: int, q_shape):
-        """A layer's buffers and products for M rows."""
+    def _buffers(self, L, M: int, q_shape, shared=None):
+        """A layer's buffers and products for M rows.  With `shared`, what no later layer reads is taken
+        from there, where another of the same size has left it."""
         D, dev = self.head_dim, self.device
 
         def buf(*shape, dtype=torch.float32):
             return torch.empty(shape, dtype=dtype, device=dev)
         K, F, hq, hk, P, S = L["K"], L["F"], L["heads"]["q"], L["heads"]["k"], L["P"], L["S"]
-        B = {"x_i8": buf(M, k_pad(K), dtype=torch.int8), "s": buf(M), "a_i8": buf(M, k_pad(hq * D), dtype=torch.int8),
-             "sa": buf(M), "h_i8": buf(M, k_pad(F), dtype=torch.int8), "sh": buf(M),
-             "q": buf(M, hq * D), "k": buf(M, hk * D), "v": buf(M, hk * D), "o": buf(M, K), "down": buf(M, K),
-             "gate": buf(M, F, dtype=torch.int32), "up": buf(M, F, dtype=torch.int32),
-             "q_rot": buf(*q_shape, dtype=self.dtype), "attn": buf(*q_shape)}
+        i8, i32, f32 = torch.int8, torch.int32, torch.float32
+        B = {"q_rot": buf(*q_shape, dtype=self.dtype), "attn": buf(*q_shape)}
+        for name, width, dtype in (("x_i8", k_pad(K), i8), ("a_i8", k_pad(hq * D), i8), ("h_i8", k_pad(F), i8), ("s", 0, f32),
+                                   ("sa", 0, f32), ("sh", 0, f32), ("q", hq * D, f32), ("k", hk * D, f32), ("v", hk * D, f32),
+                                   ("o", K, f32), ("down", K, f32), ("gate", F, i32), ("up", F, i32)):
+            at = (name, width)
+            if shared is None or at not in shared:
+                B[name] = buf(*((M, width) if width else (M,)), dtype=dtype)
+                if shared is not None:
+                    shared[at] = B[name]
+            else:
+                B[name] = shared[at]
         B["qkv_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, None, B[n]) for n in "qkv"])
         B["o_list"] = ProjList([(P["o"], S["o"], B["a_i8"], B["sa"], hq * D, None, B["o"])])
         B["gu_list"] = ProjList([(P[n], S[n], B["x_i8"], B["s"], K, B[n], None) for n in ("gate", "up")])

@@ -48,3 +48,36 @@ def test_one_workspace_for_a_plan_s_layers(t, bits):  # noqa: F811
     want = stack.step(apart, x.clone())
     torch.cuda.synchronize()
     assert torch.equal(got, want) and int(stack.err.item()) == 0 and bool(got.isfinite().all())
+
+
+def test_a_prompt_plan_s_layers_share_buffers(t):  # noqa: F811
+    """The products' buffers for a prompt's rows are there once for layers of one size; the first layer's results do
+    not change as more layers follow."""
+    g = torch.Generator().manual_seed(3)
+    total = [300, 41]
+    pages, _, table = ref.make_batch(g, total, 1, PAGE)
+    lens = torch.tensor(total, dtype=torch.int32).cuda()
+    starts = torch.tensor([0, 300, 341], dtype=torch.int32).cuda()
+    x = torch.randn(341, K, generator=g).cuda()
+    plans, outs = [], []
+    for layers in (1, 2, 3):
+        stack = stack_of(t, layers, 4, pages)
+        plan = stack.prompt_plan(t.KvBatch(table.cuda(), lens, 300), 341, starts, 341, starts)
+        outs.append(stack.step(plan, x.clone()))
+        torch.cuda.synchronize()
+        assert int(stack.err.item()) == 0
+        plans.append(plan)
+    for name in ("x_i8", "a_i8", "h_i8", "s", "sa", "sh", "q", "k", "v", "o", "down", "gate", "up"):
+        assert len({p[name].data_ptr() for p in plans[2]}) == 1, name
+    for name in ("q_rot", "attn"):
+        assert len({p[name].data_ptr() for p in plans[2]}) == 3
+        assert all(torch.equal(a[name], b[name]) for a, b in zip(plans[2], plans[1]))
+        assert torch.equal(plans[0][0][name], plans[1][0][name])
+    # the layers one by one, a plan each, on the caches of the last stack
+    y = x.clone()
+    every = list(stack.layers)
+    for L in every:
+        stack.layers = [L]
+        stack.step(stack.prompt_plan(t.KvBatch(table.cuda(), lens, 300), 341, starts, 341, starts), y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, outs[2])
