@@ -35,11 +35,14 @@
 //
 // Measured, 20 query heads over 5 of 128: 64 sequences of 6000 to 16000 keys 109 us, 4.7 TB/s; two of
 // 90000 and 131001 keys 48 us; one of 700 keys 8.6 us.  24 x 5 drafts of 24 heads over 8 of
-// 64 behind 8005 keys: 54 us (71 without the tensor cores).  What bounds it is not memory but the issue of
-// instructions (0.55 a clock and scheduler; masks and shifts keep the ALU at 53%).  Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
+// 64 behind 8005 keys: 54 us (71 without the tensor cores).  No unit is full (issue 0.54 a clock and scheduler, ALU 53%,
+// memory 57%): with 165 registers there are 2.7 warps a scheduler, and an instruction is most often held by the one
+// before it in its warp (1.4 warps an issue wait so, 0.55 for the ALU), a third of them masks and shifts.
+// Slower: codes by TMA (boxes of 32 keys of 64 bytes: 127 us), four CTAs
 // of two stages (registers spill), chunks of uneven length for CTAs of uneven speed (125 us: calls that
 // follow one another overlap worse), tiles of 32 rows (2 x 8 drafts over
-// 3443 keys 37 us where tiles of 16 take 29: registers spill and the join has more to do alone).
+// 3443 keys 37 us where tiles of 16 take 29: more registers spill and the join has more to do alone).
+// Tiles of 16 rows spill too where D = 128 (212 bytes stored, 176 loaded a thread; none in the other forms).
 #include <type_traits>
 
 #include "trit_attn_items.cuh"

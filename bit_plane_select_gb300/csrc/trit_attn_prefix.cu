@@ -499,7 +499,9 @@ void prefix_layout(Args &A, int64_t most) {
     // Every part is written and read once more.  (2.0 and 1.6, or 1.4 and 1.1, per block
     // choose parts that take 41.4 instead of 39.8 us for 24 x 5 drafts and 41.7 or 44.4 instead of
     // 39.6 for 96 sequences of D = 64.  256 sequences behind 32768 keys, before P went in
-    // quarters, 3, 4, 5 parts: 196, 151, 165.)
+    // quarters, 3, 4, 5 parts: 196, 151, 165.)  All of these are of 16-bit keys.  A prefix written out in two
+    // parts (split) takes the same numbers, although its products run twice and the own keys' steps are other ones
+    // (128 keys from codes): not fitted, and the parts chosen there may not be the best.
     const bool single = A.tc_tiles == 1, wide = J.cache.head_dim == 128;
     const double per_block = wide ? (single ? 1.2 : 1.6) : (single ? 0.9 : 1.3);
     const double per_step = A.RT > 16 ? 2.2 : wide ? 1.25 : 1.43;

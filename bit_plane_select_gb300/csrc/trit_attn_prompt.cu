@@ -671,7 +671,7 @@ cudaError_t launch_attn_prompt(const trit_prompt_job &J, uint32_t *err, cudaStre
     const bool turns = grid <= sms;
     // The search for the next longest pays where an SM takes a few tiles: four prompts of 595 to 1003
     // tokens behind 4125 to 9000 keys (512 tiles) 187 us, in their order 211; sixteen of 129 to 2048
-    // (2800 tiles) 164 and 154.
+    // (2800 tiles) 164 and 154.  Where between the two the orders cross has not been measured.
     A.sorted = J.B > 1 && J.B <= 32 && grid <= 4 * sms;
     return J.dtype == TRIT_BF16 ? attn::launch_t<__nv_bfloat16>(A, turns, grid, s) : attn::launch_t<__half>(A, turns, grid, s);
 }

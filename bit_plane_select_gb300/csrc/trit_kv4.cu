@@ -22,7 +22,9 @@ namespace trit {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kCtas = 6;                 // of append, an SM: 80 registers, 24 warps (five: 111 us where six take 107)
+// of append, an SM: 80 registers, 24 warps, for which the forms of eight columns a lane spill 4 to 56 bytes a thread (five,
+// which spill nothing: 111 us where six take 107)
+constexpr int kCtas = 6;
 constexpr int kGroup = TRIT_KV4_GROUP;
 constexpr float kMost = 65504.0f;        // fp16's largest: values saturate there
 
