@@ -121,6 +121,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // meet itself.
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// Whether a score of a row, m, is so far from 0 that half a step of fp32 there is two powers of two of a weight and
+// more: fma(s, scale2, -m), whose product is not rounded as m was, may then pass what 16 bits hold.
+__device__ __forceinline__ bool far_score(float m) { return fabsf(m) >= 33554432.0f; }     // 2^25
+
 // Four consecutive columns of a finished row.
 template <typename T>
 __device__ __forceinline__ void store_out(const trit_attn_job &J, int64_t at, float4 v) {

@@ -4,7 +4,7 @@
 
 #include <cuda.h>
 
-#include "trit_serve.cuh"
+#include "trit_attn.cuh"
 #include "trit_tc.cuh"
 
 namespace trit {
@@ -106,6 +106,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
+}
+// Of a row with a far score (far_score): its scale becomes the power of two below it, and its base m_raw in that scale, so
+// that weights are of exact differences from m_raw, the score that they are against.  (A score is known to a step there,
+// which is four powers of two of a weight and more.)
+__device__ __forceinline__ void far_scale(float m_raw, float &scale, float &base) {
+    scale = __uint_as_float(__float_as_uint(scale) & 0x7f800000u);
+    base = m_raw * scale;
 }
 // The same for a whole warp: one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t *timed_out) {
