@@ -376,6 +376,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
                 const float top = fmaxf(m[n][e], mx * A.scale2), base = base_of(top);
+                float k = A.scale2;
+                if (far_score(base)) {
+#pragma unroll
+                    for (int km = 0; km < KM; ++km) {
+                        s[km][n][e] = __fmul_rn(s[km][n][e], A.scale2);
+                        s[km][n][2 + e] = __fmul_rn(s[km][n][2 + e], A.scale2);
+                    }
+                    k = 1.0f;
+                }
                 alpha[n][e] = ex2(m[n][e] - base);
                 moved |= alpha[n][e] != 1.0f;
                 m[n][e] = top;
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NB)) attn_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float &v = s[km][n][2 * i + e];
-                        v = ex2(fmaf(v, A.scale2, -base));
+                        v = ex2(fmaf(v, k, -base));
                         sum += v;
                     }
                 l[n][e] = l[n][e] * alpha[n][e] + sum;

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scale2 *= A.q_units[(int64_t(b) * J.batch.T + t) * J.q_heads + int64_t(h) * A.G + rr - t * A.G];
         }
         const int mine = pair ? n : (n + 1 - s) / 2;       // this stream's blocks
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, m_raw = 0.0f, l = 0.0f;      // m: m_raw scaled
         bool ok = true;
         for (int i = 0; i < mine; ++i) {
             ok = warp_wait(&s_full[s], i & 1, timed_out);
@@ -354,15 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 8; c < 128; c += 2)
                 mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+            const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = raw * scale2;
             if (i == 0) {
                 m = top;
+                m_raw = raw;
             } else {
-                const bool grow = top > m + kGrow;
+                const bool grow = (raw - m_raw) * scale2 > kGrow;
                 if (__any_sync(~0u, grow)) {
                     // every product into O has completed: S was issued after them
                     const float f = grow ? ex2(m - top) : 1.0f;
-                    if (grow) m = top;
+                    if (grow) m = top, m_raw = raw;
                     l *= f;
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) {
@@ -375,8 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const float base = base_of(m);
-            const uint64_t k2 = pack2(scale2, scale2), b2 = pack2(-base, -base);
+            float k = scale2, base = base_of(m);
+            if (far_score(base)) far_scale(m_raw, k, base);
+            const uint64_t k2 = pack2(k, k), b2 = pack2(-base, -base);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
