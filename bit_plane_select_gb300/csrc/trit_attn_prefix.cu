@@ -27,7 +27,7 @@
 // products twice: 992 rows of D = 128 on each of 5 heads against 16000 keys 150 us in all.
 //
 // Measured: 1024 rows of D = 128 on each of 5 heads against 32768 keys, on 80 of 152 SMs,
-// beside the sequences' own keys: 137 us in all, 645 TFLOP/s, most of it here; what bounds
+// beside the sequences' own keys: 139 us in all, 635 TFLOP/s, most of it here; what bounds
 // it is the chain of a stream's block (S, softmax, P V, S).  P goes to the products in
 // quarters of 32 keys (in halves: 151 us).
 #include "trit_attn.cuh"
